@@ -3,13 +3,14 @@
 ``lib()`` is a ctypes handle with every entry point; ``calls()`` is the
 CPython module ``_sggcall`` with the hot entry points (plan upload, shrink,
 expand, qkv, embedding), which take integer arguments and cost far less per
-call than ctypes.
+call than ctypes.  ``spec_calls()`` is the like module ``_sggspec`` with the
+entry points of include/sgg_spec.h.
 """
 
 import ctypes
 import os
 
-from .build import CALLMOD, LIB
+from .build import CALLMOD, LIB, SPECMOD
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _pi32, _pi64 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)
@@ -108,6 +109,23 @@ def calls():
         from . import _sggcall
         _calls = _sggcall
     return _calls
+
+
+_spec = None
+
+
+def spec_calls():
+    """The CPython call module of the speculative decoding entry points.  Raises if it
+    has not been built."""
+    global _spec
+    if _spec is None:
+        if not os.path.exists(SPECMOD):
+            raise ImportError(
+                f"{SPECMOD} is missing: build it with `python segmented_gather_gemm_amd/build.py`")
+        lib()
+        from . import _sggspec
+        _spec = _sggspec
+    return _spec
 
 
 def check(rc):

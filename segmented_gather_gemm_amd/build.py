@@ -1,5 +1,5 @@
 """Compile libsgg_lora.so (host planner + gfx950 HIP kernels) and the CPython
-call module over it, in the package directory."""
+call modules over it, in the package directory."""
 
 import os
 import subprocess
@@ -11,8 +11,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsgg_lora.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 CALLMOD = os.path.join(PKG, "_sggcall" + sysconfig.get_config_var("EXT_SUFFIX"))
-SOURCES = ["plan.cpp", "tiling.cpp", "plan_device.hip", "shrink.hip", "shrink_gemm.hip",
-           "expand.hip", "fused.hip", "moe.hip", "lora_api.hip"]
+SPECMOD = os.path.join(PKG, "_sggspec" + sysconfig.get_config_var("EXT_SUFFIX"))
+SOURCES = ["spec_attention_bf16.hip", "spec_attention_fp16.hip", "plan.cpp", "tiling.cpp",
+           "plan_device.hip", "shrink.hip", "shrink_gemm.hip", "expand.hip", "fused.hip",
+           "moe.hip", "lora_api.hip", "spec_kv.hip", "spec_verify.hip", "spec_api.hip"]
 ARCH = os.environ.get("SGG_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
@@ -39,7 +41,7 @@ def _run(cmd, verbose, what):
 
 
 def build(verbose=False):
-    """Build the shared library and the CPython call module; always
+    """Build the shared library and the CPython call modules; always
     recompiles (one hipcc per source, in parallel, then one link).  Returns
     the library's path."""
     from concurrent.futures import ThreadPoolExecutor
@@ -59,12 +61,13 @@ def build(verbose=False):
          "hipcc link")
     os.replace(tmp, LIB)
     # integer-argument entry points for the hot calls, linked to the library
-    tmp = CALLMOD + ".tmp"
-    _run([os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall",
-          "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-          os.path.join(CSRC, "pycall.c"), "-L", PKG, "-lsgg_lora",
-          "-Wl,-rpath,$ORIGIN", "-o", tmp], verbose, "cc")
-    os.replace(tmp, CALLMOD)
+    for module, source in ((CALLMOD, "pycall.c"), (SPECMOD, "speccall.c")):
+        tmp = module + ".tmp"
+        _run([os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall",
+              "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+              os.path.join(CSRC, source), "-L", PKG, "-lsgg_lora",
+              "-Wl,-rpath,$ORIGIN", "-o", tmp], verbose, "cc")
+        os.replace(tmp, module)
     return LIB
 
 

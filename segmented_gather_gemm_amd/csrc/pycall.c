@@ -7,89 +7,8 @@
  * call, against several microseconds for a ctypes call with twenty-odd
  * arguments, which matters for a decode step of a few tens of microseconds.
  */
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-#include <stdint.h>
-#include <string.h>
-
+#include "pycall_args.h"
 #include "sgg_lora.h"
-
-/* Host buffers exported by the arguments of one call (NumPy arrays passed
- * for host pointers), held until the call returns. */
-#define MAX_HELD 8
-typedef struct {
-  Py_buffer view[MAX_HELD];
-  int n;
-} Held;
-
-static void release(Held* held) {
-  for (int i = 0; i < held->n; ++i) PyBuffer_Release(&held->view[i]);
-  held->n = 0;
-}
-
-/* Convert args[i] by sig[i]: 'p' pointer -- an integer address, None (NULL)
- * or a C-contiguous buffer (its first byte, e.g. a NumPy array's data);
- * 'l' int64; 'i' int32. */
-static int convert(const char* name, const char* sig, PyObject* const* args, Py_ssize_t nargs,
-                   int64_t* out, Held* held) {
-  const Py_ssize_t want = (Py_ssize_t)strlen(sig);
-  held->n = 0;
-  if (nargs != want) {
-    PyErr_Format(PyExc_TypeError, "%s takes %zd arguments (%zd given)", name, want, nargs);
-    return 0;
-  }
-  for (Py_ssize_t k = 0; k < want; ++k) {
-    PyObject* a = args[k];
-    if (sig[k] == 'p') {
-      if (a == Py_None) {
-        out[k] = 0;
-        continue;
-      }
-      if (!PyLong_Check(a) && PyObject_CheckBuffer(a)) {
-        if (held->n == MAX_HELD) {
-          PyErr_Format(PyExc_TypeError, "%s: too many buffer arguments", name);
-          release(held);
-          return 0;
-        }
-        if (PyObject_GetBuffer(a, &held->view[held->n], PyBUF_C_CONTIGUOUS) < 0) {
-          release(held);
-          return 0;
-        }
-        out[k] = (int64_t)(uintptr_t)held->view[held->n].buf;
-        ++held->n;
-        continue;
-      }
-      unsigned long long v;
-      if (PyLong_CheckExact(a)) {
-        v = PyLong_AsUnsignedLongLong(a);
-      } else {  /* integer-like objects (NumPy scalars) */
-        PyObject* idx = PyNumber_Index(a);
-        if (idx == NULL) goto bad;
-        v = PyLong_AsUnsignedLongLong(idx);
-        Py_DECREF(idx);
-      }
-      if (v == (unsigned long long)-1 && PyErr_Occurred()) goto bad;
-      out[k] = (int64_t)v;
-    } else {
-      const long long v = PyLong_AsLongLong(a);
-      if (v == -1 && PyErr_Occurred()) goto bad;
-      if (sig[k] == 'i' && (v < INT32_MIN || v > INT32_MAX)) {
-        PyErr_Format(PyExc_OverflowError, "%s: argument %zd does not fit in int32", name, k);
-        release(held);
-        return 0;
-      }
-      out[k] = (int64_t)v;
-    }
-    continue;
-  bad:
-    PyErr_Clear();
-    PyErr_Format(PyExc_TypeError, "%s: argument %zd must be an integer%s", name, k,
-                 sig[k] == 'p' ? " address, a contiguous buffer or None" : "");
-    release(held);
-    return 0;
-  }
-  return 1;
-}
 
 /* Argument signature of each entry point, in the order of its C parameters:
  * 'p' pointer, 'l' int64_t, 'i' int32_t.  Also exported as the module's
@@ -105,24 +24,6 @@ static int convert(const char* name, const char* sig, PyObject* const* args, Py_
 #define SIG_lora_expand "plplplliipiippipppip"
 #define SIG_lora_qkv "plpplpllliipiippipppiplp"
 #define SIG_lora_a_embedding "pplplliilppippip"
-
-/* One int64 per argument, sized by the signature string; CALL runs the
- * entry point, then releases the held buffers. */
-#define CONVERT(fn)                   \
-  int64_t v[sizeof(SIG_##fn) - 1];    \
-  Held held;                          \
-  if (!convert(#fn, SIG_##fn, args, n, v, &held)) return NULL
-#define RETURN_INT(expr)              \
-  do {                                \
-    const long long rc_ = (expr);     \
-    release(&held);                   \
-    return PyLong_FromLongLong(rc_);  \
-  } while (0)
-
-#define P(k) ((void*)(uintptr_t)v[k])
-#define I32P(k) ((int32_t*)(uintptr_t)v[k])
-#define L(k) (v[k])
-#define I(k) ((int32_t)v[k])
 
 static PyObject* py_lora_plan_max_segments(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   CONVERT(lora_plan_max_segments);
@@ -199,8 +100,6 @@ static PyObject* py_lora_a_embedding(PyObject* self, PyObject* const* args, Py_s
                                           I(6), I(7), L(8), I32P(9), I32P(10), I(11), I32P(12),
                                           I32P(13), I(14), P(15)));
 }
-
-#define ENTRY(fn) {#fn, (PyCFunction)(void (*)(void))py_##fn, METH_FASTCALL, NULL}
 
 static PyMethodDef methods[] = {
     ENTRY(lora_plan_max_segments),

@@ -1,0 +1,117 @@
+// Kernel parameter blocks and host launchers of the speculative decoding step
+// (internal to libsgg_lora; the calls are in include/sgg_spec.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <cstdint>
+
+namespace sgg {
+
+constexpr int kSpecMaxRequests = 4096;  // SPEC_MAX_REQUESTS
+
+// A paged cache with its strides in bytes.
+struct KvView {
+  char* k;
+  char* v;
+  int64_t ks[4];  // layer, page, token, head
+  int64_t vs[4];
+  int64_t num_pages;
+  int32_t layers, page_shift, heads;
+  int32_t row_bytes;  // one head of one token
+};
+
+// The page tables of a batch.
+struct KvRows {
+  int32_t* table;
+  int64_t ld;
+  int32_t max_pages, num_rows;
+  const int32_t* rows;     // cache row of request r (null: r)
+  const int32_t* kv_lens;  // by cache row
+};
+
+struct ResizeParams {
+  KvRows t;
+  int32_t* counts;
+  int32_t* refs;
+  int64_t num_pages;
+  const int32_t* new_lens;
+  int32_t* kv_lens;  // null: lengths are not recorded
+  int32_t* status;
+  int32_t n, page_shift;
+};
+hipError_t launch_kv_resize(const ResizeParams& p, hipStream_t stream);
+
+struct ForkParams {
+  KvRows t;
+  int32_t* counts;
+  int32_t* refs;
+  int32_t* kv_lens;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t* status;
+  int32_t* list;  // [3][n]: source page, destination page, tokens (0: nothing)
+  int64_t num_pages;
+  int32_t n, page_shift;
+};
+hipError_t launch_kv_fork(const ForkParams& p, const KvView& c, hipStream_t stream);
+
+// tokens null: whole pages.
+hipError_t launch_kv_copy(const KvView& c, const int32_t* src, const int32_t* dst,
+                          const int32_t* tokens, int64_t n, hipStream_t stream);
+
+struct WriteParams {
+  const char* k;
+  const char* v;
+  int64_t kt, kh, vt, vh;  // strides in bytes
+  KvRows t;
+  const int32_t* q_indptr;
+  const float* k_scale;  // e4m3 cache only
+  const float* v_scale;
+  int64_t num_tokens;
+  int32_t bs, head_dim;
+};
+// dtype of the new rows; to_e4m3: the cache holds 8-bit values.
+hipError_t launch_kv_write(const WriteParams& p, const KvView& c, int dtype, bool to_e4m3,
+                           hipStream_t stream);
+
+struct CompactParams {
+  KvRows t;
+  const int32_t* path;
+  int64_t ld_path;
+  const int32_t* accept;
+  int32_t* new_lens;
+  int32_t bs, path_width;
+};
+hipError_t launch_kv_compact(const CompactParams& p, const KvView& c, hipStream_t stream);
+
+struct TreeMaskParams {
+  const int32_t* parents;
+  const int32_t* q_indptr;
+  const int32_t* kv_lens;
+  const int32_t* rows;
+  uint64_t* mask;
+  int32_t* positions;
+  int64_t num_tokens;
+  int32_t bs, num_rows, words;
+};
+hipError_t launch_tree_mask(const TreeMaskParams& p, hipStream_t stream);
+
+struct VerifyParams {
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* q_indptr;
+  const float* p;  // target
+  const float* q;  // draft, or null
+  const float* u;
+  const float* u_final;
+  int32_t* path;
+  int32_t* accept;
+  int32_t* next;
+  int64_t num_tokens, ldp, ldq, vocab, ld_path;
+  int32_t bs, path_width;
+  void* workspace;
+};
+int64_t verify_workspace_bytes(int32_t bs, int64_t vocab);
+hipError_t launch_verify(const VerifyParams& p, hipStream_t stream);
+
+}  // namespace sgg
