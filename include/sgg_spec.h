@@ -156,8 +156,9 @@ int spec_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t bs,
  *   max_q_len, max_kv_len (context and drafted tokens together): bounds that
  *   shape the launch; the result does not depend on them, a batch that exceeds
  *   them is only slower.
- *   workspace: spec_attention_workspace_bytes(), 16-byte aligned, contents
- *   irrelevant, not shared by overlapping calls.
+ *   workspace: spec_attention_workspace_bytes(), 16-byte aligned, zero on first
+ *   use (each call leaves its counters at zero), not shared by overlapping calls.
+ *   The same inputs give the same bits on every run.
  */
 int64_t spec_attention_workspace_bytes(int32_t bs, int32_t num_q_heads, int32_t num_kv_heads,
                                        int32_t head_dim, int32_t cache_dtype, int32_t max_q_len,

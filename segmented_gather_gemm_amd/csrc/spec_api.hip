@@ -121,38 +121,48 @@ namespace sgg {
 // The workgroup shape of an attention call and the division of its keys.
 //
 // Rows: the smallest block that holds the query rows of one request and kv
-// head (max_q_len tokens times the group), up to 64 * mf rows with all four
-// waves side by side over the rows; blocks of up to 32 rows leave the other
-// waves to the keys.
+// head (max_q_len tokens times the group).  Up to 16 rows, waves share the rows
+// and take different keys, each loading only its own: one wave a workgroup
+// where there are enough requests and kv heads to fill the GPU that way, else
+// four, which need no join through memory.  Above, the waves lie side by side
+// over the rows and share the keys.
 AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                      int32_t cache_bytes, int32_t max_q_len, int64_t max_kv_len) {
   AttnShape s{};
-  (void)cache_bytes;
   const int64_t rows = static_cast<int64_t>(max_q_len) * (q_heads / kv_heads);
+  int64_t resident;  // workgroups that the GPU holds at once
   s.padded_dim = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
   s.mf = 1;
-  if (rows <= 16 && s.padded_dim <= 128) s.wr = 1;
-  else if (rows <= 32) s.wr = 2;
-  else s.wr = 4;
-  if (rows > 64) s.mf = 2;
-  if (rows > 128 && s.padded_dim < 128) s.mf = 4;
+  if (rows <= 16 && s.padded_dim <= 128) {
+    s.wr = 1;
+    s.nw = static_cast<int64_t>(bs) * kv_heads >= 1024 ? 1 : 4;
+    resident = s.nw == 1 ? 1024 : 256;
+  } else if (rows <= 32) {
+    s.wr = s.nw = 2;
+    resident = 768;
+  } else {
+    s.wr = s.nw = 4;
+    resident = 512;
+    if (rows > 64) s.mf = 2;
+    if (rows > 128 && s.padded_dim < 128) s.mf = 4;
+  }
   s.block_rows = 16 * s.mf * s.wr;
-  s.tile_keys = 32 * (4 / s.wr) * (s.wr == 4 && s.padded_dim <= 128 ? 2 : 1);
-  const int64_t blocks = (rows + s.block_rows - 1) / s.block_rows;
-  s.max_blocks = static_cast<int32_t>(blocks < 1 ? 1 : blocks);
-  s.units = static_cast<int64_t>(bs) * s.max_blocks;
-  s.target = 512;
-  s.min_tiles = 256 / s.tile_keys > 1 ? 256 / s.tile_keys : 1;
-  const int64_t tiles = (max_kv_len + s.tile_keys - 1) / s.tile_keys;
-  const int64_t most = (tiles + s.min_tiles - 1) / s.min_tiles;
-  s.max_chunks = static_cast<int32_t>(most < 1 ? 1 : most < s.target ? most : s.target);
-  // a chunk holds more than (sum of tiles) * kv_heads / target tiles, so the sum
-  // of ceil(tiles / chunk) is below target / kv_heads + units
-  int64_t items = s.units * s.max_chunks;
-  const int64_t cap = s.target / kv_heads + s.units;
-  if (items > cap) items = cap;
-  s.slots = s.max_chunks > 1 ? items : 0;
-  s.grid = items * kv_heads;
+  s.tile_keys = 32 * (s.nw / s.wr) * (cache_bytes == 1 && s.wr == 4 ? 2 : 1);
+  const int64_t blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
+  const int64_t units = bs * blocks;
+  s.min_tiles = 128 / s.tile_keys > 1 ? 128 / s.tile_keys : 1;
+  if (blocks > 1 && units * kv_heads >= 2 * resident) {
+    s.ranges = 0;
+    s.grid = units * kv_heads;
+  } else {
+    const int64_t tiles = (max_kv_len + s.tile_keys - 1) / s.tile_keys;
+    const int64_t most = units * ((tiles + s.min_tiles - 1) / s.min_tiles);
+    int64_t n = resident / kv_heads;
+    if (n > most) n = most;
+    s.ranges = static_cast<int32_t>(n < 1 ? 1 : n);
+    s.grid = static_cast<int64_t>(s.ranges) * kv_heads;
+    if (s.ranges > 1) s.slots = 2 * s.grid;
+  }
   return s;
 }
 
@@ -317,9 +327,9 @@ extern "C" int spec_tree_mask(const int32_t* parents, const int32_t* q_indptr, i
 
 namespace {
 
-int64_t attention_bytes(const sgg::AttnShape& s, int32_t kv_heads) {
-  // per slot and kv head: block_rows rows of padded_dim floats, and of (maximum, sum)
-  return s.slots * kv_heads * s.block_rows * (s.padded_dim * 4 + 8);
+int64_t attention_bytes(const sgg::AttnShape& s) {
+  // the counters; per slot block_rows rows of padded_dim floats and of (maximum, sum)
+  return s.slots ? sgg::kJoinBytes + s.slots * s.block_rows * (s.padded_dim * 4 + 8) : 0;
 }
 
 int check_heads(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
@@ -350,7 +360,7 @@ extern "C" int64_t spec_attention_workspace_bytes(int32_t bs, int32_t num_q_head
       sgg::attn_shape(bs, num_q_heads, num_kv_heads, head_dim, cache_dtype == SPEC_E4M3 ? 1 : 2,
                       max_q_len, max_kv_len);
   sgg::ok();
-  return attention_bytes(s, num_kv_heads);
+  return attention_bytes(s);
 }
 
 extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, void* out,
@@ -388,12 +398,14 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   const sgg::AttnShape s =
       sgg::attn_shape(bs, num_q_heads, cache->num_kv_heads, cache->head_dim, e4m3 ? 1 : 2,
                       max_q_len, max_kv_len);
-  const int64_t need = attention_bytes(s, cache->num_kv_heads);
+  const int64_t need = attention_bytes(s);
   SGG_CHECK(need == 0 || workspace, SGG_ERR_INVALID, "workspace is NULL");
   SGG_CHECK(workspace_bytes >= need, SGG_ERR_CAPACITY,
             "workspace of %" PRId64 " bytes, the call needs %" PRId64, workspace_bytes, need);
   SGG_CHECK(sgg::aligned16(workspace), SGG_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
-  SGG_CHECK(s.grid * 16 <= INT32_MAX, SGG_ERR_UNSUPPORTED,
+  SGG_CHECK(s.slots <= sgg::kJoinSlots, SGG_ERR_UNSUPPORTED,
+            "%d kv heads are above %d", cache->num_kv_heads, sgg::kJoinSlots / 4);
+  SGG_CHECK(s.grid <= INT32_MAX, SGG_ERR_UNSUPPORTED,
             "%d requests of %d tokens are above the grid", bs, max_q_len);
   p.q = static_cast<const char*>(q);
   p.out = static_cast<char*>(out);
@@ -404,23 +416,18 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   p.mask = reinterpret_cast<const uint64_t*>(tree_mask);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
-                                        s.slots * cache->num_kv_heads * s.block_rows *
-                                            s.padded_dim * 4);
+  p.counters = static_cast<int32_t*>(workspace);
+  p.part = static_cast<char*>(workspace) + sgg::kJoinBytes;
   p.num_tokens = num_tokens;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.bs = bs;
   p.words = tree_mask ? mask_words : 0;
   p.head_dim = cache->head_dim;
-  p.q_heads = num_q_heads;
   p.group = num_q_heads / cache->num_kv_heads;
   p.block_rows = s.block_rows;
   p.tile_keys = s.tile_keys;
-  p.target = s.target;
   p.min_tiles = s.min_tiles;
-  p.max_chunks = s.max_chunks;
-  p.max_blocks = s.max_blocks;
+  p.ranges = s.ranges;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   return launch_status(q_dtype == SPEC_BF16 ? sgg::launch_attention_bf16(p, s, e4m3, st)
                                             : sgg::launch_attention_fp16(p, s, e4m3, st),
@@ -463,14 +470,13 @@ extern "C" int spec_verify(const int32_t* tokens, const int32_t* parents, const 
   return launch_status(sgg::launch_verify(p, static_cast<hipStream_t>(stream)), "verify");
 }
 
-// The division of an attention call as the host computes it, for tests:
-// rows and keys of a block, target, min_tiles, max_chunks, max_blocks, slots, grid.
+// The division of an attention call as the host computes it, for tests: rows
+// and keys of a block, min_tiles, ranges, slots, grid.
 extern "C" void sgg_spec_attention_shape(int32_t bs, int32_t q_heads, int32_t kv_heads,
                                          int32_t head_dim, int32_t cache_bytes, int32_t max_q_len,
                                          int64_t max_kv_len, int64_t* out) {
   const sgg::AttnShape s =
       sgg::attn_shape(bs, q_heads, kv_heads, head_dim, cache_bytes, max_q_len, max_kv_len);
-  const int64_t v[8] = {s.block_rows, s.tile_keys, s.target, s.min_tiles, s.max_chunks,
-                        s.max_blocks, s.slots, s.grid};
-  for (int i = 0; i < 8; ++i) out[i] = v[i];
+  const int64_t v[6] = {s.block_rows, s.tile_keys, s.min_tiles, s.ranges, s.slots, s.grid};
+  for (int i = 0; i < 6; ++i) out[i] = v[i];
 }

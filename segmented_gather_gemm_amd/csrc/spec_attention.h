@@ -9,8 +9,13 @@
 
 namespace sgg {
 
-constexpr int kAttnThreads = 256;
-constexpr int kAttnWaves = 4;
+// The chunks of a unit are joined in groups of kJoin, level by level.
+constexpr int kJoin = 8;
+constexpr int kJoinLevels = 4;  // up to 4096 chunks
+// Arrival counters lie in a fixed region at the start of the workspace, so
+// that they never share memory with another call's partial results.
+constexpr int kJoinSlots = 32768;
+constexpr int64_t kJoinBytes = int64_t{4} * kJoinLevels * kJoinSlots;
 
 struct AttnParams {
   const char* q;
@@ -22,21 +27,22 @@ struct AttnParams {
   const uint64_t* mask;    // null: causal among the request's tokens
   const float* k_scale;    // e4m3 cache (null: 1)
   const float* v_scale;
-  float* part_o;           // [slots][heads of kv][block rows][padded head_dim]
-  float2* part_ml;         // [slots][heads of kv][block rows]: maximum, sum
+  int32_t* counters;       // [kJoinLevels][kJoinSlots], zero between calls
+  char* part;              // slots of partial results (attention_kernel)
   int64_t num_tokens;
   float scale_log2;        // scale * log2(e): the softmax runs on powers of two
-  int32_t bs, words, head_dim, q_heads, group;
+  int32_t bs, words, head_dim, group;
   // division of the work (AttnShape)
-  int32_t block_rows, tile_keys, target, min_tiles, max_chunks, max_blocks;
+  int32_t block_rows, tile_keys, min_tiles;
+  int32_t ranges;          // per kv head; 0: each workgroup takes one unit
 };
 
-// Workgroup shape: each of the 4 waves holds 16 * mf query rows; wr waves lie
-// side by side over the rows and 4 / wr over the keys of a tile.
+// Workgroup shape: nw waves of 16 * mf query rows each; wr of them lie side by
+// side over the rows and nw / wr over the keys of a tile, 32 keys a wave.
 struct AttnShape {
-  int32_t mf, wr, block_rows, tile_keys, padded_dim;
-  int32_t target, min_tiles, max_chunks, max_blocks;
-  int64_t units, slots, grid;
+  int32_t mf, wr, nw, block_rows, tile_keys, padded_dim;
+  int32_t min_tiles, ranges;
+  int64_t slots, grid;
 };
 AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                      int32_t cache_bytes, int32_t max_q_len, int64_t max_kv_len);

@@ -1,5 +1,6 @@
-// The attention kernel (one pass over keys and values with a running maximum
-// and sum) and the kernel that joins the chunks of a split row block.
+// The attention kernel: one pass over keys and values with a running maximum
+// and sum; the keys of a long request are cut into chunks for several
+// workgroups, the last of which to arrive joins them.
 //
 // Rows.  The query rows of a request and one kv head are its tokens times the
 // group of query heads that share the head, row = token * group + head, cut
@@ -34,21 +35,16 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 #define SGG_GLOBAL __attribute__((address_space(1)))
 
 // ------------------------------------------------------- division of the work
-
-struct AttnItem {
-  int r, mb, chunk, chunks;  // request, row block, chunk of its keys
-  int slot;                  // first slot of the unit's partial results is slot - chunk * blocks
-  int blocks;                // row blocks of the request
-  int tile0, tile1;
-};
-
-// LDS of attn_find.
-struct AttnFind {
-  double sum[kAttnWaves];
-  unsigned long long scan[kAttnWaves];
-  AttnItem item;
-  int found;
-};
+//
+// A unit is a row block of a request (for one kv head) with the key tiles that
+// it may see.  The tiles of all units, one after another, are cut into N equal
+// ranges per kv head, one a workgroup, whatever the units' lengths: workgroups
+// end together although requests differ.  A range covers the end of one unit,
+// whole units, and the beginning of another; the pieces of a unit are joined
+// through the workspace.  Reading two arrays of bs numbers and one workgroup
+// scan stand in for a plan on the host, so that the call depends on nothing but
+// its inputs and can be captured.  Where there are many times more units than
+// workgroups that fit (chunks of prompts), each workgroup takes one unit.
 
 // Tokens of context in cache row `row`, as it counts beside `tokens` new ones:
 // positions stay below 2^31 - 2^16.
@@ -56,88 +52,107 @@ __device__ __forceinline__ int context_of(const AttnParams& p, int row, int toke
   return min(max(p.t.kv_lens[row], 0), INT32_MAX - (1 << 16) - tokens);
 }
 
-// Item `idx` of the batch, the same division in every workgroup.  Each request
-// has blocks x chunks items: its key tiles are cut into chunks so that the
-// batch has about `target` items over all kv heads, none under min_tiles, and
-// a request that one chunk covers is not split.  Reading two arrays of bs
-// numbers and two workgroup scans stand in for a plan on the host, so that the
-// call depends on nothing but its inputs and can be captured.
-__device__ __forceinline__ bool attn_find(const AttnParams& p, int idx, AttnFind* f) {
+struct AttnRequest {
+  int tokens, context, blocks;
+};
+__device__ __forceinline__ AttnRequest request_of(const AttnParams& p, int r) {
+  const int q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
+  const int row = p.t.rows ? p.t.rows[r] : r;
+  if (q0 < 0 || q1 <= q0 || q1 > p.num_tokens || row < 0 || row >= p.t.num_rows)
+    return {0, 0, 0};
+  const int tokens = q1 - q0;
+  return {tokens, context_of(p, row, tokens),
+          static_cast<int>((static_cast<int64_t>(tokens) * p.group + p.block_rows - 1) /
+                           p.block_rows)};
+}
+// Keys that row block mb of a request may see.
+__device__ __forceinline__ int keys_of(const AttnParams& p, const AttnRequest& q, int mb) {
+  if (p.mask) return q.context + q.tokens;
+  const int64_t last = (static_cast<int64_t>(mb + 1) * p.block_rows - 1) / p.group;
+  return q.context + static_cast<int>(last < q.tokens ? last + 1 : q.tokens);
+}
+__device__ __forceinline__ int tiles_of(const AttnParams& p, const AttnRequest& q, int mb) {
+  return (keys_of(p, q, mb) + p.tile_keys - 1) / p.tile_keys;
+}
+// Tiles of all blocks of a request (units where each workgroup takes one).
+__device__ __forceinline__ int64_t weight_of(const AttnParams& p, int r) {
+  const AttnRequest q = request_of(p, r);
+  if (p.ranges == 0) return q.blocks;
+  if (p.mask || q.blocks <= 1) return static_cast<int64_t>(q.blocks) * tiles_of(p, q, q.blocks - 1);
+  int64_t sum = 0;
+  for (int mb = 0; mb < q.blocks; ++mb) sum += tiles_of(p, q, mb);
+  return sum;
+}
+
+struct AttnUnit {
+  AttnRequest q;
+  int r, mb, tiles;
+  int64_t start;  // its first tile among all (its index where each workgroup takes one)
+};
+template <int NW>
+struct AttnFind {
+  int64_t scan[NW];
+  AttnUnit unit;
+};
+
+// The weights before this thread's requests, and of them (`mine`); returns the total.
+template <int NW>
+__device__ __forceinline__ int64_t attn_scan(const AttnParams& p, AttnFind<NW>* f, int64_t* before,
+                                             int64_t* mine) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int per = (p.bs + kAttnThreads - 1) / kAttnThreads;
-  const int r0 = tid * per, r1 = min(r0 + per, p.bs);
-  auto size = [&](int r, int* blocks) -> int {
-    const int q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
-    const int row = p.t.rows ? p.t.rows[r] : r;
-    *blocks = 0;
-    if (q0 < 0 || q1 <= q0 || q1 > p.num_tokens || row < 0 || row >= p.t.num_rows) return 0;
-    const int kv = context_of(p, row, q1 - q0);
-    *blocks = static_cast<int>((static_cast<int64_t>(q1 - q0) * p.group + p.block_rows - 1) /
-                               p.block_rows);
-    return (kv + q1 - q0 + p.tile_keys - 1) / p.tile_keys;
-  };
-  int blocks1 = 0, tiles1 = 0;  // per == 1: kept from the first pass
-  double work = 0.0;
-#pragma unroll 1
-  for (int r = r0; r < r1; ++r) {
-    tiles1 = size(r, &blocks1);
-    work += static_cast<double>(tiles1) * blocks1;
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) work += __shfl_xor(work, d);
-  if (lane == 0) f->sum[wave] = work;
-  if (tid == 0) f->found = 0;
-  __syncthreads();
-  const double all = (f->sum[0] + f->sum[1]) + (f->sum[2] + f->sum[3]);
-  const int per_chunk = max(static_cast<int>(fmin(all * p.c.heads / p.target, 1e9)) + 1,
-                            p.min_tiles);
-  auto chunks_of = [&](int tiles, int blocks) -> int {
-    // bounds of the launch that the batch exceeds: not split (the slots are bounded by them)
-    const int n = (tiles + per_chunk - 1) / per_chunk;
-    return n <= 1 || n > p.max_chunks || blocks > p.max_blocks ? 1 : n;
-  };
-  unsigned long long mine = 0;  // items, and above them the slots
-#pragma unroll 1
-  for (int r = r0; r < r1; ++r) {
-    int blocks = blocks1;
-    const int tiles = per == 1 ? tiles1 : size(r, &blocks);
-    const int n = chunks_of(tiles, blocks);
-    const unsigned long long items = static_cast<unsigned long long>(n) * blocks;
-    mine += items | (n > 1 ? items << 32 : 0);
-  }
-  unsigned long long x = mine;
+  const int per = (p.bs + NW * kWave - 1) / (NW * kWave);
+  int64_t w = 0;
+  for (int r = tid * per; r < min((tid + 1) * per, p.bs); ++r) w += weight_of(p, r);
+  int64_t x = w;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
-    const unsigned long long y = __shfl_up(x, d);
+    const int64_t y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
   if (lane == kWave - 1) f->scan[wave] = x;
   __syncthreads();
-  x -= mine;
-  for (int w = 0; w < wave; ++w) x += f->scan[w];
-#pragma unroll 1
-  for (int r = r0; r < r1; ++r) {
-    int blocks = blocks1;
-    const int tiles = per == 1 ? tiles1 : size(r, &blocks);
-    const int n = chunks_of(tiles, blocks);
-    const int items = n * blocks, start = static_cast<int>(x & 0xffffffffu);
-    if (idx >= start && idx < start + items) {
-      const int local = idx - start, chunk = local / blocks;
-      f->item.r = r;
-      f->item.mb = local - chunk * blocks;
-      f->item.chunk = chunk;
-      f->item.chunks = n;
-      f->item.blocks = blocks;
-      f->item.slot = static_cast<int>(x >> 32) + local;
-      f->item.tile0 = static_cast<int>(static_cast<int64_t>(tiles) * chunk / n);
-      f->item.tile1 = static_cast<int>(static_cast<int64_t>(tiles) * (chunk + 1) / n);
-      f->found = 1;
+  int64_t total = 0, below = 0;
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    if (k < wave) below += f->scan[k];
+    total += f->scan[k];
+  }
+  *before = below + x - w;
+  *mine = w;
+  return total;
+}
+
+// The unit that holds position `pos` (below the total), in LDS for all.
+template <int NW>
+__device__ __forceinline__ void attn_locate(const AttnParams& p, AttnFind<NW>* f, int64_t before,
+                                            int64_t mine, int64_t pos) {
+  if (pos >= before && pos < before + mine) {
+    const int per = (p.bs + NW * kWave - 1) / (NW * kWave);
+    int64_t at = before;
+    for (int r = threadIdx.x * per;; ++r) {
+      const int64_t w = weight_of(p, r);
+      if (pos >= at + w) {
+        at += w;
+        continue;
+      }
+      const AttnRequest q = request_of(p, r);
+      int mb = 0;
+      if (p.ranges == 0) {
+        mb = static_cast<int>(pos - at);
+        at = pos;
+        mb = q.blocks - 1 - mb;  // the blocks that see most first
+      } else if (p.mask || q.blocks <= 1) {
+        const int tiles = tiles_of(p, q, 0);
+        mb = static_cast<int>((pos - at) / tiles);
+        at += static_cast<int64_t>(mb) * tiles;
+      } else {
+        for (int t; pos >= at + (t = tiles_of(p, q, mb)); ++mb) at += t;
+      }
+      f->unit = {q, r, mb, tiles_of(p, q, mb), at};
+      break;
     }
-    const unsigned long long it = items;
-    x += it | (n > 1 ? it << 32 : 0);
   }
   __syncthreads();
-  return f->found != 0;
 }
 
 // ----------------------------------------------------------------- the kernel
@@ -201,24 +216,32 @@ __device__ __forceinline__ void wait_lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Shape constants of an instance.
-template <bool kE4M3, int DP, int MF, int WR>
+// Shape constants of an instance: NW waves, WR of them over the rows, and a
+// ring of NST stages of keys and values.
+template <bool kE4M3, int DP, int MF, int WR, int NW, int NST>
 struct AttnDims {
-  static constexpr int kWK = kAttnWaves / WR;          // waves over the keys
-  static constexpr int kSteps = WR == 4 && DP <= 128 ? 2 : 1;
+  static constexpr int kWK = NW / WR;                  // waves over the keys
+  static constexpr bool kOwn = WR == 1;                // a wave reads only the keys it loads
+  static constexpr int kSteps = kE4M3 && WR == 4 ? 2 : 1;  // steps of 32 keys a wave and tile
   static constexpr int kKeys = 32 * kWK * kSteps;      // keys of a tile
   static constexpr int kEs = kE4M3 ? 1 : 2;
   static constexpr int kRow = DP * kEs;                // bytes of a key in LDS
   static constexpr int kVecs = kRow / 16;
   static constexpr int kSwz = kVecs < 8 ? kVecs - 1 : 7;
   static constexpr int kPer = kWave / kVecs;           // keys of one load instruction
-  static constexpr int kLoads = kKeys / kAttnWaves / kPer;  // load instructions a wave, K or V
+  static constexpr int kPart = kKeys / NW;             // keys that a wave loads
+  static constexpr int kLoads = (kPart + kPer - 1) / kPer;  // load instructions a wave, K or V
   static constexpr int kTileBytes = kKeys * kRow;
   static constexpr int kRows = 16 * MF * WR;
   static constexpr int kStage = 2 * kTileBytes;
-  static constexpr int kMergeBytes = kAttnWaves * (DP / 16) * MF * kWave * 16;
-  static constexpr int kLds = kWK > 1 && kMergeBytes > 2 * kStage ? kMergeBytes : 2 * kStage;
+  static constexpr int kMergeBytes = kWK > 1 ? NW * (DP / 16) * MF * kWave * 16 : 0;
+  static constexpr int kLds = kMergeBytes > NST * kStage ? kMergeBytes : NST * kStage;
+  // a slot: rows x DP sums, then rows pairs of (maximum, sum)
+  static constexpr int kSlotBytes = kRows * (DP * 4 + 8);
+  static_assert(kPart % kPer == 0 && kPart >= kPer, "a load instruction brings whole keys");
+  static_assert(kPart % (kSwz + 1) == 0, "the swizzle counts from a wave's part");
 };
+constexpr int kPageWindow = 256;  // page ids held in LDS
 
 // In fp16 the exponentials, at most 1, are kept 2^12 times as large, so that
 // those down to 2^-26 of the largest are normal numbers; bf16 has the range.
@@ -250,17 +273,20 @@ __device__ __forceinline__ float widen16(uint32_t bits) {
     return bf16_to_f32(bits);
 }
 
-template <bool kFp16, bool kE4M3, int DP, int MF, int WR>
-__global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnParams p) {
-  using D = AttnDims<kE4M3, DP, MF, WR>;
+template <bool kFp16, bool kE4M3, int DP, int MF, int WR, int NW, int NST>
+__global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
+  using D = AttnDims<kE4M3, DP, MF, WR, NW, NST>;
+  constexpr int kThreads = NW * kWave;
   constexpr int kKS = DP / 32;   // K steps of S^T
   constexpr int kDT = DP / 16;   // 16-column tiles of O^T
   __shared__ __align__(1024) char lds[D::kLds];
-  __shared__ AttnFind find;
-  __shared__ float2 merge_ml[kAttnWaves][MF][16];
+  __shared__ int pages[kPageWindow];
+  __shared__ AttnFind<NW> find;
+  __shared__ float2 merge_ml[D::kWK > 1 ? NW : 1][MF][16];
+  __shared__ int arrived;
 
   const int tid = threadIdx.x, lane = tid % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wave = NW > 1 ? __builtin_amdgcn_readfirstlane(tid / kWave) : 0;
   const int wr = wave % WR, wk = wave / WR;
   const int l16 = lane % 16, g = lane / 16;
   const int heads = p.c.heads;
@@ -286,62 +312,89 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnParams p) {
 #pragma unroll
     for (int d = 0; d < kNV; ++d) {
       const int c = kE4M3 ? d : 2 * d + (l16 >> 1 & 1);
-      va[d] = vr * D::kRow + ((c ^ (vr & D::kSwz)) << 4) + 8 * (l16 & 1);
+      va[d] = D::kTileBytes + vr * D::kRow + ((c ^ (vr & D::kSwz)) << 4) + 8 * (l16 & 1);
     }
   }
 
-  for (int idx = blockIdx.x / heads; attn_find(p, idx, &find); idx += gridDim.x / heads) {
-    const AttnItem it = find.item;
-    const int64_t q0 = p.q_indptr[it.r];
-    const int T = static_cast<int>(p.q_indptr[it.r + 1] - q0);
-    const int crow = p.t.rows ? p.t.rows[it.r] : it.r;
-    const int kv = context_of(p, crow, T);
+  // this workgroup's range of tiles, or of units
+  int64_t before, mine;
+  const int64_t total = attn_scan<NW>(p, &find, &before, &mine);
+  const int64_t range = blockIdx.x / heads, stride = gridDim.x / heads;
+  int64_t ranges = p.ranges;
+  if (ranges) ranges = max(min(ranges, (total + p.min_tiles - 1) / p.min_tiles), int64_t{1});
+  int64_t pos = ranges ? range * total / ranges : range;
+  const int64_t stop = ranges ? min((range + 1) * total / ranges, total) : total;
+  while (pos < stop) {
+    attn_locate<NW>(p, &find, before, mine, pos);
+    const AttnUnit u = find.unit;
+    const int64_t q0 = p.q_indptr[u.r];
+    const int T = u.q.tokens, kv = u.q.context;
+    const int crow = p.t.rows ? p.t.rows[u.r] : u.r;
     const int32_t* table = p.t.table + crow * p.t.ld;
-    const int64_t first_row = static_cast<int64_t>(it.mb) * D::kRows;
-    const int last_token =
-        static_cast<int>(min((first_row + D::kRows - 1) / p.group, static_cast<int64_t>(T) - 1));
-    // keys that this block may see, and its tiles
-    const int end = kv + (p.mask ? T : last_token + 1);
-    const int tile0 = it.tile0;
-    const int tile1 = min(it.tile1, (end + D::kKeys - 1) / D::kKeys);
+    const int64_t first_row = static_cast<int64_t>(u.mb) * D::kRows;
+    const int end = keys_of(p, u.q, u.mb);
+    int tile0 = 0, tile1 = u.tiles, chunk = 0, chunks = 1;
+    int64_t range0 = range;  // the range that holds the unit's first tile
+    if (ranges) {
+      tile0 = static_cast<int>(pos - u.start);
+      tile1 = static_cast<int>(min(static_cast<int64_t>(u.tiles), stop - u.start));
+      // position x lies in range ((x + 1) ranges - 1) / total
+      range0 = ((u.start + 1) * ranges - 1) / total;
+      chunk = static_cast<int>(range - range0);
+      chunks = static_cast<int>(((u.start + u.tiles) * ranges - 1) / total - range0) + 1;
+      pos = u.start + tile1;
+    } else {
+      pos += stride;
+    }
 
-    // loading: instruction i of a wave brings keys wave * kKeys / 4 + i * kPer + lane / kVecs;
-    // LDS takes 16 bytes a lane in lane order, so the swizzle is on the source's side
-    const int key_of = lane / D::kVecs, vec_of = lane % D::kVecs;
+    // Loading: instruction i of a wave brings keys wave * kPart + i * kPer +
+    // lane / kVecs of the tile straight into LDS, which takes 16 bytes a lane
+    // in lane order: the swizzle is on the source's side.  Page ids come from
+    // LDS, so that the wait for a tile is a wait for that tile alone.
+    const int key_of = wave * D::kPart + lane / D::kVecs;
     const int low = (1 << p.c.page_shift) - 1;
     const char* kbase = p.c.k + h * p.c.ks[3];
     const char* vbase = p.c.v + h * p.c.vs[3];
     const uint32_t kps = static_cast<uint32_t>(p.c.ks[1]), kts = static_cast<uint32_t>(p.c.ks[2]);
     const uint32_t vps = static_cast<uint32_t>(p.c.vs[1]), vts = static_cast<uint32_t>(p.c.vs[2]);
-    const int last_page = static_cast<int>(p.c.num_pages) - 1;
-    // the page of key lane % (kKeys / 4) of this wave's part of a tile
-    auto page_of = [&](int tile) -> int {
-      const int key = min(tile * D::kKeys + wave * (D::kKeys / 4) + lane % (D::kKeys / 4), end - 1);
-      return table[min(key >> p.c.page_shift, p.t.max_pages - 1)];
-    };
-    auto load_tile = [&](int tile, int page, int stage) {
-      char* kd = lds + stage * D::kStage + wave * (D::kTileBytes / 4);
-      char* vd = kd + D::kTileBytes;
-      page = min(max(page, 0), last_page);
+    int slot0 = 0;  // first page slot of the window
+    // A lane's piece of a key is the same every kNL instructions.  Lanes past
+    // the end of a short head read zeros.
+    constexpr int kNL = (D::kSwz + 1) / D::kPer > 1 ? (D::kSwz + 1) / D::kPer : 1;
+    const char *kl[kNL], *vl[kNL];
+    uint32_t kpl[kNL], ktl[kNL], vpl[kNL], vtl[kNL];
+#pragma unroll
+    for (int i = 0; i < kNL; ++i) {
+      const int vec = (lane % D::kVecs) ^ ((lane / D::kVecs + i * D::kPer) & D::kSwz);
+      const bool in = vec < vecs;
+      kl[i] = in ? kbase + 16 * vec : reinterpret_cast<const char*>(&kZeroVec);
+      vl[i] = in ? vbase + 16 * vec : reinterpret_cast<const char*>(&kZeroVec);
+      kpl[i] = in ? kps : 0u, ktl[i] = in ? kts : 0u;
+      vpl[i] = in ? vps : 0u, vtl[i] = in ? vts : 0u;
+    }
+    auto load_tile = [&](int tile, int stage) {
+      char* kd = lds + stage * D::kStage + wave * (D::kPart * D::kRow);
 #pragma unroll
       for (int i = 0; i < D::kLoads; ++i) {
-        const int kr = i * D::kPer + key_of;  // within the wave's part
-        const int key = min(tile * D::kKeys + wave * (D::kKeys / 4) + kr, end - 1);
-        const uint32_t pg = static_cast<uint32_t>(__shfl(page, kr));
+        const int key = min(tile * D::kKeys + key_of + i * D::kPer, end - 1), x = i % kNL;
+        const uint32_t pg = static_cast<uint32_t>(pages[(key >> p.c.page_shift) - slot0]);
         const uint32_t off = static_cast<uint32_t>(key & low);
-        const int vec = vec_of ^ (kr & D::kSwz);
-        const char* ks = kbase + static_cast<uint64_t>(pg) * kps + static_cast<uint64_t>(off) * kts;
-        const char* vs = vbase + static_cast<uint64_t>(pg) * vps + static_cast<uint64_t>(off) * vts;
-        const char* zero = reinterpret_cast<const char*>(&kZeroVec);
-        ks = vec < vecs ? ks + 16 * vec : zero;
-        vs = vec < vecs ? vs + 16 * vec : zero;
+        const char* ks = kl[x] + static_cast<uint64_t>(pg) * kpl[x] +
+                         static_cast<uint64_t>(off) * ktl[x];
+        const char* vs = vl[x] + static_cast<uint64_t>(pg) * vpl[x] +
+                         static_cast<uint64_t>(off) * vtl[x];
         __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)ks,
                                          (SGG_LDS void*)(kd + i * 1024), 16, 0, 0);
         __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)vs,
-                                         (SGG_LDS void*)(vd + i * 1024), 16, 0, 0);
+                                         (SGG_LDS void*)(kd + D::kTileBytes + i * 1024), 16, 0, 0);
       }
     };
-    int page = page_of(tile0 < tile1 ? tile0 : 0);
+    // wait until at most n tiles of this wave's loads are under way
+    auto wait_tiles = [&](int n) {
+      if (n <= 0) wait_vm<0>();
+      else if (n == 1) wait_vm<2 * D::kLoads>();
+      else wait_vm<NST >= 3 ? 4 * D::kLoads : 0>();
+    };
 
     // query rows of this lane: row l16 of each 16-row fragment
     int tok[MF], qh[MF];
@@ -393,165 +446,180 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnParams p) {
     }
     const float sc = p.scale_log2 * (kE4M3 && p.k_scale ? p.k_scale[h] : 1.0f);
 
-    if (tile0 < tile1) {
-      load_tile(tile0, page, 0);
-      page = page_of(min(tile0 + 1, tile1 - 1));
-    }
-#pragma unroll 1
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const int stage = (tile - tile0) & 1;
-      if (tile + 1 < tile1) {
-        const int after = page_of(min(tile + 2, tile1 - 1));
-        load_tile(tile + 1, page, stage ^ 1);
-        page = after;
-        wait_vm<2 * D::kLoads>();
-      } else {
-        wait_vm<0>();
+    // windows of page ids: one, unless the chunk has more pages than the window
+    for (int w0 = tile0; w0 < tile1;) {
+      slot0 = (w0 * D::kKeys) >> p.c.page_shift;
+      // tiles whose last key lies in the window (a tile's keys take up to kKeys slots of it)
+      const int64_t keys = static_cast<int64_t>(slot0 + kPageWindow) << p.c.page_shift;
+      const int w1 = static_cast<int>(min(static_cast<int64_t>(tile1), keys / D::kKeys));
+      const int slots = ((min(w1 * D::kKeys, end) - 1) >> p.c.page_shift) - slot0 + 1;
+      if (w0 > tile0) __syncthreads();  // the last window's ids have been read
+      for (int e = tid; e < slots; e += kThreads) {
+        const int page = table[min(slot0 + e, p.t.max_pages - 1)];
+        pages[e] = min(max(page, 0), static_cast<int>(p.c.num_pages) - 1);
       }
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      const char* kt = lds + stage * D::kStage;
-      const char* vt = kt + D::kTileBytes;
+      __syncthreads();
 #pragma unroll
-      for (int step = 0; step < D::kSteps; ++step) {
-        constexpr int kStepBytes = 32 * D::kWK * D::kRow;
-        const int key0 = tile * D::kKeys + (step * D::kWK + wk) * 32;
-        const char* ks = kt + step * kStepBytes;
-        const char* vs = vt + step * kStepBytes;
-        // S^T of two 16-key tiles
-        f32x4 st[MF][2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          u32x4_t kf[kKS];
-#pragma unroll
-          for (int s = 0; s < kKS; ++s) {
-            const char* at = ks + ka[s % kNK] + 128 * (s / kNK) + 16 * t * D::kRow;
-            if constexpr (!kE4M3) {
-              kf[s] = *reinterpret_cast<const u32x4_t*>(at);
-            } else {
-              const i32x2_t w = *reinterpret_cast<const i32x2_t*>(at);
-              uint32_t x0, x1, x2, x3;
-              widen4<kFp16>(w[0], &x0, &x1);
-              widen4<kFp16>(w[1], &x2, &x3);
-              kf[s] = u32x4_t{x0, x1, x2, x3};
-            }
-          }
-#pragma unroll
-          for (int m = 0; m < MF; ++m) {
-            f32x4 a = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < kKS; ++s) a = attn_mfma<kFp16>(kf[s], qf[m][s], a);
-            st[m][t] = a;
-          }
+      for (int k = 0; k < NST - 1; ++k)
+        if (w0 + k < w1) load_tile(w0 + k, k);
+      int stage = 0;
+#pragma unroll 1
+      for (int tile = w0; tile < w1; ++tile) {
+        // the stage to be filled next is the one that the last turn has read
+        const int ahead = tile + NST - 1, fill = stage == 0 ? NST - 1 : stage - 1;
+        if constexpr (D::kOwn) {
+          if (ahead < w1) load_tile(ahead, fill);
+          wait_tiles(min(w1 - 1 - tile, NST - 1));
+          asm volatile("" ::: "memory");
+        } else {
+          wait_tiles(min(w1 - 1 - tile, NST - 2));
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          if (ahead < w1) load_tile(ahead, fill);
         }
-        // scores, and what the row does not see
-        const bool open = key0 + 32 <= kv;  // the whole step is context
-        uint32_t seen[MF][2];
+        const char* at_stage = lds + stage * D::kStage;
+        stage = stage + 1 == NST ? 0 : stage + 1;
 #pragma unroll
-        for (int m = 0; m < MF; ++m)
+        for (int step = 0; step < D::kSteps; ++step) {
+          const char* base = at_stage + step * (32 * D::kWK * D::kRow);
+          const int key0 = tile * D::kKeys + (step * D::kWK + wk) * 32;
+          // S^T of two 16-key tiles
+          f32x4 st[MF][2];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            seen[m][t] = 15u;
+            u32x4_t kf[kKS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st[m][t][i] *= sc;
+            for (int s = 0; s < kKS; ++s) {
+              const char* at = base + ka[s % kNK] + 128 * (s / kNK) + 16 * t * D::kRow;
+              if constexpr (!kE4M3) {
+                kf[s] = *reinterpret_cast<const u32x4_t*>(at);
+              } else {
+                const i32x2_t w = *reinterpret_cast<const i32x2_t*>(at);
+                uint32_t x0, x1, x2, x3;
+                widen4<kFp16>(w[0], &x0, &x1);
+                widen4<kFp16>(w[1], &x2, &x3);
+                kf[s] = u32x4_t{x0, x1, x2, x3};
+              }
+            }
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+              f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+              for (int s = 0; s < kKS; ++s) a = attn_mfma<kFp16>(kf[s], qf[m][s], a);
+              st[m][t] = a;
+            }
           }
-        if (!open) {
+          // scores, and what the row does not see
+          const bool open = key0 + 32 <= kv;  // the whole step is context
+          uint32_t seen[MF][2];
 #pragma unroll
           for (int m = 0; m < MF; ++m)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              seen[m][t] = seen4(m, key0 + 16 * t + 4 * g - kv);
+              seen[m][t] = 15u;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (!(seen[m][t] >> i & 1)) st[m][t][i] = -INFINITY;
+              for (int i = 0; i < 4; ++i) st[m][t][i] *= sc;
             }
-        }
-        u32x4_t pf[MF];
+          if (!open) {
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-          float top = fmaxf(fmaxf(fmaxf(st[m][0][0], st[m][0][1]), fmaxf(st[m][0][2], st[m][0][3])),
-                            fmaxf(fmaxf(st[m][1][0], st[m][1][1]), fmaxf(st[m][1][2], st[m][1][3])));
-          top = fmaxf(row_max(top), mx[m]);
-          if (__ballot(top > mx[m])) {  // a row's maximum has grown
-            const float alpha = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - top);
-            sum[m] *= alpha;
+            for (int m = 0; m < MF; ++m)
 #pragma unroll
-            for (int d = 0; d < kDT; ++d)
+              for (int t = 0; t < 2; ++t) {
+                seen[m][t] = seen4(m, key0 + 16 * t + 4 * g - kv);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[m][d][i] *= alpha;
-            mx[m] = top;
+                for (int i = 0; i < 4; ++i)
+                  if (!(seen[m][t] >> i & 1)) st[m][t][i] = -INFINITY;
+              }
           }
-          const float ref = (mx[m] == -INFINITY ? 0.0f : mx[m]) - kPShift<kFp16>;
+          u32x4_t pf[MF];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int m = 0; m < MF; ++m) {
+            float top =
+                fmaxf(fmaxf(fmaxf(st[m][0][0], st[m][0][1]), fmaxf(st[m][0][2], st[m][0][3])),
+                      fmaxf(fmaxf(st[m][1][0], st[m][1][1]), fmaxf(st[m][1][2], st[m][1][3])));
+            top = fmaxf(row_max(top), mx[m]);
+            if (__ballot(top > mx[m])) {  // a row's maximum has grown
+              const float alpha = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - top);
+              sum[m] *= alpha;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              st[m][t][i] = __builtin_amdgcn_exp2f(st[m][t][i] - ref);
-              sum[m] += st[m][t][i];
+              for (int d = 0; d < kDT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][d][i] *= alpha;
+              mx[m] = top;
             }
-          pf[m] = u32x4_t{pack16<kFp16>(st[m][0][0], st[m][0][1]),
-                          pack16<kFp16>(st[m][0][2], st[m][0][3]),
-                          pack16<kFp16>(st[m][1][0], st[m][1][1]),
-                          pack16<kFp16>(st[m][1][2], st[m][1][3])};
-        }
-        // O^T += V^T P^T
-        auto v_fragment = [&](int d) -> u32x4_t {
-          const char* at = vs + va[d % kNV] + 128 * (d / kNV);
-          if constexpr (!kE4M3) {
-            const i32x2_t x = __builtin_bit_cast(
-                i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)at));
-            const i32x2_t y = __builtin_bit_cast(
-                i32x2_t,
-                __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)(at + 16 * D::kRow)));
-            return u32x4_t{static_cast<unsigned>(x[0]), static_cast<unsigned>(x[1]),
-                           static_cast<unsigned>(y[0]), static_cast<unsigned>(y[1])};
+            const float ref = (mx[m] == -INFINITY ? 0.0f : mx[m]) - kPShift<kFp16>;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                st[m][t][i] = __builtin_amdgcn_exp2f(st[m][t][i] - ref);
+                sum[m] += st[m][t][i];
+              }
+            pf[m] = u32x4_t{pack16<kFp16>(st[m][0][0], st[m][0][1]),
+                            pack16<kFp16>(st[m][0][2], st[m][0][3]),
+                            pack16<kFp16>(st[m][1][0], st[m][1][1]),
+                            pack16<kFp16>(st[m][1][2], st[m][1][3])};
+          }
+          // O^T += V^T P^T
+          auto v_fragment = [&](int d) -> u32x4_t {
+            const char* at = base + va[d % kNV] + 128 * (d / kNV);
+            if constexpr (!kE4M3) {
+              const i32x2_t x = __builtin_bit_cast(
+                  i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)at));
+              const i32x2_t y = __builtin_bit_cast(
+                  i32x2_t,
+                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)(at + 16 * D::kRow)));
+              return u32x4_t{static_cast<unsigned>(x[0]), static_cast<unsigned>(x[1]),
+                             static_cast<unsigned>(y[0]), static_cast<unsigned>(y[1])};
+            } else {
+              const i32x2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((SGG_LDS i32x2_t*)at);
+              uint32_t x0, x1, x2, x3;
+              widen4<kFp16>(w[0], &x0, &x1);
+              widen4<kFp16>(w[1], &x2, &x3);
+              return u32x4_t{x0, x1, x2, x3};
+            }
+          };
+          if (open) {
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) {
+              const u32x4_t vf = v_fragment(d);
+#pragma unroll
+              for (int m = 0; m < MF; ++m) o[m][d] = attn_mfma<kFp16>(vf, pf[m], o[m][d]);
+            }
           } else {
-            const i32x2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((SGG_LDS i32x2_t*)at);
-            uint32_t x0, x1, x2, x3;
-            widen4<kFp16>(w[0], &x0, &x1);
-            widen4<kFp16>(w[1], &x2, &x3);
-            return u32x4_t{x0, x1, x2, x3};
-          }
-        };
-        if (open) {
+            // A key hidden from a row has weight 0 there, but 0 times an
+            // infinity or NaN in its value is NaN: such values go through the
+            // product as 0 and are then added to the rows that do see them.
+            bool finite = true;
 #pragma unroll
-          for (int d = 0; d < kDT; ++d) {
-            const u32x4_t vf = v_fragment(d);
+            for (int d = 0; d < kDT; ++d) {
+              u32x4_t vf = v_fragment(d);
 #pragma unroll
-            for (int m = 0; m < MF; ++m) o[m][d] = attn_mfma<kFp16>(vf, pf[m], o[m][d]);
-          }
-        } else {
-          // A key hidden from a row has weight 0 there, but 0 times an infinity
-          // or NaN in its value is NaN: such values go through the product as
-          // 0 and are then added to the rows that do see them.
-          bool finite = true;
+              for (int i = 0; i < 4; ++i) vf[i] = finite_pair<kFp16>(vf[i], &finite);
 #pragma unroll
-          for (int d = 0; d < kDT; ++d) {
-            u32x4_t vf = v_fragment(d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vf[i] = finite_pair<kFp16>(vf[i], &finite);
-#pragma unroll
-            for (int m = 0; m < MF; ++m) o[m][d] = attn_mfma<kFp16>(vf, pf[m], o[m][d]);
-          }
-          if (__ballot(!finite)) {
+              for (int m = 0; m < MF; ++m) o[m][d] = attn_mfma<kFp16>(vf, pf[m], o[m][d]);
+            }
+            if (__ballot(!finite)) {
 #pragma unroll 1
-            for (int e = 0; e < 32; ++e) {  // key e: register e % 4 of tile e / 16, lanes 4 e' ..
-              const int kr = (step * D::kWK + wk) * 32 + e, from = (e / 4 % 4) * 16 + l16;
-#pragma unroll
-              for (int m = 0; m < MF; ++m) {
+              for (int e = 0; e < 32; ++e) {  // key e: register e % 4 of tile e / 16
+                const int kr = wk * 32 + e, from = (e / 4 % 4) * 16 + l16;
+                const char* row = base + D::kTileBytes + kr * D::kRow;
                 const int t = e >> 4, i = e & 3;
-                const f32x4 w4 = t ? st[m][1] : st[m][0];
-                const float w =
-                    __shfl(i == 0 ? w4[0] : i == 1 ? w4[1] : i == 2 ? w4[2] : w4[3], from);
-                const uint32_t sees = __shfl(t ? seen[m][1] : seen[m][0], from) >> i & 1;
+                float w[MF];
+                bool sees[MF];
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                  const f32x4 w4 = t ? st[m][1] : st[m][0];
+                  w[m] = __shfl(i == 0 ? w4[0] : i == 1 ? w4[1] : i == 2 ? w4[2] : w4[3], from);
+                  sees[m] = __shfl(t ? seen[m][1] : seen[m][0], from) >> i & 1;
+                }
 #pragma unroll
                 for (int d = 0; d < kDT; ++d)
 #pragma unroll
                   for (int x = 0; x < 4; ++x) {
                     const int col = 16 * d + 4 * g + x;
-                    const char* at = vt + kr * D::kRow +
-                                     (((col * D::kEs >> 4) ^ (kr & D::kSwz)) << 4) +
-                                     (col * D::kEs & 15);
+                    const char* at =
+                        row + (((col * D::kEs >> 4) ^ (kr & D::kSwz)) << 4) + (col * D::kEs & 15);
                     uint32_t bits;
                     if constexpr (kE4M3) {
                       uint32_t hi;
@@ -560,20 +628,28 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnParams p) {
                     } else {
                       bits = *reinterpret_cast<const uint16_t*>(at);
                     }
-                    if (sees && !finite16<kFp16>(bits)) o[m][d][x] += w * widen16<kFp16>(bits);
+                    if (!finite16<kFp16>(bits)) {
+                      const float v = widen16<kFp16>(bits);
+#pragma unroll
+                      for (int m = 0; m < MF; ++m)
+                        if (sees[m]) o[m][d][x] += w[m] * v;
+                    }
                   }
               }
             }
           }
         }
+        // this wave's reads of the stage have returned
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
-      wait_lds_barrier();  // the stage is free
+      w0 = w1;
     }
 
     // join the waves that shared the rows
 #pragma unroll
     for (int m = 0; m < MF; ++m) sum[m] = row_sum(sum[m]);
     if constexpr (D::kWK > 1) {
+      __syncthreads();  // the last tile has been read
       f32x4* mo = reinterpret_cast<f32x4*>(lds);  // [wave][m][d][lane]
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
@@ -610,12 +686,105 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnParams p) {
       }
     }
 
-    // the result, or this chunk's part of it
-    const float vs = kE4M3 && p.v_scale ? p.v_scale[h] : 1.0f;
+    // Join the chunks of the unit.  Level by level, the items of a group of
+    // kJoin leave their sums in the workspace and count themselves; the last
+    // to arrive reads the group's, in order, and goes on for it.  The sums
+    // move with device-scope accesses, so no cache is written back or dropped.
+    bool last = true;
+    if (chunks > 1) {
+      int c = chunk;
+#pragma unroll 1
+      for (int level = 0, step = 1; step < chunks; ++level, step *= kJoin) {
+        const int n = (chunks + step - 1) / step, group = c / step / kJoin;
+        const int members = min(n - group * kJoin, kJoin);
+        const int first = group * kJoin * step;
+        // a range has two slots: for the unit that it begins in the middle of, and
+        // for the one that it leaves in the middle
+        auto slot_of = [&](int k) -> int64_t {
+          return (2 * (range0 + k) + (k == 0 ? 1 : 0)) * heads + h;
+        };
+        if (members > 1) {
+          char* mine = p.part + slot_of(c) * D::kSlotBytes;
+          const __amdgpu_buffer_rsrc_t out = buffer_rsrc(mine, D::kSlotBytes);
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      if (tok[m] >= T) continue;
-      if (it.chunks == 1) {
+          for (int m = 0; m < MF; ++m) {
+            const int row = (wr * MF + m) * 16 + l16;
+            if (tok[m] >= T) continue;
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) {
+              if (D::kWK > 1 && d % D::kWK != wk) continue;
+              store_coherent16(out, (row * DP + 16 * d + 4 * g) * 4, o[m][d]);
+            }
+            if (wk == 0 && g == 0) {
+              __hip_atomic_store(reinterpret_cast<float*>(mine + D::kRows * DP * 4) + 2 * row,
+                                 mx[m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+              __hip_atomic_store(reinterpret_cast<float*>(mine + D::kRows * DP * 4) + 2 * row + 1,
+                                 sum[m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+          }
+          wave_stores_done();
+          __syncthreads();
+          if (tid == 0) {
+            int32_t* counter = p.counters + level * kJoinSlots + slot_of(first);
+            const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED,
+                                                      __HIP_MEMORY_SCOPE_AGENT);
+            if (before == members - 1)
+              __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            arrived = before;
+          }
+          __syncthreads();
+          last = arrived == members - 1;
+          if (!last) break;
+          float top[MF], total[MF];
+#pragma unroll
+          for (int m = 0; m < MF; ++m) {
+            top[m] = -INFINITY;
+            total[m] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) o[m][d] = f32x4{0, 0, 0, 0};
+          }
+#pragma unroll 2
+          for (int k = 0; k < members; ++k) {
+            const char* from = p.part + slot_of(first + k * step) * D::kSlotBytes;
+            const __amdgpu_buffer_rsrc_t in = buffer_rsrc(from, D::kSlotBytes);
+            const float* ml = reinterpret_cast<const float*>(from + D::kRows * DP * 4);
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+              const int row = (wr * MF + m) * 16 + l16;
+              if (tok[m] >= T) continue;
+              const float a = __hip_atomic_load(ml + 2 * row, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+              const float b = __hip_atomic_load(ml + 2 * row + 1, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+              const float t2 = fmaxf(top[m], a);
+              const float wa = top[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top[m] - t2);
+              const float wb = a == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(a - t2);
+              total[m] = total[m] * wa + b * wb;
+              top[m] = t2;
+#pragma unroll
+              for (int d = 0; d < kDT; ++d) {
+                if (D::kWK > 1 && d % D::kWK != wk) continue;
+                const f32x4 y = load_coherent16(in, (row * DP + 16 * d + 4 * g) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][d][i] = o[m][d][i] * wa + y[i] * wb;
+              }
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < MF; ++m) {
+            mx[m] = top[m];
+            sum[m] = total[m];
+          }
+        }
+        c = first;
+      }
+    }
+
+    if (last) {
+      const float vs = kE4M3 && p.v_scale ? p.v_scale[h] : 1.0f;
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        if (tok[m] >= T) continue;
         const float inv = sum[m] > 0.0f ? vs / sum[m] : sum[m] != sum[m] ? sum[m] : 0.0f;
         char* op = p.out + (q0 + tok[m]) * p.o_token + qh[m] * p.o_head;
 #pragma unroll
@@ -627,108 +796,40 @@ __global__ __launch_bounds__(kAttnThreads) void attention_kernel(AttnParams p) {
           y.y = pack16<kFp16>(o[m][d][2] * inv, o[m][d][3] * inv);
           *reinterpret_cast<uint2*>(op + 2 * d0) = y;
         }
-      } else {
-        const int64_t slot = static_cast<int64_t>(it.slot) * heads + h;
-        const int64_t row = slot * D::kRows + (wr * MF + m) * 16 + l16;
-        if (wk == 0 && g == 0) p.part_ml[row] = make_float2(mx[m], sum[m]);
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          if (D::kWK > 1 && d % D::kWK != wk) continue;
-          *reinterpret_cast<f32x4*>(p.part_o + row * DP + 16 * d + 4 * g) = o[m][d];
-        }
       }
     }
     __syncthreads();  // LDS is free for the next item
   }
 }
 
-// Joins the chunks of split row blocks: a wave per row, each lane 4 columns of
-// every (DP / 256 or less) part.  grid: items of the attention launch as if no
-// request were split, times the kv heads, times parts of 4 rows.
-template <bool kFp16, int DP>
-__global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnParams p, int parts) {
-  __shared__ AttnFind find;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int heads = p.c.heads;
-  const int h = blockIdx.x % heads, part = blockIdx.x / heads % parts;
-  constexpr int kLanes = DP / 4;            // lanes of a row
-  constexpr int kRowsPer = kWave / kLanes;  // rows of a wave: 4, 2 or 1
-  for (int idx = blockIdx.x / heads / parts; attn_find(p, idx, &find);
-       idx += gridDim.x / heads / parts) {
-    const AttnItem it = find.item;
-    if (it.chunks > 1 && it.chunk == 0) {
-      const int64_t q0 = p.q_indptr[it.r];
-      const int T = static_cast<int>(p.q_indptr[it.r + 1] - q0);
-      const float vs = p.v_scale ? p.v_scale[h] : 1.0f;
-      const int col = 4 * (lane % kLanes);
-      for (int b = (part * kAttnWaves + wave) * kRowsPer + lane / kLanes; b < p.block_rows;
-           b += parts * kAttnWaves * kRowsPer) {
-        const int64_t row = static_cast<int64_t>(it.mb) * p.block_rows + b;
-        if (row >= static_cast<int64_t>(T) * p.group) break;
-        const int tok = static_cast<int>(row / p.group);
-        float top = -INFINITY, total = 0.0f;
-        f32x4 a = {0, 0, 0, 0};
-        for (int k = 0; k < it.chunks; ++k) {
-          const int64_t at = (static_cast<int64_t>(it.slot + k * it.blocks) * heads + h) *
-                                 p.block_rows + b;
-          const float2 ml = p.part_ml[at];
-          const f32x4 y = *reinterpret_cast<const f32x4*>(p.part_o + at * DP + col);
-          const float t2 = fmaxf(top, ml.x);
-          const float wa = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - t2);
-          const float wb = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - t2);
-          total = total * wa + ml.y * wb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = a[i] * wa + y[i] * wb;
-          top = t2;
-        }
-        if (col < p.head_dim) {
-          const float inv = total > 0.0f ? vs / total : total != total ? total : 0.0f;
-          char* op = p.out + (q0 + tok) * p.o_token +
-                     (h * p.group + row - static_cast<int64_t>(tok) * p.group) * p.o_head;
-          uint2 y;
-          y.x = pack16<kFp16>(a[0] * inv, a[1] * inv);
-          y.y = pack16<kFp16>(a[2] * inv, a[3] * inv);
-          *reinterpret_cast<uint2*>(op + 2 * col) = y;
-        }
-      }
-    }
-    __syncthreads();
-  }
-}
-
-template <bool kFp16, bool kE4M3, int DP, int MF, int WR>
+template <bool kFp16, bool kE4M3, int DP, int MF, int WR, int NW, int NST>
 hipError_t launch_attention_as(const AttnParams& p, const AttnShape& s, hipStream_t stream) {
-  using D = AttnDims<kE4M3, DP, MF, WR>;
+  using D = AttnDims<kE4M3, DP, MF, WR, NW, NST>;
   if (p.tile_keys != D::kKeys || p.block_rows != D::kRows) return hipErrorInvalidValue;
-  attention_kernel<kFp16, kE4M3, DP, MF, WR>
-      <<<dim3(static_cast<uint32_t>(s.grid)), dim3(kAttnThreads), 0, stream>>>(p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || s.max_chunks <= 1) return e;
-  const int parts = (D::kRows + 15) / 16;
-  const int64_t grid = s.grid * parts;
-  attention_join_kernel<kFp16, DP>
-      <<<dim3(static_cast<uint32_t>(grid)), dim3(kAttnThreads), 0, stream>>>(p, parts);
+  attention_kernel<kFp16, kE4M3, DP, MF, WR, NW, NST>
+      <<<dim3(static_cast<uint32_t>(s.grid)), dim3(NW * kWave), 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <bool kFp16, bool kE4M3>
 hipError_t launch_attention(const AttnParams& p, const AttnShape& s, hipStream_t stream) {
-#define SGG_ATTN(dp, m, w)                             \
-  if (s.padded_dim == dp && s.mf == m && s.wr == w)    \
-    return launch_attention_as<kFp16, kE4M3, dp, m, w>(p, s, stream)
-  SGG_ATTN(64, 1, 1);
-  SGG_ATTN(64, 1, 2);
-  SGG_ATTN(64, 1, 4);
-  SGG_ATTN(64, 2, 4);
-  SGG_ATTN(64, 4, 4);
-  SGG_ATTN(128, 1, 1);
-  SGG_ATTN(128, 1, 2);
-  SGG_ATTN(128, 1, 4);
-  SGG_ATTN(128, 2, 4);
-  SGG_ATTN(128, 4, 4);
-  SGG_ATTN(256, 1, 2);
-  SGG_ATTN(256, 1, 4);
-  SGG_ATTN(256, 2, 4);
+#define SGG_ATTN(dp, m, w, n, st)                                       \
+  if (s.padded_dim == dp && s.mf == m && s.wr == w && s.nw == n)        \
+    return launch_attention_as<kFp16, kE4M3, dp, m, w, n, st>(p, s, stream)
+  SGG_ATTN(64, 1, 1, 1, 3);
+  SGG_ATTN(64, 1, 1, 4, 2);
+  SGG_ATTN(64, 1, 2, 2, 3);
+  SGG_ATTN(64, 1, 4, 4, 4);
+  SGG_ATTN(64, 2, 4, 4, 4);
+  SGG_ATTN(64, 4, 4, 4, 4);
+  SGG_ATTN(128, 1, 1, 1, 2);
+  SGG_ATTN(128, 1, 1, 4, 2);
+  SGG_ATTN(128, 1, 2, 2, 3);
+  SGG_ATTN(128, 1, 4, 4, 3);
+  SGG_ATTN(128, 2, 4, 4, 3);
+  SGG_ATTN(256, 1, 2, 2, 2);
+  SGG_ATTN(256, 1, 4, 4, 2);
+  SGG_ATTN(256, 2, 4, 4, 2);
 #undef SGG_ATTN
   return hipErrorInvalidValue;
 }

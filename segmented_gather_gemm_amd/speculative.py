@@ -22,6 +22,35 @@ _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 _CACHE = struct.Struct("=QQ4q4qq6i")   # SpecKvCache
 
 
+_workspaces = {}
+_outgrown = []
+
+
+def _workspace(t, nbytes):
+    """Scratch of ``nbytes`` for a call on tensor ``t``'s current stream: (address, bytes).
+
+    Zero when it is made; every call leaves its counters at zero.  One grow-only buffer per
+    stream, so calls on different streams never share one; an outgrown buffer is kept, for a
+    kernel under way may still use it.  While a graph is captured the call gets a buffer of its
+    own, cleared in the graph: the graph's memory is not the streams'.
+    """
+    if nbytes <= 0:
+        return 0, 0, None
+    stream = _stream(t)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
+        return ws.data_ptr(), nbytes, ws
+    key = (t.get_device(), stream)
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        size = max(int(nbytes), 1 << 22)
+        if ws is not None:
+            size = max(size, 2 * ws.numel())
+            _outgrown.append(ws)
+        ws = _workspaces[key] = torch.zeros(size, dtype=torch.uint8, device=t.device)
+    return ws.data_ptr(), ws.numel(), ws
+
+
 def _i32(name, t, dev, shape=None):
     """Address of a contiguous int32 tensor on device `dev` (of `shape`, if given)."""
     if t.dtype is not torch.int32:
@@ -250,16 +279,16 @@ def spec_attention(q, k_cache, v_cache, page_table, kv_lens, q_indptr, max_q_len
     calls, code = spec_calls(), _CODES[k_cache.dtype]
     if workspace is None:
         need = calls.spec_attention_workspace_bytes(bs, hq, H, D, code, max_q_len, max_kv_len)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        wp, wn, _held = _workspace(q, need)
+    else:   # the library checks its size
+        wp, wn = workspace.data_ptr(), workspace.numel()
     check(calls.spec_attention(
         qp, qt, qh, op, ot, oh, _CODES[q.dtype], hq, c, t, ld, width, num_rows,
         _i32("kv_lens", kv_lens, dev, (num_rows,)), rp, ind, bs, n, mp, words,
         D ** -0.5 if scale is None else scale,
         0 if k_scale is None else _f32("k_scale", k_scale, dev, (H,)),
-        0 if v_scale is None else _f32("v_scale", v_scale, dev, (H,)), max_q_len, max_kv_len,
-        0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(q)))
+        0 if v_scale is None else _f32("v_scale", v_scale, dev, (H,)), max_q_len, max_kv_len, wp, wn,
+        _stream(q)))
     return out
 
 
@@ -285,18 +314,17 @@ def spec_verify(tokens, parents, q_indptr, target_probs, uniforms, final_uniform
     accept, nxt = got[0], got[1]
     calls = spec_calls()
     if workspace is None:
-        need = calls.spec_verify_workspace_bytes(bs, V)
-        if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=target_probs.device)
+        wp, wn, _held = _workspace(target_probs, calls.spec_verify_workspace_bytes(bs, V))
+    else:   # the library checks its size
+        wp, wn = workspace.data_ptr(), workspace.numel()
     check(calls.spec_verify(
         _i32("tokens", tokens, dev, (n,)), _i32("parents", parents, dev, (n,)), ind, bs, n,
         target_probs.data_ptr(), target_probs.stride(0) if n > 1 else V,
         0 if draft_probs is None else draft_probs.data_ptr(),
         0 if draft_probs is None else (draft_probs.stride(0) if n > 1 else V), V,
         _f32("uniforms", uniforms, dev, (n,)), _f32("final_uniforms", final_uniforms, dev, (bs,)),
-        path.data_ptr(), int(max_q_len), int(max_q_len), accept.data_ptr(), nxt.data_ptr(),
-        0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(target_probs)))
+        path.data_ptr(), int(max_q_len), int(max_q_len), accept.data_ptr(), nxt.data_ptr(), wp, wn,
+        _stream(target_probs)))
     return path, accept, nxt
 
 

@@ -188,10 +188,14 @@ def test_empty_batches_are_nothing_to_do():
     assert C.spec_kv_copy_pages(cache(), 0, 0, 0, 0) == 0
 
 
-def test_workspace_covers_the_split():
-    """No more chunks than the launch's bounds allow, whatever the batch: the sum over requests
-    of row blocks times chunks, with the kernel's rule, stays within the workspace's slots."""
+JOIN_BYTES = 4 * 4 * 32768
+
+
+def test_ranges_cover_every_tile_and_fit_the_workspace():
+    """The kernel's division, followed on the host: every tile of every unit belongs to one
+    range, the pieces of a unit are its consecutive chunks, and no two pieces share a slot."""
     rng = np.random.default_rng(3)
+    split = whole = 0
     for _ in range(300):
         bs = int(rng.integers(1, 70))
         hkv = int(rng.integers(1, 20))
@@ -200,28 +204,59 @@ def test_workspace_covers_the_split():
         T = int(rng.choice([1, 3, 16, 61, 300]))
         kv = int(10 ** rng.uniform(0, 5.3))
         need = C.spec_attention_workspace_bytes(bs, hq, hkv, dim, BF16, T, kv)
-        shape = _shape(bs, hq, hkv, dim, T, kv)
-        assert need == shape["slots"] * hkv * shape["rows"] * (dim * 4 + 8)
-        lens = rng.integers(1, kv + 1, bs)
-        ts = np.minimum(rng.integers(1, T + 1, bs), lens)
-        blocks = -(-ts * (hq // hkv) // shape["rows"])
-        tiles = -(-lens // shape["keys"])
-        per = max(int((tiles * blocks).sum() * hkv / shape["target"]) + 1, shape["min_tiles"])
-        n = -(-tiles // per)
-        n[(n > shape["chunks"]) | (blocks > shape["blocks"])] = 1
-        assert (n * blocks)[n > 1].sum() <= shape["slots"]
-        assert (n == -(-tiles // per)).all()      # within its bounds no batch is left unsplit
+        s = _shape(bs, hq, hkv, dim, T, kv)
+        assert need == (s["slots"] > 0) * JOIN_BYTES + s["slots"] * s["rows"] * (
+            -(-dim // 64) * 64 * 4 + 8)
+        assert s["slots"] <= 32768
+        # the batch may exceed the bounds that shaped the launch
+        over = int(rng.integers(1, 3))
+        lens = rng.integers(1, over * kv + 1, bs)
+        ts = rng.integers(0, over * T + 1, bs)
+        blocks = -(-ts * (hq // hkv) // s["rows"])
+        units = [-(-int(n + t) // s["keys"]) for n, t, b in zip(lens, ts, blocks)
+                 for _ in range(b)]
+        total = sum(units)
+        if total == 0:
+            continue
+        if s["ranges"] == 0:
+            assert s["grid"] % hkv == 0 and s["slots"] == 0
+            whole += 1
+            continue
+        N = max(min(s["ranges"], -(-total // s["min_tiles"])), 1)
+        assert s["grid"] == s["ranges"] * hkv
+        used, starts = set(), np.concatenate([[0], np.cumsum(units)])
+        pieces = {}
+        for i in range(N):
+            pos, stop = i * total // N, min((i + 1) * total // N, total)
+            while pos < stop:
+                u = int(np.searchsorted(starts, pos, side="right")) - 1
+                at, n = int(starts[u]), units[u]
+                t0, t1 = pos - at, min(n, stop - at)
+                r0 = ((at + 1) * N - 1) // total
+                chunks = ((at + n) * N - 1) // total - r0 + 1
+                pieces.setdefault(u, []).append((i - r0, chunks, t0, t1))
+                if chunks > 1:
+                    slot = 2 * i + (1 if i == r0 else 0)
+                    assert slot not in used and slot * hkv + hkv - 1 < s["slots"]
+                    used.add(slot)
+                    split += 1
+                pos = at + t1
+        assert len(pieces) == len(units)
+        for u, got in pieces.items():
+            assert [c for c, *_ in got] == list(range(got[0][1])) and len(got) == got[0][1]
+            assert got[0][2] == 0 and got[-1][3] == units[u]
+            assert all(a[3] == b[2] for a, b in zip(got, got[1:]))
+    assert split > 1000 and whole > 10
     assert C.spec_attention_workspace_bytes(1, 30, 8, 128, 0, 1, 100) == -1
 
 
 def _shape(bs, hq, hkv, dim, T, kv):
     """The launch's division, as the host computes it (read through the library)."""
-    out = (ctypes.c_int64 * 8)()
+    out = (ctypes.c_int64 * 6)()
     fn = ctypes.CDLL(_lib.LIB).sgg_spec_attention_shape
     fn.argtypes = [ctypes.c_int32] * 6 + [ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
     fn(bs, hq, hkv, dim, 2, T, kv, out)
-    return dict(zip(("rows", "keys", "target", "min_tiles", "chunks", "blocks", "slots", "grid"),
-                    out))
+    return dict(zip(("rows", "keys", "min_tiles", "ranges", "slots", "grid"), out))
 
 
 # ------------------------------------------------------------ the oracle, by hand
