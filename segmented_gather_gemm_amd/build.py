@@ -12,8 +12,9 @@ LIB = os.path.join(PKG, "libsgg_lora.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 CALLMOD = os.path.join(PKG, "_sggcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SPECMOD = os.path.join(PKG, "_sggspec" + sysconfig.get_config_var("EXT_SUFFIX"))
-SOURCES = ["spec_attention_bf16.hip", "spec_attention_fp16.hip", "plan.cpp", "tiling.cpp",
-           "plan_device.hip", "shrink.hip", "shrink_gemm.hip", "expand.hip", "fused.hip",
+SOURCES = ["spec_attention_bf16_same.hip", "spec_attention_bf16_e4m3.hip",
+           "spec_attention_fp16_same.hip", "spec_attention_fp16_e4m3.hip", "plan.cpp",
+           "tiling.cpp", "plan_device.hip", "shrink.hip", "shrink_gemm.hip", "expand.hip", "fused.hip",
            "moe.hip", "lora_api.hip", "spec_kv.hip", "spec_verify.hip", "spec_api.hip"]
 ARCH = os.environ.get("SGG_OFFLOAD_ARCH", "gfx950")
 

@@ -63,9 +63,11 @@ int check_cache(const SpecKvCache* c, sgg::KvView* v) {
               "cache strides must not be negative");
     SGG_CHECK(v->ks[i] % 16 == 0 && v->vs[i] % 16 == 0, SGG_ERR_UNSUPPORTED,
               "cache strides must be multiples of 16 bytes");
-    // (page, token, head) strides are multiplied in 32 x 32 -> 64 bits
     SGG_CHECK(i == 0 || (v->ks[i] <= UINT32_MAX && v->vs[i] <= UINT32_MAX), SGG_ERR_UNSUPPORTED,
               "cache strides within a layer must be below 4 GiB");
+    SGG_CHECK(i != 2 || ((v->ks[i] << v->page_shift) <= INT32_MAX &&
+                         (v->vs[i] << v->page_shift) <= INT32_MAX),
+              SGG_ERR_UNSUPPORTED, "the tokens of a page must lie within 2 GiB");
   }
   SGG_CHECK(sgg::aligned16(c->k) && sgg::aligned16(c->v), SGG_ERR_UNSUPPORTED,
             "cache k and v must be 16-byte aligned");
@@ -121,36 +123,34 @@ namespace sgg {
 // The workgroup shape of an attention call and the division of its keys.
 //
 // Rows: the smallest block that holds the query rows of one request and kv
-// head (max_q_len tokens times the group).  Up to 16 rows, waves share the rows
-// and take different keys, each loading only its own: one wave a workgroup
-// where there are enough requests and kv heads to fill the GPU that way, else
-// four, which need no join through memory.  Above, the waves lie side by side
-// over the rows and share the keys.
+// head (max_q_len tokens times the group).  Up to 64 rows each wave holds them
+// all and takes keys of its own, so that a key is read from LDS and widened once
+// for all rows and no wave waits for another; one wave a workgroup where there
+// are enough requests and kv heads to fill the GPU that way, else four.  Above,
+// and for heads of over 128 columns, waves lie side by side over the rows too.
 AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                      int32_t cache_bytes, int32_t max_q_len, int64_t max_kv_len) {
   AttnShape s{};
   const int64_t rows = static_cast<int64_t>(max_q_len) * (q_heads / kv_heads);
-  int64_t resident;  // workgroups that the GPU holds at once
+  int64_t resident = 256;  // workgroups that the GPU holds at once
   s.padded_dim = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  s.mf = 1;
-  if (rows <= 16 && s.padded_dim <= 128) {
-    s.wr = 1;
-    s.nw = static_cast<int64_t>(bs) * kv_heads >= 1024 ? 1 : 4;
-    resident = s.nw == 1 ? 1024 : 256;
-  } else if (rows <= 32) {
-    s.wr = s.nw = 2;
-    resident = 768;
+  s.nw = 4;
+  if (s.padded_dim == 256) {
+    s.mf = rows <= 32 ? 1 : 2;
+    s.wr = rows <= 64 ? 2 : 4;
   } else {
-    s.wr = s.nw = 4;
-    resident = 512;
-    if (rows > 64) s.mf = 2;
-    if (rows > 128 && s.padded_dim < 128) s.mf = 4;
+    s.mf = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    s.wr = rows <= 16 * s.mf ? 1 : rows <= 32 * s.mf ? 2 : 4;
+  }
+  if (rows <= 16 && s.padded_dim <= 128 && static_cast<int64_t>(bs) * kv_heads >= 1024) {
+    s.nw = 1;
+    resident = 1024;
   }
   s.block_rows = 16 * s.mf * s.wr;
   s.tile_keys = 32 * (s.nw / s.wr) * (cache_bytes == 1 && s.wr == 4 ? 2 : 1);
   const int64_t blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
   const int64_t units = bs * blocks;
-  s.min_tiles = 128 / s.tile_keys > 1 ? 128 / s.tile_keys : 1;
+  s.min_tiles = 512 / s.tile_keys;
   if (blocks > 1 && units * kv_heads >= 2 * resident) {
     s.ranges = 0;
     s.grid = units * kv_heads;
@@ -405,6 +405,9 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   SGG_CHECK(sgg::aligned16(workspace), SGG_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
   SGG_CHECK(s.slots <= sgg::kJoinSlots, SGG_ERR_UNSUPPORTED,
             "%d kv heads are above %d", cache->num_kv_heads, sgg::kJoinSlots / 4);
+  SGG_CHECK(num_tokens * (num_q_heads / cache->num_kv_heads) < (1 << 30), SGG_ERR_UNSUPPORTED,
+            "%" PRId64 " tokens of %d heads a kv head are 2^30 rows or more", num_tokens,
+            num_q_heads / cache->num_kv_heads);
   SGG_CHECK(s.grid <= INT32_MAX, SGG_ERR_UNSUPPORTED,
             "%d requests of %d tokens are above the grid", bs, max_q_len);
   p.q = static_cast<const char*>(q);
@@ -424,14 +427,14 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   p.words = tree_mask ? mask_words : 0;
   p.head_dim = cache->head_dim;
   p.group = num_q_heads / cache->num_kv_heads;
-  p.block_rows = s.block_rows;
-  p.tile_keys = s.tile_keys;
   p.min_tiles = s.min_tiles;
   p.ranges = s.ranges;
-  const hipStream_t st = static_cast<hipStream_t>(stream);
-  return launch_status(q_dtype == SPEC_BF16 ? sgg::launch_attention_bf16(p, s, e4m3, st)
-                                            : sgg::launch_attention_fp16(p, s, e4m3, st),
-                       "attention");
+  const bool bf16 = q_dtype == SPEC_BF16;
+  const auto launch = e4m3 ? (bf16 ? sgg::launch_attention_bf16_e4m3
+                                   : sgg::launch_attention_fp16_e4m3)
+                           : (bf16 ? sgg::launch_attention_bf16_same
+                                   : sgg::launch_attention_fp16_same);
+  return launch_status(launch(p, s, static_cast<hipStream_t>(stream)), "attention");
 }
 
 extern "C" int64_t spec_verify_workspace_bytes(int32_t bs, int64_t vocab) {

@@ -33,7 +33,7 @@ struct AttnParams {
   float scale_log2;        // scale * log2(e): the softmax runs on powers of two
   int32_t bs, words, head_dim, group;
   // division of the work (AttnShape)
-  int32_t block_rows, tile_keys, min_tiles;
+  int32_t min_tiles;       // tiles of a range at least
   int32_t ranges;          // per kv head; 0: each workgroup takes one unit
 };
 
@@ -47,9 +47,10 @@ struct AttnShape {
 AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                      int32_t cache_bytes, int32_t max_q_len, int64_t max_kv_len);
 
-hipError_t launch_attention_bf16(const AttnParams& p, const AttnShape& s, bool e4m3,
-                                 hipStream_t stream);
-hipError_t launch_attention_fp16(const AttnParams& p, const AttnShape& s, bool e4m3,
-                                 hipStream_t stream);
+// One for each type of queries and cache (spec_attention_*.hip).
+hipError_t launch_attention_bf16_same(const AttnParams& p, const AttnShape& s, hipStream_t stream);
+hipError_t launch_attention_bf16_e4m3(const AttnParams& p, const AttnShape& s, hipStream_t stream);
+hipError_t launch_attention_fp16_same(const AttnParams& p, const AttnShape& s, hipStream_t stream);
+hipError_t launch_attention_fp16_e4m3(const AttnParams& p, const AttnShape& s, hipStream_t stream);
 
 }  // namespace sgg

@@ -1,0 +1,10 @@
+// The attention kernels for bf16 queries and an 8-bit cache.
+#include "spec_attention_tile.h"
+
+namespace sgg {
+
+hipError_t launch_attention_bf16_e4m3(const AttnParams& p, const AttnShape& s, hipStream_t stream) {
+  return launch_attention<false, true>(p, s, stream);
+}
+
+}  // namespace sgg

@@ -37,7 +37,7 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 // ------------------------------------------------------- division of the work
 //
 // A unit is a row block of a request (for one kv head) with the key tiles that
-// it may see.  The tiles of all units, one after another, are cut into N equal
+// it may see.  The tiles of all units, one after another, are cut into equal
 // ranges per kv head, one a workgroup, whatever the units' lengths: workgroups
 // end together although requests differ.  A range covers the end of one unit,
 // whole units, and the beginning of another; the pieces of a unit are joined
@@ -45,6 +45,10 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 // scan stand in for a plan on the host, so that the call depends on nothing but
 // its inputs and can be captured.  Where there are many times more units than
 // workgroups that fit (chunks of prompts), each workgroup takes one unit.
+//
+// Rows of a request, tokens * group, are below 2^30 (checked on the host), and
+// so are a batch's units; the tiles of a batch are counted in 64 bits, and
+// batches of 2^31 tiles or more are divided by units.
 
 // Tokens of context in cache row `row`, as it counts beside `tokens` new ones:
 // positions stay below 2^31 - 2^16.
@@ -53,56 +57,83 @@ __device__ __forceinline__ int context_of(const AttnParams& p, int row, int toke
 }
 
 struct AttnRequest {
-  int tokens, context, blocks;
+  int first, tokens, context, row;  // first token, tokens, context, cache row
 };
 __device__ __forceinline__ AttnRequest request_of(const AttnParams& p, int r) {
   const int q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
   const int row = p.t.rows ? p.t.rows[r] : r;
   if (q0 < 0 || q1 <= q0 || q1 > p.num_tokens || row < 0 || row >= p.t.num_rows)
-    return {0, 0, 0};
-  const int tokens = q1 - q0;
-  return {tokens, context_of(p, row, tokens),
-          static_cast<int>((static_cast<int64_t>(tokens) * p.group + p.block_rows - 1) /
-                           p.block_rows)};
+    return {0, 0, 0, 0};
+  return {q0, q1 - q0, context_of(p, row, q1 - q0), row};
 }
-// Keys that row block mb of a request may see.
-__device__ __forceinline__ int keys_of(const AttnParams& p, const AttnRequest& q, int mb) {
-  if (p.mask) return q.context + q.tokens;
-  const int64_t last = (static_cast<int64_t>(mb + 1) * p.block_rows - 1) / p.group;
-  return q.context + static_cast<int>(last < q.tokens ? last + 1 : q.tokens);
-}
-__device__ __forceinline__ int tiles_of(const AttnParams& p, const AttnRequest& q, int mb) {
-  return (keys_of(p, q, mb) + p.tile_keys - 1) / p.tile_keys;
-}
-// Tiles of all blocks of a request (units where each workgroup takes one).
-__device__ __forceinline__ int64_t weight_of(const AttnParams& p, int r) {
-  const AttnRequest q = request_of(p, r);
-  if (p.ranges == 0) return q.blocks;
-  if (p.mask || q.blocks <= 1) return static_cast<int64_t>(q.blocks) * tiles_of(p, q, q.blocks - 1);
-  int64_t sum = 0;
-  for (int mb = 0; mb < q.blocks; ++mb) sum += tiles_of(p, q, mb);
-  return sum;
-}
+
+// The division for row blocks of R rows and tiles of K keys.
+template <int NW, int R, int K>
+struct AttnWork {
+  const AttnParams& p;
+  bool by_unit;  // positions count units, not tiles
+
+  __device__ __forceinline__ int blocks(const AttnRequest& q) const {
+    return (q.tokens * p.group + R - 1) / R;
+  }
+  // keys that row block mb of a request may see, and their tiles
+  __device__ __forceinline__ int keys(const AttnRequest& q, int mb) const {
+    const int last = static_cast<int>(static_cast<uint32_t>((mb + 1) * R - 1) /
+                                      static_cast<uint32_t>(p.group));
+    return q.context + (p.mask ? q.tokens : min(last + 1, q.tokens));
+  }
+  __device__ __forceinline__ int tiles(const AttnRequest& q, int mb) const {
+    return (keys(q, mb) + K - 1) / K;
+  }
+  __device__ __forceinline__ int64_t weight(const AttnRequest& q) const {
+    const int n = blocks(q);
+    if (by_unit) return n;
+    if (n == 0) return 0;
+    if (p.mask || n == 1) return static_cast<int64_t>(n) * ((q.context + q.tokens + K - 1) / K);
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int mb = 0; mb < n; ++mb) sum += tiles(q, mb);
+    return sum;
+  }
+};
 
 struct AttnUnit {
   AttnRequest q;
-  int r, mb, tiles;
-  int64_t start;  // its first tile among all (its index where each workgroup takes one)
+  int mb, keys, start;  // start: its first position
 };
+// A value that is the same in all lanes, kept in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+__device__ __forceinline__ char* uniform_ptr(char* x) {
+  const uint64_t u = reinterpret_cast<uint64_t>(x);
+  const uint32_t lo = uniform(static_cast<int>(u)), hi = uniform(static_cast<int>(u >> 32));
+  return reinterpret_cast<char*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 template <int NW>
 struct AttnFind {
   int64_t scan[NW];
   AttnUnit unit;
 };
 
-// The weights before this thread's requests, and of them (`mine`); returns the total.
-template <int NW>
-__device__ __forceinline__ int64_t attn_scan(const AttnParams& p, AttnFind<NW>* f, int64_t* before,
-                                             int64_t* mine) {
+// A thread's requests: the weights of all before them, their own, and the first.
+struct AttnShare {
+  int64_t before, mine;
+  AttnRequest first;
+};
+
+// Returns the total weight.
+template <int NW, int R, int K>
+__device__ __forceinline__ int64_t attn_scan(const AttnWork<NW, R, K>& a, AttnFind<NW>* f,
+                                             AttnShare* s) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int per = (p.bs + NW * kWave - 1) / (NW * kWave);
-  int64_t w = 0;
-  for (int r = tid * per; r < min((tid + 1) * per, p.bs); ++r) w += weight_of(p, r);
+  const int bs = a.p.bs, per = (bs + NW * kWave - 1) / (NW * kWave);
+  const int r0 = tid * per, r1 = min(r0 + per, bs);
+  s->first = AttnRequest{0, 0, 0, 0};
+  if (r0 < r1) s->first = request_of(a.p, r0);
+  int64_t w = a.weight(s->first);
+#pragma unroll 1
+  for (int r = r0 + 1; r < r1; ++r) w += a.weight(request_of(a.p, r));
   int64_t x = w;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
@@ -117,42 +148,49 @@ __device__ __forceinline__ int64_t attn_scan(const AttnParams& p, AttnFind<NW>* 
     if (k < wave) below += f->scan[k];
     total += f->scan[k];
   }
-  *before = below + x - w;
-  *mine = w;
-  return total;
+  s->before = below + x - w;
+  s->mine = w;
+  const uint32_t hi = uniform(static_cast<int>(total >> 32));
+  const uint32_t lo = uniform(static_cast<int>(total));
+  return static_cast<int64_t>(hi) << 32 | lo;
 }
 
-// The unit that holds position `pos` (below the total), in LDS for all.
-template <int NW>
-__device__ __forceinline__ void attn_locate(const AttnParams& p, AttnFind<NW>* f, int64_t before,
-                                            int64_t mine, int64_t pos) {
-  if (pos >= before && pos < before + mine) {
-    const int per = (p.bs + NW * kWave - 1) / (NW * kWave);
-    int64_t at = before;
-    for (int r = threadIdx.x * per;; ++r) {
-      const int64_t w = weight_of(p, r);
-      if (pos >= at + w) {
-        at += w;
-        continue;
+// The unit that holds position `pos` (below the total).
+template <int NW, int R, int K>
+__device__ __forceinline__ AttnUnit attn_locate(const AttnWork<NW, R, K>& a, AttnFind<NW>* f,
+                                            const AttnShare& s, int pos) {
+  if (pos >= s.before && pos < s.before + s.mine) {
+    const int per = (a.p.bs + NW * kWave - 1) / (NW * kWave);
+    int at = static_cast<int>(s.before);
+    AttnRequest q = s.first;
+    if (per > 1) {
+#pragma unroll 1
+      for (int r = threadIdx.x * per;;) {
+        const int64_t w = a.weight(q);
+        if (pos < at + w) break;
+        at += static_cast<int>(w);
+        q = request_of(a.p, ++r);
       }
-      const AttnRequest q = request_of(p, r);
-      int mb = 0;
-      if (p.ranges == 0) {
-        mb = static_cast<int>(pos - at);
-        at = pos;
-        mb = q.blocks - 1 - mb;  // the blocks that see most first
-      } else if (p.mask || q.blocks <= 1) {
-        const int tiles = tiles_of(p, q, 0);
-        mb = static_cast<int>((pos - at) / tiles);
-        at += static_cast<int64_t>(mb) * tiles;
-      } else {
-        for (int t; pos >= at + (t = tiles_of(p, q, mb)); ++mb) at += t;
-      }
-      f->unit = {q, r, mb, tiles_of(p, q, mb), at};
-      break;
     }
+    const int n = a.blocks(q);
+    int mb = 0;
+    if (a.by_unit) {
+      mb = n - 1 - (pos - at);  // the blocks that see most first
+      at = pos;
+    } else if (n > 1 && a.p.mask) {
+      const uint32_t tiles = a.tiles(q, 0);
+      mb = static_cast<int>(static_cast<uint32_t>(pos - at) / tiles);
+      at += mb * tiles;
+    } else if (n > 1) {
+#pragma unroll 1
+      for (int t; pos >= at + (t = a.tiles(q, mb)); ++mb) at += t;
+    }
+    f->unit = {q, mb, a.keys(q, mb), at};
   }
   __syncthreads();
+  const AttnUnit u = f->unit;
+  return {{uniform(u.q.first), uniform(u.q.tokens), uniform(u.q.context), uniform(u.q.row)},
+          uniform(u.mb), uniform(u.keys), uniform(u.start)};
 }
 
 // ----------------------------------------------------------------- the kernel
@@ -226,30 +264,42 @@ struct AttnDims {
   static constexpr int kKeys = 32 * kWK * kSteps;      // keys of a tile
   static constexpr int kEs = kE4M3 ? 1 : 2;
   static constexpr int kRow = DP * kEs;                // bytes of a key in LDS
-  static constexpr int kVecs = kRow / 16;
-  static constexpr int kSwz = kVecs < 8 ? kVecs - 1 : 7;
+  static constexpr int kVecs = kRow / 16;              // its 16-byte pieces
   static constexpr int kPer = kWave / kVecs;           // keys of one load instruction
   static constexpr int kPart = kKeys / NW;             // keys that a wave loads
-  static constexpr int kLoads = (kPart + kPer - 1) / kPer;  // load instructions a wave, K or V
+  static constexpr int kLoads = kPart / kPer;          // load instructions a wave, K or V
   static constexpr int kTileBytes = kKeys * kRow;
   static constexpr int kRows = 16 * MF * WR;
   static constexpr int kStage = 2 * kTileBytes;
+  static constexpr int kCols = DP / 16 / kWK;          // 16-column tiles a wave ends up with
   static constexpr int kMergeBytes = kWK > 1 ? NW * (DP / 16) * MF * kWave * 16 : 0;
   static constexpr int kLds = kMergeBytes > NST * kStage ? kMergeBytes : NST * kStage;
   // a slot: rows x DP sums, then rows pairs of (maximum, sum)
   static constexpr int kSlotBytes = kRows * (DP * 4 + 8);
   static_assert(kPart % kPer == 0 && kPart >= kPer, "a load instruction brings whole keys");
-  static_assert(kPart % (kSwz + 1) == 0, "the swizzle counts from a wave's part");
+  static_assert(kCols * kWK * 16 == DP, "the waves share the columns evenly");
+  // a wave's loads under way are counted in 6 bits; room for the 15 of its queries
+  static_assert((kOwn ? NST : NST - 1) * 2 * kLoads <= 48, "too many loads under way");
 };
-constexpr int kPageWindow = 256;  // page ids held in LDS
+constexpr int kPageWindow = 256;  // pages whose addresses are held in LDS
+
+// Where piece c of key r lies in LDS: at piece c ^ swizzle(r) of the key's row.
+// A fragment of K takes one piece of 8 neighbouring keys at a time, a
+// transposing read of V two neighbouring pieces of 8 keys (16-bit) or one piece
+// of keys 0 - 7 and 16 - 23 (8-bit); with these the 16-byte accesses of each
+// such group fall into different banks (64 of 4 bytes).
+template <int kVecs, bool kE4M3>
+__device__ __forceinline__ int swizzle(int r) {
+  const int x = kVecs >= 16 ? 2 * (r & 7) : kVecs == 8 ? (r & 6) : (r >> 1) & 2;
+  return kE4M3 ? x | (r >> 4 & 1) : x;
+}
+template <int kVecs>
+constexpr int kSwizzled = kVecs < 16 ? kVecs : 16;  // pieces among which it permutes
 
 // In fp16 the exponentials, at most 1, are kept 2^12 times as large, so that
 // those down to 2^-26 of the largest are normal numbers; bf16 has the range.
 template <bool kFp16>
 constexpr float kPShift = kFp16 ? 12.0f : 0.0f;
-
-// Sixteen zero bytes: the source of the padding of a head shorter than DP.
-__device__ __constant__ const uint4 kZeroVec = {0, 0, 0, 0};
 
 // Whether a 16-bit value of a packed pair is an infinity or NaN (bits of its exponent).
 template <bool kFp16>
@@ -273,38 +323,49 @@ __device__ __forceinline__ float widen16(uint32_t bits) {
     return bf16_to_f32(bits);
 }
 
+// Waves that a SIMD holds: two where the registers allow it; four row fragments
+// (or two of 256 columns) take the registers of one.
+template <int DP, int MF>
+constexpr int kAttnWavesPerSimd = DP * MF > 256 ? 1 : 2;
+
 template <bool kFp16, bool kE4M3, int DP, int MF, int WR, int NW, int NST>
-__global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
+__global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attention_kernel(
+    AttnParams p) {
   using D = AttnDims<kE4M3, DP, MF, WR, NW, NST>;
   constexpr int kThreads = NW * kWave;
   constexpr int kKS = DP / 32;   // K steps of S^T
   constexpr int kDT = DP / 16;   // 16-column tiles of O^T
   __shared__ __align__(1024) char lds[D::kLds];
-  __shared__ int pages[kPageWindow];
+  __shared__ ulonglong2 pages[kPageWindow];  // addresses of this head's keys and values
   __shared__ AttnFind<NW> find;
   __shared__ float2 merge_ml[D::kWK > 1 ? NW : 1][MF][16];
-  __shared__ int arrived;
+  __shared__ int arrived, patch;
+  __shared__ uint8_t seen_of[NW][MF * 2][kWave];
 
   const int tid = threadIdx.x, lane = tid % kWave;
-  const int wave = NW > 1 ? __builtin_amdgcn_readfirstlane(tid / kWave) : 0;
+  const int wave = NW > 1 ? uniform(tid / kWave) : 0;
   const int wr = wave % WR, wk = wave / WR;
   const int l16 = lane % 16, g = lane / 16;
   const int heads = p.c.heads;
-  const int h = blockIdx.x % heads;
+  const int h = uniform(blockIdx.x % heads);
   const int vecs = p.c.row_bytes / 16;  // 16-byte pieces of a key that exist
 
-  // Fragment addresses in a tile.  The 16-byte piece c of key r lies at piece
-  // c ^ (r & kSwz) of its row, so the pieces of a fragment repeat every kNK
-  // (kNV) steps, 128 bytes further on.
+  // Fragment addresses in a tile: the pieces of a fragment repeat every kNK
+  // (kNV) steps, kSpan bytes further on; the second 16 keys of a step of K lie
+  // 16 rows on, swizzled on their own in the 8-bit type.
   constexpr int kPK = kE4M3 ? 2 : 4, kPV = kE4M3 ? 1 : 2;  // pieces of a step
-  constexpr int kNK = (D::kSwz + 1) / kPK, kNV = (D::kSwz + 1) / kPV;
-  int ka[kNK], va[kNV];
+  constexpr int kNK = kSwizzled<D::kVecs> / kPK, kNV = kSwizzled<D::kVecs> / kPV;
+  constexpr int kSpan = 16 * kSwizzled<D::kVecs>, kNT = kE4M3 ? 2 : 1;
+  int ka[kNT][kNK], va[kNV];
   {
-    const int kr = wk * 32 + l16;
 #pragma unroll
-    for (int s = 0; s < kNK; ++s) {
-      const int c = kE4M3 ? (4 * s + g) >> 1 : 4 * s + g;
-      ka[s] = kr * D::kRow + ((c ^ (kr & D::kSwz)) << 4) + (kE4M3 ? 8 * (g & 1) : 0);
+    for (int t = 0; t < kNT; ++t) {
+      const int kr = wk * 32 + 16 * t + l16, x = swizzle<D::kVecs, kE4M3>(kr);
+#pragma unroll
+      for (int s = 0; s < kNK; ++s) {
+        const int c = kE4M3 ? (4 * s + g) >> 1 : 4 * s + g;
+        ka[t][s] = kr * D::kRow + ((c ^ x) << 4) + (kE4M3 ? 8 * (g & 1) : 0);
+      }
     }
     // lane j of 16 gives the address of 8 bytes of the block to be transposed
     const int r8 = l16 >> 1;
@@ -312,81 +373,94 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
 #pragma unroll
     for (int d = 0; d < kNV; ++d) {
       const int c = kE4M3 ? d : 2 * d + (l16 >> 1 & 1);
-      va[d] = D::kTileBytes + vr * D::kRow + ((c ^ (vr & D::kSwz)) << 4) + 8 * (l16 & 1);
+      va[d] = D::kTileBytes + vr * D::kRow + ((c ^ swizzle<D::kVecs, kE4M3>(vr)) << 4) +
+              8 * (l16 & 1);
     }
   }
+  // Loading: instruction i of a wave brings keys wave * kPart + i * kPer +
+  // lane / kVecs of a tile straight into LDS, which takes 16 bytes a lane in
+  // lane order: the swizzle is on the source's side.
+  const int key_of = wave * D::kPart + lane / D::kVecs;
+  uint32_t piece[D::kLoads];
+#pragma unroll
+  for (int i = 0; i < D::kLoads; ++i)
+    piece[i] = (lane % D::kVecs) ^ swizzle<D::kVecs, kE4M3>(key_of + i * D::kPer);
+  // the maximum is taken of the bare products, so the sign of the scale goes to q
+  const float signed_scale = p.scale_log2 * (kE4M3 && p.k_scale ? p.k_scale[h] : 1.0f);
+  // (a scale of 0 must not make NaN of what is hidden, -inf)
+  const float scale = signed_scale == 0.0f ? 0x1p-126f : fabsf(signed_scale);
+  const uint32_t flip = signed_scale < 0.0f ? 0x80008000u : 0u;
 
-  // this workgroup's range of tiles, or of units
-  int64_t before, mine;
-  const int64_t total = attn_scan<NW>(p, &find, &before, &mine);
-  const int64_t range = blockIdx.x / heads, stride = gridDim.x / heads;
-  int64_t ranges = p.ranges;
-  if (ranges) ranges = max(min(ranges, (total + p.min_tiles - 1) / p.min_tiles), int64_t{1});
-  int64_t pos = ranges ? range * total / ranges : range;
-  const int64_t stop = ranges ? min((range + 1) * total / ranges, total) : total;
+  // this workgroup's range of positions: of per_range tiles, or single units
+  AttnWork<NW, D::kRows, D::kKeys> work{p, p.ranges == 0};
+  AttnShare share;
+  int64_t all = attn_scan(work, &find, &share);
+  if (!work.by_unit && all > INT32_MAX) {
+    work.by_unit = true;
+    __syncthreads();
+    all = attn_scan(work, &find, &share);
+  }
+  const int total = static_cast<int>(all);
+  const uint32_t range = uniform(blockIdx.x / heads), stride = uniform(gridDim.x / heads);
+  // (quotients come from the vector unit: back to scalar registers)
+  const uint32_t per_range = uniform(
+      work.by_unit ? 1u
+                   : max((static_cast<uint32_t>(total) + p.ranges - 1) / p.ranges,
+                         static_cast<uint32_t>(p.min_tiles)));
+  const uint32_t used = uniform((static_cast<uint32_t>(total) + per_range - 1) / per_range);
+  int pos = range < used ? static_cast<int>(range * per_range) : total;
+  const int stop =
+      work.by_unit ? total : pos + min(total - pos, static_cast<int>(per_range));
   while (pos < stop) {
-    attn_locate<NW>(p, &find, before, mine, pos);
-    const AttnUnit u = find.unit;
-    const int64_t q0 = p.q_indptr[u.r];
+    const AttnUnit u = attn_locate(work, &find, share, pos);
+    const int64_t q0 = u.q.first;
     const int T = u.q.tokens, kv = u.q.context;
-    const int crow = p.t.rows ? p.t.rows[u.r] : u.r;
-    const int32_t* table = p.t.table + crow * p.t.ld;
-    const int64_t first_row = static_cast<int64_t>(u.mb) * D::kRows;
-    const int end = keys_of(p, u.q, u.mb);
-    int tile0 = 0, tile1 = u.tiles, chunk = 0, chunks = 1;
-    int64_t range0 = range;  // the range that holds the unit's first tile
-    if (ranges) {
-      tile0 = static_cast<int>(pos - u.start);
-      tile1 = static_cast<int>(min(static_cast<int64_t>(u.tiles), stop - u.start));
-      // position x lies in range ((x + 1) ranges - 1) / total
-      range0 = ((u.start + 1) * ranges - 1) / total;
-      chunk = static_cast<int>(range - range0);
-      chunks = static_cast<int>(((u.start + u.tiles) * ranges - 1) / total - range0) + 1;
-      pos = u.start + tile1;
-    } else {
+    const int32_t* table = p.t.table + u.q.row * p.t.ld;
+    const int first_row = u.mb * D::kRows;
+    const int end = u.keys, tiles = (end + D::kKeys - 1) / D::kKeys;
+    int tile0 = 0, tile1 = tiles, chunk = 0, chunks = 1;
+    uint32_t range0 = range;  // the range that holds the unit's first tile
+    if (work.by_unit) {
       pos += stride;
+    } else {
+      tile0 = pos - u.start;
+      tile1 = min(tiles, stop - u.start);
+      pos = u.start + tile1;
+      if (tile1 - tile0 < tiles) {
+        range0 = uniform(static_cast<uint32_t>(u.start) / per_range);
+        chunk = static_cast<int>(range - range0);
+        chunks = uniform(static_cast<uint32_t>(u.start + tiles - 1) / per_range) - range0 + 1;
+      }
     }
 
-    // Loading: instruction i of a wave brings keys wave * kPart + i * kPer +
-    // lane / kVecs of the tile straight into LDS, which takes 16 bytes a lane
-    // in lane order: the swizzle is on the source's side.  Page ids come from
-    // LDS, so that the wait for a tile is a wait for that tile alone.
-    const int key_of = wave * D::kPart + lane / D::kVecs;
     const int low = (1 << p.c.page_shift) - 1;
-    const char* kbase = p.c.k + h * p.c.ks[3];
-    const char* vbase = p.c.v + h * p.c.vs[3];
-    const uint32_t kps = static_cast<uint32_t>(p.c.ks[1]), kts = static_cast<uint32_t>(p.c.ks[2]);
-    const uint32_t vps = static_cast<uint32_t>(p.c.vs[1]), vts = static_cast<uint32_t>(p.c.vs[2]);
+    const uint32_t kts = static_cast<uint32_t>(p.c.ks[2]), vts = static_cast<uint32_t>(p.c.vs[2]);
     int slot0 = 0;  // first page slot of the window
-    // A lane's piece of a key is the same every kNL instructions.  Lanes past
-    // the end of a short head read zeros.
-    constexpr int kNL = (D::kSwz + 1) / D::kPer > 1 ? (D::kSwz + 1) / D::kPer : 1;
-    const char *kl[kNL], *vl[kNL];
-    uint32_t kpl[kNL], ktl[kNL], vpl[kNL], vtl[kNL];
-#pragma unroll
-    for (int i = 0; i < kNL; ++i) {
-      const int vec = (lane % D::kVecs) ^ ((lane / D::kVecs + i * D::kPer) & D::kSwz);
-      const bool in = vec < vecs;
-      kl[i] = in ? kbase + 16 * vec : reinterpret_cast<const char*>(&kZeroVec);
-      vl[i] = in ? vbase + 16 * vec : reinterpret_cast<const char*>(&kZeroVec);
-      kpl[i] = in ? kps : 0u, ktl[i] = in ? kts : 0u;
-      vpl[i] = in ? vps : 0u, vtl[i] = in ? vts : 0u;
+    if (vecs < D::kVecs) {  // the padding of a short head is never loaded and stays zero
+      for (int e = tid; e < NST * D::kStage / 16; e += kThreads)
+        reinterpret_cast<uint4*>(lds)[e] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
     }
     auto load_tile = [&](int tile, int stage) {
       char* kd = lds + stage * D::kStage + wave * (D::kPart * D::kRow);
+      ulonglong2 page[D::kLoads];
 #pragma unroll
       for (int i = 0; i < D::kLoads; ++i) {
-        const int key = min(tile * D::kKeys + key_of + i * D::kPer, end - 1), x = i % kNL;
-        const uint32_t pg = static_cast<uint32_t>(pages[(key >> p.c.page_shift) - slot0]);
-        const uint32_t off = static_cast<uint32_t>(key & low);
-        const char* ks = kl[x] + static_cast<uint64_t>(pg) * kpl[x] +
-                         static_cast<uint64_t>(off) * ktl[x];
-        const char* vs = vl[x] + static_cast<uint64_t>(pg) * vpl[x] +
-                         static_cast<uint64_t>(off) * vtl[x];
-        __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)ks,
-                                         (SGG_LDS void*)(kd + i * 1024), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)vs,
-                                         (SGG_LDS void*)(kd + D::kTileBytes + i * 1024), 16, 0, 0);
+        const int key = min(tile * D::kKeys + key_of + i * D::kPer, end - 1);
+        page[i] = pages[(key >> p.c.page_shift) - slot0];
+      }
+#pragma unroll
+      for (int i = 0; i < D::kLoads; ++i) {
+        const uint32_t off = min(tile * D::kKeys + key_of + i * D::kPer, end - 1) & low;
+        const uint64_t ks = page[i].x + (off * kts + 16 * piece[i]);
+        const uint64_t vs = page[i].y + (off * vts + 16 * piece[i]);
+        if (piece[i] < static_cast<uint32_t>(vecs)) {
+          __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)ks,
+                                           (SGG_LDS void*)(kd + i * 1024), 16, 0, 0);
+          __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)vs,
+                                           (SGG_LDS void*)(kd + D::kTileBytes + i * 1024), 16, 0,
+                                           0);
+        }
       }
     };
     // wait until at most n tiles of this wave's loads are under way
@@ -396,44 +470,46 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
       else wait_vm<NST >= 3 ? 4 * D::kLoads : 0>();
     };
 
-    // query rows of this lane: row l16 of each 16-row fragment
-    int tok[MF], qh[MF];
-    uint64_t word0[MF];
+    // Row l16 of this lane's fragment m is query head qh of token tok.
+    auto row_of = [&](int m, int* tok, int* qh) {
+      const uint32_t row = first_row + (wr * MF + m) * 16 + l16;
+      *tok = static_cast<int>(row / static_cast<uint32_t>(p.group));
+      *qh = h * p.group + static_cast<int>(row) - *tok * p.group;
+      return *tok < T;
+    };
     u32x4_t qf[MF][kKS];
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-      const int64_t row = first_row + (wr * MF + m) * 16 + l16;
-      tok[m] = static_cast<int>(row / p.group);
-      qh[m] = h * p.group + static_cast<int>(row - static_cast<int64_t>(tok[m]) * p.group);
-      const bool in = tok[m] < T;
-      const char* qp = p.q + (q0 + tok[m]) * p.q_token + qh[m] * p.q_head;
+      int tok, qh;
+      const bool in = row_of(m, &tok, &qh);
+      const char* qp = p.q + (q0 + tok) * p.q_token + qh * p.q_head;
 #pragma unroll
       for (int s = 0; s < kKS; ++s) {
         const int d0 = 32 * s + 8 * g;
         qf[m][s] = in && d0 < p.head_dim ? *reinterpret_cast<const u32x4_t*>(qp + 2 * d0)
                                          : u32x4_t{0, 0, 0, 0};
+        qf[m][s] ^= flip;
       }
-      word0[m] = p.mask && in ? p.mask[(q0 + tok[m]) * p.words] : 0;
     }
-    // which of the drafted keys j0 .. j0 + 3 row m sees, as bits (j0 < 0: context below 0)
-    auto seen4 = [&](int m, int j0) -> uint32_t {
+    // which of the keys j0 .. j0 + 3 past the context token tok sees, as bits (j0 < 0: in it)
+    auto seen4 = [&](int tok, int j0) -> uint32_t {
       if (j0 <= -4) return 15u;
-      if (!p.mask) {
-        const int n = tok[m] - j0 + 1;
-        return n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1u;
-      }
+      const int n = (p.mask ? T : tok + 1) - j0;  // keys that are there, or come no later
+      const uint32_t there = n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1u;
+      if (!p.mask) return there;
+      const uint64_t* words = p.mask + (q0 + min(tok, T - 1)) * p.words;
       uint64_t b;
       if (j0 < 0) {
-        b = word0[m] << -j0 | ((1u << -j0) - 1u);
+        b = words[0] << -j0 | ((1u << -j0) - 1u);
       } else {
-        const uint64_t* words = p.mask + (q0 + min(tok[m], T - 1)) * p.words;
         const int i = j0 >> 6, sh = j0 & 63;
-        b = i >= p.words ? 0 : (i ? words[i] : word0[m]) >> sh;
+        b = i >= p.words ? 0 : words[i] >> sh;
         if (sh > 60 && i + 1 < p.words) b |= words[i + 1] << (64 - sh);
       }
-      const int n = T - j0;  // keys past the last drafted token are not there
-      return static_cast<uint32_t>(b) & (n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1u);
+      return static_cast<uint32_t>(b) & there;
     };
+    bool finite = true;  // no infinity or NaN among the values of the steps past the context
+    if (tid == 0) patch = 0;
 
     f32x4 o[MF][kDT];
     float mx[MF], sum[MF];
@@ -444,38 +520,40 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
 #pragma unroll
       for (int d = 0; d < kDT; ++d) o[m][d] = f32x4{0, 0, 0, 0};
     }
-    const float sc = p.scale_log2 * (kE4M3 && p.k_scale ? p.k_scale[h] : 1.0f);
-
-    // windows of page ids: one, unless the chunk has more pages than the window
+    // windows of pages: one, unless the chunk has more pages than the window
     for (int w0 = tile0; w0 < tile1;) {
       slot0 = (w0 * D::kKeys) >> p.c.page_shift;
       // tiles whose last key lies in the window (a tile's keys take up to kKeys slots of it)
       const int64_t keys = static_cast<int64_t>(slot0 + kPageWindow) << p.c.page_shift;
       const int w1 = static_cast<int>(min(static_cast<int64_t>(tile1), keys / D::kKeys));
       const int slots = ((min(w1 * D::kKeys, end) - 1) >> p.c.page_shift) - slot0 + 1;
-      if (w0 > tile0) __syncthreads();  // the last window's ids have been read
+      if (w0 > tile0) __syncthreads();  // the last window has been read
       for (int e = tid; e < slots; e += kThreads) {
         const int page = table[min(slot0 + e, p.t.max_pages - 1)];
-        pages[e] = min(max(page, 0), static_cast<int>(p.c.num_pages) - 1);
+        const uint64_t at = min(max(page, 0), static_cast<int>(p.c.num_pages) - 1);
+        pages[e].x = reinterpret_cast<uint64_t>(p.c.k) + h * p.c.ks[3] + at * p.c.ks[1];
+        pages[e].y = reinterpret_cast<uint64_t>(p.c.v) + h * p.c.vs[3] + at * p.c.vs[1];
       }
       __syncthreads();
-#pragma unroll
-      for (int k = 0; k < NST - 1; ++k)
-        if (w0 + k < w1) load_tile(w0 + k, k);
-      int stage = 0;
+      // the first NST - 1 turns only fill the ring
+      int stage = 0, fill = 0;
 #pragma unroll 1
-      for (int tile = w0; tile < w1; ++tile) {
-        // the stage to be filled next is the one that the last turn has read
-        const int ahead = tile + NST - 1, fill = stage == 0 ? NST - 1 : stage - 1;
+      for (int tile = w0 - (NST - 1); tile < w1; ++tile) {
+        const int ahead = tile + NST - 1;
+        if constexpr (!D::kOwn) {
+          if (tile >= w0) {
+            wait_tiles(min(w1 - 1 - tile, NST - 2));
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+          }
+        }
+        // into the stage that the last turn has read
+        if (ahead < w1) load_tile(ahead, fill);
+        fill = fill + 1 == NST ? 0 : fill + 1;
+        if (tile < w0) continue;
         if constexpr (D::kOwn) {
-          if (ahead < w1) load_tile(ahead, fill);
           wait_tiles(min(w1 - 1 - tile, NST - 1));
           asm volatile("" ::: "memory");
-        } else {
-          wait_tiles(min(w1 - 1 - tile, NST - 2));
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-          if (ahead < w1) load_tile(ahead, fill);
         }
         const char* at_stage = lds + stage * D::kStage;
         stage = stage + 1 == NST ? 0 : stage + 1;
@@ -490,7 +568,8 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
             u32x4_t kf[kKS];
 #pragma unroll
             for (int s = 0; s < kKS; ++s) {
-              const char* at = base + ka[s % kNK] + 128 * (s / kNK) + 16 * t * D::kRow;
+              const char* at = base + ka[kNT == 2 ? t : 0][s % kNK] + kSpan * (s / kNK) +
+                               (kNT == 2 ? 0 : 16 * t * D::kRow);
               if constexpr (!kE4M3) {
                 kf[s] = *reinterpret_cast<const u32x4_t*>(at);
               } else {
@@ -511,24 +590,21 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
           }
           // scores, and what the row does not see
           const bool open = key0 + 32 <= kv;  // the whole step is context
-          uint32_t seen[MF][2];
-#pragma unroll
-          for (int m = 0; m < MF; ++m)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              seen[m][t] = 15u;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) st[m][t][i] *= sc;
-            }
           if (!open) {
+#pragma unroll 1
+            for (int e = 0; e < 2 * MF; ++e) {
+              int tok, qh;
+              row_of(e >> 1, &tok, &qh);
+              seen_of[wave][e][lane] = seen4(tok, key0 + 16 * (e & 1) + 4 * g - kv);
+            }
 #pragma unroll
             for (int m = 0; m < MF; ++m)
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
-                seen[m][t] = seen4(m, key0 + 16 * t + 4 * g - kv);
+                const uint32_t seen = seen_of[wave][2 * m + t][lane];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (!(seen[m][t] >> i & 1)) st[m][t][i] = -INFINITY;
+                  if (!(seen >> i & 1)) st[m][t][i] = -INFINITY;
               }
           }
           u32x4_t pf[MF];
@@ -539,7 +615,8 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
                       fmaxf(fmaxf(st[m][1][0], st[m][1][1]), fmaxf(st[m][1][2], st[m][1][3])));
             top = fmaxf(row_max(top), mx[m]);
             if (__ballot(top > mx[m])) {  // a row's maximum has grown
-              const float alpha = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - top);
+              const float alpha =
+                  mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx[m] - top) * scale);
               sum[m] *= alpha;
 #pragma unroll
               for (int d = 0; d < kDT; ++d)
@@ -547,12 +624,12 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
                 for (int i = 0; i < 4; ++i) o[m][d][i] *= alpha;
               mx[m] = top;
             }
-            const float ref = (mx[m] == -INFINITY ? 0.0f : mx[m]) - kPShift<kFp16>;
+            const float ref = (mx[m] == -INFINITY ? 0.0f : mx[m] * scale) - kPShift<kFp16>;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                st[m][t][i] = __builtin_amdgcn_exp2f(st[m][t][i] - ref);
+                st[m][t][i] = __builtin_amdgcn_exp2f(fmaf(st[m][t][i], scale, -ref));
                 sum[m] += st[m][t][i];
               }
             pf[m] = u32x4_t{pack16<kFp16>(st[m][0][0], st[m][0][1]),
@@ -562,7 +639,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
           }
           // O^T += V^T P^T
           auto v_fragment = [&](int d) -> u32x4_t {
-            const char* at = base + va[d % kNV] + 128 * (d / kNV);
+            const char* at = base + va[d % kNV] + kSpan * (d / kNV);
             if constexpr (!kE4M3) {
               const i32x2_t x = __builtin_bit_cast(
                   i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)at));
@@ -579,64 +656,26 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
               return u32x4_t{x0, x1, x2, x3};
             }
           };
-          if (open) {
+          // A key hidden from a row has weight 0 there, but 0 times an infinity
+          // or NaN in its value is NaN: past the context, such values go through
+          // the product as 0, and are added to the rows that see them at the end.
+          constexpr int kGroup = kDT < 8 ? kDT : 8;
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) {
-              const u32x4_t vf = v_fragment(d);
+          for (int d0 = 0; d0 < kDT; d0 += kGroup) {
+            u32x4_t vf[kGroup];
 #pragma unroll
-              for (int m = 0; m < MF; ++m) o[m][d] = attn_mfma<kFp16>(vf, pf[m], o[m][d]);
+            for (int d = 0; d < kGroup; ++d) vf[d] = v_fragment(d0 + d);
+            if (!open) {
+#pragma unroll
+              for (int d = 0; d < kGroup; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vf[d][i] = finite_pair<kFp16>(vf[d][i], &finite);
             }
-          } else {
-            // A key hidden from a row has weight 0 there, but 0 times an
-            // infinity or NaN in its value is NaN: such values go through the
-            // product as 0 and are then added to the rows that do see them.
-            bool finite = true;
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) {
-              u32x4_t vf = v_fragment(d);
+            for (int d = 0; d < kGroup; ++d)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) vf[i] = finite_pair<kFp16>(vf[i], &finite);
-#pragma unroll
-              for (int m = 0; m < MF; ++m) o[m][d] = attn_mfma<kFp16>(vf, pf[m], o[m][d]);
-            }
-            if (__ballot(!finite)) {
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) {  // key e: register e % 4 of tile e / 16
-                const int kr = wk * 32 + e, from = (e / 4 % 4) * 16 + l16;
-                const char* row = base + D::kTileBytes + kr * D::kRow;
-                const int t = e >> 4, i = e & 3;
-                float w[MF];
-                bool sees[MF];
-#pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                  const f32x4 w4 = t ? st[m][1] : st[m][0];
-                  w[m] = __shfl(i == 0 ? w4[0] : i == 1 ? w4[1] : i == 2 ? w4[2] : w4[3], from);
-                  sees[m] = __shfl(t ? seen[m][1] : seen[m][0], from) >> i & 1;
-                }
-#pragma unroll
-                for (int d = 0; d < kDT; ++d)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    const int col = 16 * d + 4 * g + x;
-                    const char* at =
-                        row + (((col * D::kEs >> 4) ^ (kr & D::kSwz)) << 4) + (col * D::kEs & 15);
-                    uint32_t bits;
-                    if constexpr (kE4M3) {
-                      uint32_t hi;
-                      widen4<kFp16>(*reinterpret_cast<const uint8_t*>(at), &bits, &hi);
-                      bits &= 0xffffu;
-                    } else {
-                      bits = *reinterpret_cast<const uint16_t*>(at);
-                    }
-                    if (!finite16<kFp16>(bits)) {
-                      const float v = widen16<kFp16>(bits);
-#pragma unroll
-                      for (int m = 0; m < MF; ++m)
-                        if (sees[m]) o[m][d][x] += w[m] * v;
-                    }
-                  }
-              }
-            }
+              for (int m = 0; m < MF; ++m)
+                o[m][d0 + d] = attn_mfma<kFp16>(vf[d], pf[m], o[m][d0 + d]);
           }
         }
         // this wave's reads of the stage have returned
@@ -645,9 +684,15 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
       w0 = w1;
     }
 
-    // join the waves that shared the rows
+    if (!finite) patch = 1;
+    // the waves that shared the rows join theirs: w holds columns col_of(j) of the sums
+    f32x4 w[MF][D::kCols];
+    auto col_of = [&](int j) -> int { return 16 * (D::kWK > 1 ? wk * D::kCols + j : j) + 4 * g; };
 #pragma unroll
-    for (int m = 0; m < MF; ++m) sum[m] = row_sum(sum[m]);
+    for (int m = 0; m < MF; ++m) {
+      sum[m] = row_sum(sum[m]);
+      mx[m] *= scale;  // from here on, in units of powers of two
+    }
     if constexpr (D::kWK > 1) {
       __syncthreads();  // the last tile has been read
       f32x4* mo = reinterpret_cast<f32x4*>(lds);  // [wave][m][d][lane]
@@ -660,30 +705,40 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
       __syncthreads();
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        float top = -INFINITY, w[D::kWK], total = 0.0f;
+        float top = -INFINITY, f[D::kWK], total = 0.0f;
+        float2 ml[D::kWK];
 #pragma unroll
-        for (int k = 0; k < D::kWK; ++k) top = fmaxf(top, merge_ml[k * WR + wr][m][l16].x);
+        for (int k = 0; k < D::kWK; ++k) ml[k] = merge_ml[k * WR + wr][m][l16];
+#pragma unroll
+        for (int k = 0; k < D::kWK; ++k) top = fmaxf(top, ml[k].x);
 #pragma unroll
         for (int k = 0; k < D::kWK; ++k) {
-          const float2 ml = merge_ml[k * WR + wr][m][l16];
-          w[k] = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-          total += ml.y * w[k];
+          f[k] = ml[k].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[k].x - top);
+          total += ml[k].y * f[k];
         }
         mx[m] = top;
         sum[m] = total;
+        f32x4 y[D::kCols][D::kWK];
 #pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          if (d % D::kWK != wk) continue;  // the waves share the columns
+        for (int j = 0; j < D::kCols; ++j)
+#pragma unroll
+          for (int k = 0; k < D::kWK; ++k)
+            y[j][k] = mo[(((k * WR + wr) * MF + m) * kDT + wk * D::kCols + j) * kWave + lane];
+#pragma unroll
+        for (int j = 0; j < D::kCols; ++j) {
           f32x4 a = {0, 0, 0, 0};
 #pragma unroll
-          for (int k = 0; k < D::kWK; ++k) {
-            const f32x4 y = mo[(((k * WR + wr) * MF + m) * kDT + d) * kWave + lane];
+          for (int k = 0; k < D::kWK; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] += w[k] * y[i];
-          }
-          o[m][d] = a;
+            for (int i = 0; i < 4; ++i) a[i] += f[k] * y[j][k][i];
+          w[m][j] = a;
         }
       }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int j = 0; j < D::kCols; ++j) w[m][j] = o[m][j];
     }
 
     // Join the chunks of the unit.  Level by level, the items of a group of
@@ -691,8 +746,10 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
     // to arrive reads the group's, in order, and goes on for it.  The sums
     // move with device-scope accesses, so no cache is written back or dropped.
     bool last = true;
-    if (chunks > 1) {
+    if (__builtin_expect(chunks > 1, 0)) {
       int c = chunk;
+      __syncthreads();
+      bool flag = patch != 0;  // travels in the sign of the sums
 #pragma unroll 1
       for (int level = 0, step = 1; step < chunks; ++level, step *= kJoin) {
         const int n = (chunks + step - 1) / step, group = c / step / kJoin;
@@ -701,25 +758,25 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
         // a range has two slots: for the unit that it begins in the middle of, and
         // for the one that it leaves in the middle
         auto slot_of = [&](int k) -> int64_t {
-          return (2 * (range0 + k) + (k == 0 ? 1 : 0)) * heads + h;
+          return (2 * static_cast<int64_t>(range0 + k) + (k == 0 ? 1 : 0)) * heads + h;
         };
         if (members > 1) {
-          char* mine = p.part + slot_of(c) * D::kSlotBytes;
+          char* mine = uniform_ptr(p.part + slot_of(c) * D::kSlotBytes);
           const __amdgpu_buffer_rsrc_t out = buffer_rsrc(mine, D::kSlotBytes);
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
             const int row = (wr * MF + m) * 16 + l16;
-            if (tok[m] >= T) continue;
+            int tok, qh;
+            if (!row_of(m, &tok, &qh)) continue;
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) {
-              if (D::kWK > 1 && d % D::kWK != wk) continue;
-              store_coherent16(out, (row * DP + 16 * d + 4 * g) * 4, o[m][d]);
-            }
+            for (int j = 0; j < D::kCols; ++j)
+              store_coherent16(out, (row * DP + col_of(j)) * 4, w[m][j]);
             if (wk == 0 && g == 0) {
               __hip_atomic_store(reinterpret_cast<float*>(mine + D::kRows * DP * 4) + 2 * row,
                                  mx[m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
               __hip_atomic_store(reinterpret_cast<float*>(mine + D::kRows * DP * 4) + 2 * row + 1,
-                                 sum[m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                                 flag ? -sum[m] : sum[m], __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
             }
           }
           wave_stores_done();
@@ -733,7 +790,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
             arrived = before;
           }
           __syncthreads();
-          last = arrived == members - 1;
+          last = uniform(arrived) == members - 1;
           if (!last) break;
           float top[MF], total[MF];
 #pragma unroll
@@ -741,17 +798,18 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
             top[m] = -INFINITY;
             total[m] = 0.0f;
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) o[m][d] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < D::kCols; ++j) w[m][j] = f32x4{0, 0, 0, 0};
           }
 #pragma unroll 2
           for (int k = 0; k < members; ++k) {
-            const char* from = p.part + slot_of(first + k * step) * D::kSlotBytes;
+            const char* from = uniform_ptr(p.part + slot_of(first + k * step) * D::kSlotBytes);
             const __amdgpu_buffer_rsrc_t in = buffer_rsrc(from, D::kSlotBytes);
             const float* ml = reinterpret_cast<const float*>(from + D::kRows * DP * 4);
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
               const int row = (wr * MF + m) * 16 + l16;
-              if (tok[m] >= T) continue;
+              int tok, qh;
+              if (!row_of(m, &tok, &qh)) continue;
               const float a = __hip_atomic_load(ml + 2 * row, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT);
               const float b = __hip_atomic_load(ml + 2 * row + 1, __ATOMIC_RELAXED,
@@ -759,14 +817,14 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
               const float t2 = fmaxf(top[m], a);
               const float wa = top[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top[m] - t2);
               const float wb = a == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(a - t2);
-              total[m] = total[m] * wa + b * wb;
+              flag |= signbit(b);
+              total[m] = total[m] * wa + fabsf(b) * wb;
               top[m] = t2;
 #pragma unroll
-              for (int d = 0; d < kDT; ++d) {
-                if (D::kWK > 1 && d % D::kWK != wk) continue;
-                const f32x4 y = load_coherent16(in, (row * DP + 16 * d + 4 * g) * 4);
+              for (int j = 0; j < D::kCols; ++j) {
+                const f32x4 y = load_coherent16(in, (row * DP + col_of(j)) * 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[m][d][i] = o[m][d][i] * wa + y[i] * wb;
+                for (int i = 0; i < 4; ++i) w[m][j][i] = w[m][j][i] * wa + y[i] * wb;
               }
             }
           }
@@ -778,34 +836,60 @@ __global__ __launch_bounds__(NW* kWave, 2) void attention_kernel(AttnParams p) {
         }
         c = first;
       }
+      if (flag) patch = 1;
     }
 
+    const float vs = kE4M3 && p.v_scale ? p.v_scale[h] : 1.0f;
     if (last) {
-      const float vs = kE4M3 && p.v_scale ? p.v_scale[h] : 1.0f;
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        if (tok[m] >= T) continue;
+        int tok, qh;
+        if (!row_of(m, &tok, &qh)) continue;
         const float inv = sum[m] > 0.0f ? vs / sum[m] : sum[m] != sum[m] ? sum[m] : 0.0f;
-        char* op = p.out + (q0 + tok[m]) * p.o_token + qh[m] * p.o_head;
+        char* op = p.out + (q0 + tok) * p.o_token + qh * p.o_head;
 #pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          const int d0 = 16 * d + 4 * g;
-          if ((D::kWK > 1 && d % D::kWK != wk) || d0 >= p.head_dim) continue;
+        for (int j = 0; j < D::kCols; ++j) {
+          const int d0 = col_of(j);
+          if (d0 >= p.head_dim) continue;
           uint2 y;
-          y.x = pack16<kFp16>(o[m][d][0] * inv, o[m][d][1] * inv);
-          y.y = pack16<kFp16>(o[m][d][2] * inv, o[m][d][3] * inv);
+          y.x = pack16<kFp16>(w[m][j][0] * inv, w[m][j][1] * inv);
+          y.y = pack16<kFp16>(w[m][j][2] * inv, w[m][j][3] * inv);
           *reinterpret_cast<uint2*>(op + 2 * d0) = y;
         }
       }
     }
-    __syncthreads();  // LDS is free for the next item
+    __syncthreads();  // LDS is free for the next item, but for `patch`
+    if (__builtin_expect(last && patch != 0, 0)) {
+      // infinities and NaN among the values of the steps past the context, left out above
+      for (int e = tid; e < D::kRows * p.head_dim; e += kThreads) {
+        const int row = first_row + e / p.head_dim, col = e % p.head_dim, tok = row / p.group;
+        if (tok >= T) continue;
+        uint16_t* op = reinterpret_cast<uint16_t*>(
+            p.out + (q0 + tok) * p.o_token +
+            (h * p.group + row - tok * p.group) * p.o_head) + col;
+        float y = widen16<kFp16>(*op);
+        for (int j = -(kv & 31); j < end - kv; ++j) {  // from the first such step on
+          if (!(seen4(tok, j) & 1u)) continue;
+          const int slot = min((kv + j) >> p.c.page_shift, p.t.max_pages - 1);
+          const int64_t page = min(max(table[slot], 0), static_cast<int>(p.c.num_pages) - 1);
+          const char* at = p.c.v + page * p.c.vs[1] + ((kv + j) & low) * p.c.vs[2] +
+                           h * p.c.vs[3] + col * D::kEs;
+          uint32_t bits, rest;
+          if constexpr (kE4M3) widen4<kFp16>(*reinterpret_cast<const uint8_t*>(at), &bits, &rest);
+          else bits = *reinterpret_cast<const uint16_t*>(at);
+          if (!finite16<kFp16>(bits & 0xffffu)) y += vs * widen16<kFp16>(bits & 0xffffu);
+        }
+        *op = static_cast<uint16_t>(pack16<kFp16>(y, y) & 0xffffu);
+      }
+      __syncthreads();
+    }
   }
 }
 
 template <bool kFp16, bool kE4M3, int DP, int MF, int WR, int NW, int NST>
 hipError_t launch_attention_as(const AttnParams& p, const AttnShape& s, hipStream_t stream) {
   using D = AttnDims<kE4M3, DP, MF, WR, NW, NST>;
-  if (p.tile_keys != D::kKeys || p.block_rows != D::kRows) return hipErrorInvalidValue;
+  if (s.tile_keys != D::kKeys || s.block_rows != D::kRows) return hipErrorInvalidValue;
   attention_kernel<kFp16, kE4M3, DP, MF, WR, NW, NST>
       <<<dim3(static_cast<uint32_t>(s.grid)), dim3(NW * kWave), 0, stream>>>(p);
   return hipGetLastError();
@@ -813,23 +897,26 @@ hipError_t launch_attention_as(const AttnParams& p, const AttnShape& s, hipStrea
 
 template <bool kFp16, bool kE4M3>
 hipError_t launch_attention(const AttnParams& p, const AttnShape& s, hipStream_t stream) {
-#define SGG_ATTN(dp, m, w, n, st)                                       \
-  if (s.padded_dim == dp && s.mf == m && s.wr == w && s.nw == n)        \
+  // an 8-bit ring holds twice the stages in the same memory
+  constexpr int k = kE4M3 ? 2 : 1;
+#define SGG_ATTN(dp, m, w, n, st)                                \
+  if (s.padded_dim == dp && s.mf == m && s.wr == w && s.nw == n) \
     return launch_attention_as<kFp16, kE4M3, dp, m, w, n, st>(p, s, stream)
-  SGG_ATTN(64, 1, 1, 1, 3);
-  SGG_ATTN(64, 1, 1, 4, 2);
-  SGG_ATTN(64, 1, 2, 2, 3);
-  SGG_ATTN(64, 1, 4, 4, 4);
-  SGG_ATTN(64, 2, 4, 4, 4);
+  SGG_ATTN(64, 1, 1, 1, 4);
+  SGG_ATTN(64, 1, 1, 4, 4);
+  SGG_ATTN(64, 2, 1, 4, 4);
+  SGG_ATTN(64, 4, 1, 4, 4);
+  SGG_ATTN(64, 4, 2, 4, 4);
   SGG_ATTN(64, 4, 4, 4, 4);
-  SGG_ATTN(128, 1, 1, 1, 2);
-  SGG_ATTN(128, 1, 1, 4, 2);
-  SGG_ATTN(128, 1, 2, 2, 3);
-  SGG_ATTN(128, 1, 4, 4, 3);
-  SGG_ATTN(128, 2, 4, 4, 3);
-  SGG_ATTN(256, 1, 2, 2, 2);
-  SGG_ATTN(256, 1, 4, 4, 2);
-  SGG_ATTN(256, 2, 4, 4, 2);
+  SGG_ATTN(128, 1, 1, 1, 2 * k);
+  SGG_ATTN(128, 1, 1, 4, 2 * k);
+  SGG_ATTN(128, 2, 1, 4, 2 * k);
+  SGG_ATTN(128, 4, 1, 4, 2 * k);
+  SGG_ATTN(128, 4, 2, 4, 3);
+  SGG_ATTN(128, 4, 4, 4, 4);
+  SGG_ATTN(256, 1, 2, 4, 2 * k);
+  SGG_ATTN(256, 2, 2, 4, 2 * k);
+  SGG_ATTN(256, 2, 4, 4, 3);
 #undef SGG_ATTN
   return hipErrorInvalidValue;
 }

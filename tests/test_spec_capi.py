@@ -160,6 +160,7 @@ def attention(q=F, qt=4096, qh=128, out=F, ot=4096, oh=128, dtype=BF16, hq=32, c
     (dict(out=0), -1, "out is NULL"), (dict(kv=0), -1, "kv_lens"), (dict(ind=0), -1, "q_indptr"),
     (dict(bs=4097), -2, "4096"), (dict(n=1 << 31), -1, "num_tokens"), (dict(mq=-1), -1, "max_q_len"),
     (dict(mkv=1 << 31), -1, "max_kv_len"), (dict(mq=1 << 30), -2, "max_q_len"),
+    (dict(n=1 << 28), -2, "2^30"),
     (dict(mkv=5000, wsb=16), -3, "workspace"), (dict(mkv=5000, ws=0), -1, "workspace"),
     (dict(mkv=5000, ws=F + 8), -2, "aligned")])
 def test_attention_refused(kw, code, text):
@@ -222,18 +223,19 @@ def test_ranges_cover_every_tile_and_fit_the_workspace():
             assert s["grid"] % hkv == 0 and s["slots"] == 0
             whole += 1
             continue
-        N = max(min(s["ranges"], -(-total // s["min_tiles"])), 1)
-        assert s["grid"] == s["ranges"] * hkv
+        size = max(-(-total // s["ranges"]), s["min_tiles"])
+        N = -(-total // size)
+        assert s["grid"] == s["ranges"] * hkv and N <= s["ranges"]
         used, starts = set(), np.concatenate([[0], np.cumsum(units)])
         pieces = {}
         for i in range(N):
-            pos, stop = i * total // N, min((i + 1) * total // N, total)
+            pos, stop = i * size, min((i + 1) * size, total)
             while pos < stop:
                 u = int(np.searchsorted(starts, pos, side="right")) - 1
                 at, n = int(starts[u]), units[u]
                 t0, t1 = pos - at, min(n, stop - at)
-                r0 = ((at + 1) * N - 1) // total
-                chunks = ((at + n) * N - 1) // total - r0 + 1
+                r0 = at // size
+                chunks = (at + n - 1) // size - r0 + 1
                 pieces.setdefault(u, []).append((i - r0, chunks, t0, t1))
                 if chunks > 1:
                     slot = 2 * i + (1 if i == r0 else 0)
