@@ -123,11 +123,16 @@ namespace sgg {
 // The workgroup shape of an attention call and the division of its keys.
 //
 // Rows: the smallest block that holds the query rows of one request and kv
-// head (max_q_len tokens times the group).  Up to 64 rows each wave holds them
+// head (max_q_len tokens times the group).  Up to 32 rows each wave holds them
 // all and takes keys of its own, so that a key is read from LDS and widened once
-// for all rows and no wave waits for another; one wave a workgroup where there
-// are enough requests and kv heads to fill the GPU that way, else four.  Above,
-// and for heads of over 128 columns, waves lie side by side over the rows too.
+// for all rows and no wave waits for another.  Above, and for heads of over 128
+// columns, two or four waves lie side by side over the rows.  Four row fragments
+// a wave need the registers of a whole SIMD and leave no second wave to fill its
+// pauses: 64 rows as 4 x 1 waves took 196 us where 2 x 2 took 181 (64 requests
+// of 16 tokens, 2048-4096 keys), 512-token chunks 288 us where 2 x 4 took 171.
+// Up to 16 rows, two waves a workgroup once that fills the GPU: a second
+// workgroup on the CU hides the beginnings and ends of the units (256 one-token
+// requests 299 us, with four waves 310; one request, split, 16 us against 13).
 AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                      int32_t cache_bytes, int32_t max_q_len, int64_t max_kv_len) {
   AttnShape s{};
@@ -139,12 +144,13 @@ AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head
     s.mf = rows <= 32 ? 1 : 2;
     s.wr = rows <= 64 ? 2 : 4;
   } else {
-    s.mf = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    s.wr = rows <= 16 * s.mf ? 1 : rows <= 32 * s.mf ? 2 : 4;
-  }
-  if (rows <= 16 && s.padded_dim <= 128 && static_cast<int64_t>(bs) * kv_heads >= 1024) {
-    s.nw = 1;
-    resident = 1024;
+    s.mf = rows <= 16 ? 1 : 2;
+    s.wr = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+    if (s.wr > 1) resident = 512;
+    if (s.mf == 1 && static_cast<int64_t>(bs) * kv_heads >= 512) {
+      s.nw = 2;
+      resident = 512;
+    }
   }
   s.block_rows = 16 * s.mf * s.wr;
   s.tile_keys = 32 * (s.nw / s.wr) * (cache_bytes == 1 && s.wr == 4 ? 2 : 1);
@@ -160,8 +166,9 @@ AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head
     int64_t n = resident / kv_heads;
     if (n > most) n = most;
     s.ranges = static_cast<int32_t>(n < 1 ? 1 : n);
-    s.grid = static_cast<int64_t>(s.ranges) * kv_heads;
-    if (s.ranges > 1) s.slots = 2 * s.grid;
+    if (s.ranges > 1) s.slots = 2 * s.ranges * static_cast<int64_t>(kv_heads);
+    // (the kernel may take the batch by units)
+    s.grid = (units > s.ranges ? units : s.ranges) * kv_heads;
   }
   return s;
 }
@@ -421,6 +428,7 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   p.v_scale = v_scale;
   p.counters = static_cast<int32_t*>(workspace);
   p.part = static_cast<char*>(workspace) + sgg::kJoinBytes;
+  p.part_bytes = static_cast<uint32_t>(need - (need ? sgg::kJoinBytes : 0));
   p.num_tokens = num_tokens;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.bs = bs;

@@ -10,8 +10,8 @@
 namespace sgg {
 
 // The chunks of a unit are joined in groups of kJoin, level by level.
-constexpr int kJoin = 8;
-constexpr int kJoinLevels = 4;  // up to 4096 chunks
+constexpr int kJoin = 32;
+constexpr int kJoinLevels = 2;  // up to 1024 chunks
 // Arrival counters lie in a fixed region at the start of the workspace, so
 // that they never share memory with another call's partial results.
 constexpr int kJoinSlots = 32768;
@@ -29,6 +29,7 @@ struct AttnParams {
   const float* v_scale;
   int32_t* counters;       // [kJoinLevels][kJoinSlots], zero between calls
   char* part;              // slots of partial results (attention_kernel)
+  uint32_t part_bytes;     // below 2^32
   int64_t num_tokens;
   float scale_log2;        // scale * log2(e): the softmax runs on powers of two
   int32_t bs, words, head_dim, group;

@@ -37,14 +37,17 @@ typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 // ------------------------------------------------------- division of the work
 //
 // A unit is a row block of a request (for one kv head) with the key tiles that
-// it may see.  The tiles of all units, one after another, are cut into equal
-// ranges per kv head, one a workgroup, whatever the units' lengths: workgroups
-// end together although requests differ.  A range covers the end of one unit,
-// whole units, and the beginning of another; the pieces of a unit are joined
-// through the workspace.  Reading two arrays of bs numbers and one workgroup
-// scan stand in for a plan on the host, so that the call depends on nothing but
-// its inputs and can be captured.  Where there are many times more units than
-// workgroups that fit (chunks of prompts), each workgroup takes one unit.
+// it may see.  Where the batch has a unit for every workgroup that fits, and no
+// unit is much longer than a workgroup's equal share, each workgroup takes one
+// unit.  Else the tiles of all units, one after another, are cut into equal
+// ranges per kv head, one a workgroup, whatever the units' lengths: a range
+// covers the end of one unit, whole units, and the beginning of another, and the
+// pieces of a unit are joined through the workspace.  (A join waits for three
+// round trips through a memory system that is busy with keys and values, 5 -
+// 10 us: 64 requests of 2048 - 4096 keys take 180 us by units, 200 by ranges.)
+// Reading two arrays of bs numbers and one workgroup scan stand in for a plan on
+// the host, so that the call depends on nothing but its inputs and can be
+// captured.
 //
 // Rows of a request, tokens * group, are below 2^30 (checked on the host), and
 // so are a batch's units; the tiles of a batch are counted in 64 bits, and
@@ -113,7 +116,13 @@ __device__ __forceinline__ char* uniform_ptr(char* x) {
 template <int NW>
 struct AttnFind {
   int64_t scan[NW];
+  int units[NW], longest[NW];
   AttnUnit unit;
+};
+// Of all requests: positions, units, and the tiles of the longest unit.
+struct AttnTotal {
+  int64_t all;
+  int units, longest;
 };
 
 // A thread's requests: the weights of all before them, their own, and the first.
@@ -122,37 +131,54 @@ struct AttnShare {
   AttnRequest first;
 };
 
-// Returns the total weight.
 template <int NW, int R, int K>
-__device__ __forceinline__ int64_t attn_scan(const AttnWork<NW, R, K>& a, AttnFind<NW>* f,
-                                             AttnShare* s) {
+__device__ __forceinline__ AttnTotal attn_scan(const AttnWork<NW, R, K>& a, AttnFind<NW>* f,
+                                               AttnShare* s) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int bs = a.p.bs, per = (bs + NW * kWave - 1) / (NW * kWave);
   const int r0 = tid * per, r1 = min(r0 + per, bs);
   s->first = AttnRequest{0, 0, 0, 0};
   if (r0 < r1) s->first = request_of(a.p, r0);
   int64_t w = a.weight(s->first);
+  int units = a.blocks(s->first);
+  int longest = units ? (s->first.context + s->first.tokens + K - 1) / K : 0;
 #pragma unroll 1
-  for (int r = r0 + 1; r < r1; ++r) w += a.weight(request_of(a.p, r));
+  for (int r = r0 + 1; r < r1; ++r) {
+    const AttnRequest q = request_of(a.p, r);
+    const int n = a.blocks(q);
+    w += a.weight(q);
+    units += n;
+    longest = max(longest, n ? (q.context + q.tokens + K - 1) / K : 0);
+  }
   int64_t x = w;
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) {
     const int64_t y = __shfl_up(x, d);
     if (lane >= d) x += y;
+    units += __shfl_xor(units, d);
+    longest = max(longest, __shfl_xor(longest, d));
   }
-  if (lane == kWave - 1) f->scan[wave] = x;
+  if (lane == kWave - 1) {
+    f->scan[wave] = x;
+    f->units[wave] = units;
+    f->longest[wave] = longest;
+  }
   __syncthreads();
   int64_t total = 0, below = 0;
+  units = longest = 0;
 #pragma unroll
   for (int k = 0; k < NW; ++k) {
     if (k < wave) below += f->scan[k];
     total += f->scan[k];
+    units += f->units[k];
+    longest = max(longest, f->longest[k]);
   }
   s->before = below + x - w;
   s->mine = w;
   const uint32_t hi = uniform(static_cast<int>(total >> 32));
   const uint32_t lo = uniform(static_cast<int>(total));
-  return static_cast<int64_t>(hi) << 32 | lo;
+  return {static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo), uniform(units),
+          uniform(longest)};
 }
 
 // The unit that holds position `pos` (below the total).
@@ -241,6 +267,18 @@ __device__ __forceinline__ float row_sum(float x) {
   x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Eight bytes with device-scope coherence, as load_coherent16 / store_coherent16.
+__device__ __forceinline__ float2 load_coherent8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(
+                                        r, static_cast<int>(off), 0, kDeviceScopePolicy));
+}
+__device__ __forceinline__ void store_coherent8(__amdgpu_buffer_rsrc_t r, uint32_t off, float x,
+                                                float y) {
+  typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+  __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, make_float2(x, y)), r,
+                                        static_cast<int>(off), 0, kDeviceScopePolicy);
 }
 
 template <int N>
@@ -394,13 +432,15 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
   // this workgroup's range of positions: of per_range tiles, or single units
   AttnWork<NW, D::kRows, D::kKeys> work{p, p.ranges == 0};
   AttnShare share;
-  int64_t all = attn_scan(work, &find, &share);
-  if (!work.by_unit && all > INT32_MAX) {
+  AttnTotal sizes = attn_scan(work, &find, &share);
+  if (!work.by_unit &&
+      (sizes.all > INT32_MAX ||
+       (sizes.units >= p.ranges && sizes.longest <= 2 * (sizes.all / p.ranges)))) {
     work.by_unit = true;
     __syncthreads();
-    all = attn_scan(work, &find, &share);
+    sizes = attn_scan(work, &find, &share);
   }
-  const int total = static_cast<int>(all);
+  const int total = static_cast<int>(sizes.all);
   const uint32_t range = uniform(blockIdx.x / heads), stride = uniform(gridDim.x / heads);
   // (quotients come from the vector unit: back to scalar registers)
   const uint32_t per_range = uniform(
@@ -659,7 +699,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
           // A key hidden from a row has weight 0 there, but 0 times an infinity
           // or NaN in its value is NaN: past the context, such values go through
           // the product as 0, and are added to the rows that see them at the end.
-          constexpr int kGroup = kDT < 8 ? kDT : 8;
+          constexpr int kGroup = 4;
 #pragma unroll
           for (int d0 = 0; d0 < kDT; d0 += kGroup) {
             u32x4_t vf[kGroup];
@@ -741,15 +781,22 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
         for (int j = 0; j < D::kCols; ++j) w[m][j] = o[m][j];
     }
 
-    // Join the chunks of the unit.  Level by level, the items of a group of
-    // kJoin leave their sums in the workspace and count themselves; the last
-    // to arrive reads the group's, in order, and goes on for it.  The sums
-    // move with device-scope accesses, so no cache is written back or dropped.
+    // Join the chunks of the unit.  The items of a group of kJoin leave their
+    // sums in the workspace and count themselves; the last to arrive reads the
+    // group's, in order, and goes on for it to the next level.  The sums move
+    // with device-scope accesses, so no cache is written back or dropped.
     bool last = true;
     if (__builtin_expect(chunks > 1, 0)) {
       int c = chunk;
       __syncthreads();
       bool flag = patch != 0;  // travels in the sign of the sums
+      // in a slot, the sums lie as the lanes hold them: whole lines move
+      auto sums_at = [&](int m, int j) -> uint32_t {
+        return ((wave * MF + m) * D::kCols + j) * 1024 + lane * 16;
+      };
+      auto stats_at = [&](int m) -> uint32_t {
+        return D::kRows * DP * 4 + ((wr * MF + m) * 16 + l16) * 8;
+      };
 #pragma unroll 1
       for (int level = 0, step = 1; step < chunks; ++level, step *= kJoin) {
         const int n = (chunks + step - 1) / step, group = c / step / kJoin;
@@ -761,23 +808,14 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
           return (2 * static_cast<int64_t>(range0 + k) + (k == 0 ? 1 : 0)) * heads + h;
         };
         if (members > 1) {
-          char* mine = uniform_ptr(p.part + slot_of(c) * D::kSlotBytes);
-          const __amdgpu_buffer_rsrc_t out = buffer_rsrc(mine, D::kSlotBytes);
+          const __amdgpu_buffer_rsrc_t out =
+              buffer_rsrc(uniform_ptr(p.part + slot_of(c) * D::kSlotBytes), D::kSlotBytes);
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
-            const int row = (wr * MF + m) * 16 + l16;
-            int tok, qh;
-            if (!row_of(m, &tok, &qh)) continue;
 #pragma unroll
-            for (int j = 0; j < D::kCols; ++j)
-              store_coherent16(out, (row * DP + col_of(j)) * 4, w[m][j]);
-            if (wk == 0 && g == 0) {
-              __hip_atomic_store(reinterpret_cast<float*>(mine + D::kRows * DP * 4) + 2 * row,
-                                 mx[m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-              __hip_atomic_store(reinterpret_cast<float*>(mine + D::kRows * DP * 4) + 2 * row + 1,
-                                 flag ? -sum[m] : sum[m], __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
-            }
+            for (int j = 0; j < D::kCols; ++j) store_coherent16(out, sums_at(m, j), w[m][j]);
+            if (wk == 0 && g == 0)
+              store_coherent8(out, stats_at(m), mx[m], flag ? -sum[m] : sum[m]);
           }
           wave_stores_done();
           __syncthreads();
@@ -792,53 +830,65 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
           __syncthreads();
           last = uniform(arrived) == members - 1;
           if (!last) break;
-          float top[MF], total[MF];
+          // a batch of members at a time, all of its loads under way at once
+          constexpr int kBatch = MF * D::kCols <= 2 ? 8 : MF * D::kCols <= 16 ? 16 / (MF * D::kCols) : 1;
+          const __amdgpu_buffer_rsrc_t in = buffer_rsrc(uniform_ptr(p.part), p.part_bytes);
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
-            top[m] = -INFINITY;
-            total[m] = 0.0f;
+            mx[m] = -INFINITY;
+            sum[m] = 0.0f;
 #pragma unroll
             for (int j = 0; j < D::kCols; ++j) w[m][j] = f32x4{0, 0, 0, 0};
           }
-#pragma unroll 2
-          for (int k = 0; k < members; ++k) {
-            const char* from = uniform_ptr(p.part + slot_of(first + k * step) * D::kSlotBytes);
-            const __amdgpu_buffer_rsrc_t in = buffer_rsrc(from, D::kSlotBytes);
-            const float* ml = reinterpret_cast<const float*>(from + D::kRows * DP * 4);
+#pragma unroll 1
+          for (int k0 = 0; k0 < members; k0 += kBatch) {
+            float2 ml[kBatch][MF];
+            f32x4 y[kBatch][MF][D::kCols];
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-              const int row = (wr * MF + m) * 16 + l16;
-              int tok, qh;
-              if (!row_of(m, &tok, &qh)) continue;
-              const float a = __hip_atomic_load(ml + 2 * row, __ATOMIC_RELAXED,
-                                                __HIP_MEMORY_SCOPE_AGENT);
-              const float b = __hip_atomic_load(ml + 2 * row + 1, __ATOMIC_RELAXED,
-                                                __HIP_MEMORY_SCOPE_AGENT);
-              const float t2 = fmaxf(top[m], a);
-              const float wa = top[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top[m] - t2);
-              const float wb = a == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(a - t2);
-              flag |= signbit(b);
-              total[m] = total[m] * wa + fabsf(b) * wb;
-              top[m] = t2;
+            for (int k = 0; k < kBatch; ++k) {
+              const uint32_t at = static_cast<uint32_t>(
+                  slot_of(first + min(k0 + k, members - 1) * step) * D::kSlotBytes);
 #pragma unroll
-              for (int j = 0; j < D::kCols; ++j) {
-                const f32x4 y = load_coherent16(in, (row * DP + col_of(j)) * 4);
+              for (int m = 0; m < MF; ++m) {
+                ml[k][m] = load_coherent8(in, at + stats_at(m));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[m][j][i] = w[m][j][i] * wa + y[i] * wb;
+                for (int j = 0; j < D::kCols; ++j)
+                  y[k][m][j] = load_coherent16(in, at + sums_at(m, j));
               }
             }
-          }
 #pragma unroll
-          for (int m = 0; m < MF; ++m) {
-            mx[m] = top[m];
-            sum[m] = total[m];
+            for (int m = 0; m < MF; ++m) {
+              float top = mx[m];
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k][m].x);
+              const float old = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - top);
+              sum[m] *= old;
+#pragma unroll
+              for (int j = 0; j < D::kCols; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[m][j][i] *= old;
+              mx[m] = top;
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const float2 e = ml[k][m];
+                const bool in_group = k0 + k < members;
+                flag |= in_group && signbit(e.y);
+                const float f =
+                    !in_group || e.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(e.x - top);
+                if (!in_group) continue;
+                sum[m] += fabsf(e.y) * f;
+#pragma unroll
+                for (int j = 0; j < D::kCols; ++j)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) w[m][j][i] += y[k][m][j][i] * f;
+              }
+            }
           }
         }
         c = first;
       }
       if (flag) patch = 1;
     }
-
     const float vs = kE4M3 && p.v_scale ? p.v_scale[h] : 1.0f;
     if (last) {
 #pragma unroll
@@ -902,18 +952,16 @@ hipError_t launch_attention(const AttnParams& p, const AttnShape& s, hipStream_t
 #define SGG_ATTN(dp, m, w, n, st)                                \
   if (s.padded_dim == dp && s.mf == m && s.wr == w && s.nw == n) \
     return launch_attention_as<kFp16, kE4M3, dp, m, w, n, st>(p, s, stream)
-  SGG_ATTN(64, 1, 1, 1, 4);
+  SGG_ATTN(64, 1, 1, 2, 4);
   SGG_ATTN(64, 1, 1, 4, 4);
   SGG_ATTN(64, 2, 1, 4, 4);
-  SGG_ATTN(64, 4, 1, 4, 4);
-  SGG_ATTN(64, 4, 2, 4, 4);
-  SGG_ATTN(64, 4, 4, 4, 4);
-  SGG_ATTN(128, 1, 1, 1, 2 * k);
+  SGG_ATTN(64, 2, 2, 4, 4);
+  SGG_ATTN(64, 2, 4, 4, 4);
+  SGG_ATTN(128, 1, 1, 2, 2 * k);
   SGG_ATTN(128, 1, 1, 4, 2 * k);
   SGG_ATTN(128, 2, 1, 4, 2 * k);
-  SGG_ATTN(128, 4, 1, 4, 2 * k);
-  SGG_ATTN(128, 4, 2, 4, 3);
-  SGG_ATTN(128, 4, 4, 4, 4);
+  SGG_ATTN(128, 2, 2, 4, 2 * k);
+  SGG_ATTN(128, 2, 4, 4, 4);
   SGG_ATTN(256, 1, 2, 4, 2 * k);
   SGG_ATTN(256, 2, 2, 4, 2 * k);
   SGG_ATTN(256, 2, 4, 4, 3);

@@ -189,7 +189,7 @@ def test_empty_batches_are_nothing_to_do():
     assert C.spec_kv_copy_pages(cache(), 0, 0, 0, 0) == 0
 
 
-JOIN_BYTES = 4 * 4 * 32768
+JOIN_BYTES = 4 * 2 * 32768
 
 
 def test_ranges_cover_every_tile_and_fit_the_workspace():
@@ -225,7 +225,7 @@ def test_ranges_cover_every_tile_and_fit_the_workspace():
             continue
         size = max(-(-total // s["ranges"]), s["min_tiles"])
         N = -(-total // size)
-        assert s["grid"] == s["ranges"] * hkv and N <= s["ranges"]
+        assert s["grid"] >= s["ranges"] * hkv and N <= s["ranges"]
         used, starts = set(), np.concatenate([[0], np.cumsum(units)])
         pieces = {}
         for i in range(N):
