@@ -255,20 +255,13 @@ __device__ __forceinline__ void widen4(int x, uint32_t* lo, uint32_t* hi) {
   }
 }
 
-// Maximum / sum over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48).
+// Maximum over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float row_max(float x) {
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-__device__ __forceinline__ float row_sum(float x) {
-  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // Eight bytes with device-scope coherence, as load_coherent16 / store_coherent16.
 __device__ __forceinline__ float2 load_coherent8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(
@@ -334,10 +327,23 @@ __device__ __forceinline__ int swizzle(int r) {
 template <int kVecs>
 constexpr int kSwizzled = kVecs < 16 ? kVecs : 16;  // pieces among which it permutes
 
-// In fp16 the exponentials, at most 1, are kept 2^12 times as large, so that
-// those down to 2^-26 of the largest are normal numbers; bf16 has the range.
+// The weights are at most 2^kPSlack of their reference.  In fp16 they are kept
+// 2^7 times as large, at most 2^15, so that those down to 2^-21 of the reference
+// are normal numbers; bf16 has the range.
+constexpr float kPSlack = 8.0f;
 template <bool kFp16>
-constexpr float kPShift = kFp16 ? 12.0f : 0.0f;
+constexpr float kPShift = kFp16 ? 7.0f : 0.0f;
+template <bool kFp16>
+constexpr u32x4_t kOnes = kFp16 ? u32x4_t{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}
+                                : u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+
+// The largest of three; a NaN gives way to a number.  (Plain fmaxf first
+// quiets each operand, an instruction of its own.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
 
 // Whether a 16-bit value of a packed pair is an infinity or NaN (bits of its exponent).
 template <bool kFp16>
@@ -552,11 +558,12 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
     if (tid == 0) patch = 0;
 
     f32x4 o[MF][kDT];
-    float mx[MF], sum[MF];
+    float mx[MF];
+    f32x4 sum[MF];  // every element of a lane: the sum of its row
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
       mx[m] = -INFINITY;
-      sum[m] = 0.0f;
+      sum[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int d = 0; d < kDT; ++d) o[m][d] = f32x4{0, 0, 0, 0};
     }
@@ -650,14 +657,18 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
           u32x4_t pf[MF];
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
-            float top =
-                fmaxf(fmaxf(fmaxf(st[m][0][0], st[m][0][1]), fmaxf(st[m][0][2], st[m][0][3])),
-                      fmaxf(fmaxf(st[m][1][0], st[m][1][1]), fmaxf(st[m][1][2], st[m][1][3])));
-            top = fmaxf(row_max(top), mx[m]);
-            if (__ballot(top > mx[m])) {  // a row's maximum has grown
+            float top = max3(st[m][0][0], st[m][0][1], st[m][0][2]);
+            top = max3(top, st[m][0][3], st[m][1][0]);
+            top = max3(top, st[m][1][1], st[m][1][2]);
+            top = max3(top, st[m][1][3], mx[m]);
+            // The reference of the exponentials need not be the maximum: it moves
+            // up once a score is 2^kPSlack past it, which a row does a few times,
+            // and only then do the lanes of the row compare theirs.
+            if (__ballot((top - mx[m]) * scale > kPSlack)) {
+              top = row_max(top);
               const float alpha =
                   mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx[m] - top) * scale);
-              sum[m] *= alpha;
+              sum[m][0] *= alpha;
 #pragma unroll
               for (int d = 0; d < kDT; ++d)
 #pragma unroll
@@ -668,14 +679,14 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 4; ++i)
                 st[m][t][i] = __builtin_amdgcn_exp2f(fmaf(st[m][t][i], scale, -ref));
-                sum[m] += st[m][t][i];
-              }
             pf[m] = u32x4_t{pack16<kFp16>(st[m][0][0], st[m][0][1]),
                             pack16<kFp16>(st[m][0][2], st[m][0][3]),
                             pack16<kFp16>(st[m][1][0], st[m][1][1]),
                             pack16<kFp16>(st[m][1][2], st[m][1][3])};
+            // the row's sum, of the weights as they are rounded: a product with ones
+            sum[m] = attn_mfma<kFp16>(kOnes<kFp16>, pf[m], sum[m]);
           }
           // O^T += V^T P^T
           auto v_fragment = [&](int d) -> u32x4_t {
@@ -727,11 +738,12 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
     if (!finite) patch = 1;
     // the waves that shared the rows join theirs: w holds columns col_of(j) of the sums
     f32x4 w[MF][D::kCols];
+    float total[MF];
     auto col_of = [&](int j) -> int { return 16 * (D::kWK > 1 ? wk * D::kCols + j : j) + 4 * g; };
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-      sum[m] = row_sum(sum[m]);
       mx[m] *= scale;  // from here on, in units of powers of two
+      total[m] = sum[m][0];
     }
     if constexpr (D::kWK > 1) {
       __syncthreads();  // the last tile has been read
@@ -740,12 +752,12 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
       for (int m = 0; m < MF; ++m) {
 #pragma unroll
         for (int d = 0; d < kDT; ++d) mo[((wave * MF + m) * kDT + d) * kWave + lane] = o[m][d];
-        if (g == 0) merge_ml[wave][m][l16] = make_float2(mx[m], sum[m]);
+        if (g == 0) merge_ml[wave][m][l16] = make_float2(mx[m], total[m]);
       }
       __syncthreads();
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        float top = -INFINITY, f[D::kWK], total = 0.0f;
+        float top = -INFINITY, f[D::kWK], all = 0.0f;
         float2 ml[D::kWK];
 #pragma unroll
         for (int k = 0; k < D::kWK; ++k) ml[k] = merge_ml[k * WR + wr][m][l16];
@@ -754,10 +766,10 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
 #pragma unroll
         for (int k = 0; k < D::kWK; ++k) {
           f[k] = ml[k].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[k].x - top);
-          total += ml[k].y * f[k];
+          all += ml[k].y * f[k];
         }
         mx[m] = top;
-        sum[m] = total;
+        total[m] = all;
         f32x4 y[D::kCols][D::kWK];
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j)
@@ -815,7 +827,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
 #pragma unroll
             for (int j = 0; j < D::kCols; ++j) store_coherent16(out, sums_at(m, j), w[m][j]);
             if (wk == 0 && g == 0)
-              store_coherent8(out, stats_at(m), mx[m], flag ? -sum[m] : sum[m]);
+              store_coherent8(out, stats_at(m), mx[m], flag ? -total[m] : total[m]);
           }
           wave_stores_done();
           __syncthreads();
@@ -836,7 +848,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
             mx[m] = -INFINITY;
-            sum[m] = 0.0f;
+            total[m] = 0.0f;
 #pragma unroll
             for (int j = 0; j < D::kCols; ++j) w[m][j] = f32x4{0, 0, 0, 0};
           }
@@ -862,7 +874,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k][m].x);
               const float old = mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - top);
-              sum[m] *= old;
+              total[m] *= old;
 #pragma unroll
               for (int j = 0; j < D::kCols; ++j)
 #pragma unroll
@@ -876,7 +888,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
                 const float f =
                     !in_group || e.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(e.x - top);
                 if (!in_group) continue;
-                sum[m] += fabsf(e.y) * f;
+                total[m] += fabsf(e.y) * f;
 #pragma unroll
                 for (int j = 0; j < D::kCols; ++j)
 #pragma unroll
@@ -895,7 +907,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
       for (int m = 0; m < MF; ++m) {
         int tok, qh;
         if (!row_of(m, &tok, &qh)) continue;
-        const float inv = sum[m] > 0.0f ? vs / sum[m] : sum[m] != sum[m] ? sum[m] : 0.0f;
+        const float inv = total[m] > 0.0f ? vs / total[m] : total[m] != total[m] ? total[m] : 0.0f;
         char* op = p.out + (q0 + tok) * p.o_token + qh * p.o_head;
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j) {
