@@ -207,6 +207,15 @@ int spec_verify(const int32_t* tokens, const int32_t* parents, const int32_t* q_
                 int32_t* accept_lens, int32_t* next_tokens, void* workspace,
                 int64_t workspace_bytes, void* stream);
 
+/*
+ * spec_set_option -- process-wide settings; returns the previous value, -1 for
+ * an unknown name or a negative value.
+ *   "verify_spin_limit"  polls after which a workgroup of spec_verify that waits
+ *                        for the others of its request adds up their parts
+ *                        itself (the result is the same).  Default 65536.
+ */
+int64_t spec_set_option(const char* name, int64_t value);
+
 #ifdef __cplusplus
 }
 #endif

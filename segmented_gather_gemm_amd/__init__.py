@@ -34,6 +34,7 @@ from .speculative import (
     spec_kv_fork,
     spec_kv_resize,
     spec_kv_write,
+    spec_set_option,
     spec_tree_mask,
     spec_verify,
 )
@@ -47,6 +48,6 @@ __all__ = [
     "lora_expand", "lora_moe_add", "lora_moe_plan", "lora_moe_route", "lora_plan_device", "lora_plan_lm_head",
     "lora_plan_max_segments", "lora_plan_segments", "lora_qkv", "lora_qkv_noalloc",
     "lora_set_option", "lora_shrink", "PagedKVCache", "spec_attention", "spec_kv_compact",
-    "spec_kv_copy_pages", "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_tree_mask",
-    "spec_verify",
+    "spec_kv_copy_pages", "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_set_option",
+    "spec_tree_mask", "spec_verify",
 ]

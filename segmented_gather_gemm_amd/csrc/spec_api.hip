@@ -1,7 +1,9 @@
 // C-ABI entry points of the speculative decoding step (include/sgg_spec.h):
 // argument validation on the host, before anything is enqueued, then launches.
+#include <atomic>
 #include <cinttypes>
 #include <cmath>
+#include <cstring>
 
 #include "sgg_internal.h"
 #include "spec_attention.h"
@@ -14,6 +16,9 @@ using sgg::fail;
 static_assert(SPEC_MAX_REQUESTS == sgg::kSpecMaxRequests, "limits differ");
 
 namespace {
+
+// spec_set_option values.
+std::atomic<int64_t> g_verify_spin_limit{int64_t{1} << 16};
 
 #define SGG_CHECK(cond, code, ...) \
   do {                             \
@@ -445,6 +450,12 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   return launch_status(launch(p, s, static_cast<hipStream_t>(stream)), "attention");
 }
 
+extern "C" int64_t spec_set_option(const char* name, int64_t value) {
+  if (name != nullptr && std::strcmp(name, "verify_spin_limit") == 0 && value >= 0)
+    return g_verify_spin_limit.exchange(value);
+  return -1;
+}
+
 extern "C" int64_t spec_verify_workspace_bytes(int32_t bs, int64_t vocab) {
   return sgg::verify_workspace_bytes(bs, vocab);
 }
@@ -475,9 +486,26 @@ extern "C" int spec_verify(const int32_t* tokens, const int32_t* parents, const 
   SGG_CHECK(workspace_bytes >= need, SGG_ERR_CAPACITY,
             "workspace of %" PRId64 " bytes, the call needs %" PRId64, workspace_bytes, need);
   SGG_CHECK(sgg::aligned16(workspace), SGG_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
-  sgg::VerifyParams p{tokens, parents, q_indptr, target_probs, draft_probs, uniforms,
-                      final_uniforms, path, accept_lens, next_tokens, num_tokens, ld_target,
-                      ld_draft, vocab, ld_path, bs, path_width, workspace};
+  sgg::VerifyParams p{};
+  p.tokens = tokens;
+  p.parents = parents;
+  p.q_indptr = q_indptr;
+  p.p = target_probs;
+  p.q = draft_probs;
+  p.u = uniforms;
+  p.u_final = final_uniforms;
+  p.path = path;
+  p.accept = accept_lens;
+  p.next = next_tokens;
+  p.num_tokens = num_tokens;
+  p.ldp = ld_target;
+  p.ldq = ld_draft;
+  p.vocab = vocab;
+  p.ld_path = ld_path;
+  p.bs = bs;
+  p.path_width = path_width;
+  p.spin_limit = g_verify_spin_limit.load(std::memory_order_relaxed);
+  p.workspace = workspace;
   return launch_status(sgg::launch_verify(p, static_cast<hipStream_t>(stream)), "verify");
 }
 

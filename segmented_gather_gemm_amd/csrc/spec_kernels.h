@@ -109,9 +109,15 @@ struct VerifyParams {
   int32_t* next;
   int64_t num_tokens, ldp, ldq, vocab, ld_path;
   int32_t bs, path_width;
+  int64_t spin_limit;  // polls of a wait for the other workgroups of a request
   void* workspace;
+  // set by launch_verify
+  int32_t parts, tiles;  // workgroups, tiles of a row
+  int32_t* counters;     // [SPEC_MAX_REQUESTS], zero between calls
+  double* partials;      // [bs][2][64]
+  double* tile_sums;     // [bs][tiles]
 };
 int64_t verify_workspace_bytes(int32_t bs, int64_t vocab);
-hipError_t launch_verify(const VerifyParams& p, hipStream_t stream);
+hipError_t launch_verify(VerifyParams p, hipStream_t stream);
 
 }  // namespace sgg

@@ -7,257 +7,447 @@
 // residual after k rejections is max(p - a q, 0) with one running scalar a, so
 // a row is never written back: each use is one pass over p and q.
 //
+// A row is cut among the workgroups of its request, so that a batch of few
+// requests uses the whole memory system; all of them walk the tree, each for
+// itself (the same steps on the same numbers), and meet where a sum over the
+// row is needed: each leaves its part's sum in the workspace, counts itself,
+// and waits until the count says that all parts are there.  A wait is bounded:
+// one that sees no end adds up the other parts itself, in the same order.  At
+// the end each leaves the sums of its tiles of 1024 values, and one wave of the
+// last to arrive finds the tile and the place in it.
+//
 // Sums and comparisons are in 64 bits.  The values that come out are whole
 // numbers: in 32 bits, a sum over a vocabulary moves a border by 1e-7 or so,
 // and of the 1e5 borders of a flat row one in a hundred draws would land on
 // the other side; in 64 bits it is one in 1e9.
+//
+// What bounds it: one row (two with draft_probs) of floats per request from
+// memory; for few requests the chain of dependent round trips (nodes, their
+// probabilities, the row, the count, the tile), about 1 us each.
 #include "sgg_device.h"
 #include "spec_kernels.h"
 
 namespace sgg {
 namespace {
 
-constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / kWave;
-constexpr int kVerifyNodes = 1024;      // nodes of a request that are visited
-constexpr int kTile = 4 * kVerifyThreads;
-constexpr int kVerifyTiles = 1024;      // vocabulary up to 4 Mi
+constexpr int kVerifyNodes = 1024;  // nodes of a request that are visited
+constexpr int kTile = 1024;         // values of a tile: 16 a lane of one wave
+constexpr int kParts = 64;          // workgroups of a request at most
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
-  return v;
+// The value that lane (l - n) holds, by a shift within 16 lanes or a broadcast
+// of the last lane of one row of 16 (or two) to the next, 0 where there is none:
+// register moves of the vector unit, where a shuffle goes through LDS.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double from_below(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), kCtrl, kRows, 0xf, false);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), kCtrl, kRows, 0xf, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-
 __device__ __forceinline__ double wave_prefix(double v) {  // inclusive
-  const int lane = threadIdx.x % kWave;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const double y = __shfl_up(v, d);
-    if (lane >= d) v += y;
-  }
+  v += from_below<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v += from_below<0x112, 0xf>(v);
+  v += from_below<0x114, 0xf>(v);
+  v += from_below<0x118, 0xf>(v);
+  v += from_below<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
+  v += from_below<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
   return v;
 }
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double wave_sum(double v) { return lane_value(wave_prefix(v), 63); }
 
-// A probability as it counts: finite and positive, or 0.
-__device__ __forceinline__ double weight(double x) {
-  return x > 0.0 && x < __builtin_huge_val() ? x : 0.0;
+__device__ __forceinline__ double load_agent(const double* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void store_agent(double* p, double v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-struct Nodes {
-  int n;
-  int32_t parent[kVerifyNodes];
-  int32_t token[kVerifyNodes];
-  float px[kVerifyNodes];
-  float qx[kVerifyNodes];
-  float u[kVerifyNodes];
-  int32_t gone[kVerifyNodes];  // rejected tokens of the current node (no draft row)
+// A probability as it counts: finite and positive, or 0 (bits 1 .. 0x7f7fffff).
+__device__ __forceinline__ double weight(float x) {
+  return __float_as_uint(x) - 1u < 0x7f7fffffu ? x : 0.0f;
+}
+// What is left of p's weight x once a times q's has been taken.
+__device__ __forceinline__ double left_of(double x, double a, double q) {
+  return fmax(x - a * q, 0.0);
+}
+
+// Four floats from an address that need not be a multiple of 16.
+struct __attribute__((packed, aligned(4))) Four {
+  float x[4];
 };
 
-__global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyParams p) {
-  __shared__ Nodes s;
+template <bool kDraft>
+struct Row {
+  const float* p;
+  const float* q;  // kDraft
+  double a;
+  const int32_t* gone;  // rejected tokens (not kDraft)
+  int gone_n;
+  int vocab;
+
+  // Four values of the row for a lane whose values begin at v: the last four of
+  // the row where it ends before v + 4 (a row of fewer: one at a time).
+  __device__ __forceinline__ int place(int v) const { return max(min(v, vocab - 4), 0); }
+  __device__ __forceinline__ Four load(const float* x, int v) const {
+    const int at = place(v);
+    if (vocab >= 4) return *reinterpret_cast<const Four*>(x + at);
+    return Four{{x[0], vocab > 1 ? x[1] : 0.0f, vocab > 2 ? x[2] : 0.0f, 0.0f}};
+  }
+  // The weights of values place(v) .. place(v) + 3; 0 for those below v.
+  __device__ __forceinline__ void weights(int v, const Four& pv, const Four& qv, double* w) const {
+    const int at = place(v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = at + k >= v ? pv.x[k] : 0.0f;
+      w[k] = weight(x);
+      if (kDraft) w[k] = left_of(w[k], a, weight(qv.x[k]));
+    }
+    if (!kDraft) {
+#pragma unroll 1
+      for (int i = 0; i < gone_n; ++i) {
+        const int hit = gone[i] - at;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (hit == k) w[k] = 0.0;
+      }
+    }
+  }
+  // This wave's tiles first, first + step, .. below `stop`: use(t, sum of tile t).
+  // The next tile's values are under way while the sum of one is taken.
+  template <class Use>
+  __device__ __forceinline__ void tiles(int first, int stop, int step, const Use& use) const {
+    Four pv[4], qv[4];
+    const int lane4 = 4 * (threadIdx.x % kWave);
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pv[i] = load(p, t * kTile + i * 256 + lane4);
+        if (kDraft) qv[i] = load(q, t * kTile + i * 256 + lane4);
+      }
+    };
+    if (first < stop) fetch(first);
+#pragma unroll 1
+    for (int t = first; t < stop; t += step) {
+      double s = 0.0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        double w[4];
+        weights(t * kTile + i * 256 + lane4, pv[i], kDraft ? qv[i] : pv[i], w);
+        s += (w[0] + w[1]) + (w[2] + w[3]);
+      }
+      if (t + step < stop) fetch(t + step);
+      use(t, wave_sum(s));
+    }
+  }
+};
+
+template <bool kDraft>
+__global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams p) {
+  __shared__ struct {
+    int32_t parent[kVerifyNodes];
+    int32_t token[kVerifyNodes];
+    float px[kVerifyNodes];
+    float qx[kVerifyNodes];
+    float u[kVerifyNodes];
+  } s;
+  __shared__ int32_t gone_of[kVerifyNodes];  // rejected tokens of the current node (no draft row)
   __shared__ double part[kVerifyWaves];
-  __shared__ double tiles[kVerifyTiles];
-  __shared__ int cur, at, gone, path_len, done, found;
+  __shared__ int cur, at, gone, path_len, state, stale, seen;
   __shared__ double a, mass;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int r = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int r = blockIdx.x / p.parts, c = blockIdx.x % p.parts;
   const int64_t q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
   int32_t* path = p.path + r * p.ld_path;
   const int n = q0 < 0 || q1 > p.num_tokens || q1 <= q0
                     ? 0
                     : static_cast<int>(q1 - q0 < kVerifyNodes ? q1 - q0 : kVerifyNodes);
-  for (int j = tid; j < p.path_width; j += kVerifyThreads) path[j] = -1;
+  int32_t* counter = p.counters + r;
+  double* partial = p.partials + static_cast<int64_t>(r) * 2 * kParts;
+  double* tile_sums = p.tile_sums + static_cast<int64_t>(r) * p.tiles;
   if (n == 0) {
-    if (tid == 0) {
-      p.accept[r] = 0;
-      p.next[r] = -1;
+    if (c == 0) {
+      for (int j = tid; j < p.path_width; j += kVerifyThreads) path[j] = -1;
+      if (tid == 0) {
+        p.accept[r] = 0;
+        p.next[r] = -1;
+      }
     }
     return;
   }
   for (int i = tid; i < n; i += kVerifyThreads) {
     int par = p.parents[q0 + i];
     const int tok = p.tokens[q0 + i];
+    const float u = p.u[q0 + i];
     if (par < 0 || par >= i) par = -1;
     const bool in = tok >= 0 && tok < p.vocab && par >= 0;
     s.parent[i] = par;
     s.token[i] = tok;
     s.px[i] = in ? p.p[(q0 + par) * p.ldp + tok] : 0.0f;
     s.qx[i] = in && p.q ? p.q[(q0 + par) * p.ldq + tok] : 0.0f;
-    s.u[i] = p.u[q0 + i];
+    s.u[i] = u;
   }
   if (tid == 0) {
-    cur = 0, at = 1, gone = 0, path_len = 1, done = 0;
+    cur = 0, at = 1, gone = 0, path_len = 1, stale = 0;
     a = 0.0, mass = 1.0;
-    if (p.path_width > 0) path[0] = 0;
+    if (c == 0) path[0] = 0;
   }
   __syncthreads();
 
-  // w(v) of the current node's row; `near`: a rejected token may be among the four
-  const int64_t V = p.vocab;
-  auto row_weight = [&](int64_t v, const float* pr, const float* qr, double aa, int ng) {
-    const double x = weight(pr[v]);
-    if (qr) return weight(x - aa * weight(qr[v]));
-    for (int k = 0; k < ng; ++k)
-      if (s.gone[k] == v) return 0.0;
-    return x;
-  };
-  const auto block_sum = [&](double v) {
-    v = wave_sum(v);
-    __syncthreads();
-    if (lane == 0) part[wave] = v;
-    __syncthreads();
-    double t = 0.0;
-    for (int w = 0; w < kVerifyWaves; ++w) t += part[w];
-    return t;
-  };
-
+  // the tiles of part k are [first_tile(k), first_tile(k + 1))
+  const int per = (p.tiles + p.parts - 1) / p.parts;
+  auto first_tile = [&](int k) { return min(k * per, p.tiles); };
+  int arrivals = 0;  // of each workgroup of the request so far
   while (true) {
     // wave 0 walks on until a rejection needs the residual's mass, or the end
     if (wave == 0) {
-      int c = cur, next = at, ng = gone, len = path_len;
+      int node = cur, next = at, ng = gone, len = path_len, old = stale;
       double aa = a, mm = mass;
-      int state = 0;  // 1: at the end, 2: the mass of the residual is wanted
-      while (state == 0) {
+      int st = 0;  // 1: at the end, 2: the mass of the residual is wanted
+      // a node's numbers: of up to 64 nodes lane i holds node i
+      const bool held = n <= kWave;
+      const int mine = held && lane < n ? lane : 0;
+      const int parent_l = lane < n ? s.parent[mine] : -2, token_l = s.token[mine];
+      const float px_l = s.px[mine], qx_l = s.qx[mine], u_l = s.u[mine];
+      while (st == 0) {
         int child = -1;
-        for (int base = next & ~(kWave - 1); base < n && child < 0; base += kWave) {
-          const int i = base + lane;
-          const unsigned long long hit = __ballot(i >= next && i < n && s.parent[i] == c);
-          if (hit) child = base + __ffsll(hit) - 1;
-        }
-        if (child < 0 || len >= p.path_width) {
-          state = 1;
-          break;
-        }
-        const double px = weight(s.px[child]), u = s.u[child];
-        bool ok;
-        if (p.q) {
-          const double qx = weight(s.qx[child]);
-          ok = u * (mm * qx) < weight(px - aa * qx);
-        } else {
-          bool spent = false;
-          for (int k = 0; k < ng; ++k) spent |= s.gone[k] == s.token[child];
-          ok = !spent && u * mm < px;
-          if (!ok && !spent) {
-            mm -= px;
-            if (lane == 0) s.gone[ng] = s.token[child];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            ++ng;
+        if (len < p.path_width) {
+          for (int base = next & ~(kWave - 1); base < n && child < 0; base += kWave) {
+            const int i = base + lane;
+            const int par = held ? parent_l : i < n ? s.parent[i] : -2;
+            const unsigned long long hit = __ballot(i >= next && par == node);
+            if (hit) child = base + __ffsll(hit) - 1;
           }
+          child = __builtin_amdgcn_readfirstlane(child);
         }
-        if (ok) {
-          if (lane == 0) path[len] = child;
-          ++len;
-          c = child;
-          next = child + 1;
-          ng = 0;
-          aa = 0.0, mm = 1.0;
+        if (child < 0) {
+          st = 1;
+        } else if (old) {
+          st = 2;
+          next = child;
         } else {
+          const double px = weight(held ? lane_value(px_l, child) : s.px[child]);
+          const double u = held ? lane_value(u_l, child) : s.u[child];
+          const int token = held ? __builtin_amdgcn_readlane(token_l, child) : s.token[child];
+          bool ok;
+          if (kDraft) {
+            const double qx = weight(held ? lane_value(qx_l, child) : s.qx[child]);
+            ok = u * (mm * qx) < left_of(px, aa, qx);
+            if (!ok) {
+              aa += mm;
+              old = 1;
+            }
+          } else {
+            bool spent = false;
+            for (int k = 0; k < ng; ++k) spent |= gone_of[k] == token;
+            ok = !spent && u * mm < px;
+            if (!ok && !spent) {
+              mm -= px;
+              if (lane == 0) gone_of[ng] = token;
+              __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+              ++ng;
+            }
+          }
           next = child + 1;
-          if (p.q) {
-            aa += mm;
-            state = 2;
+          if (ok) {
+            if (lane == 0 && c == 0) path[len] = child;
+            ++len;
+            node = child;
+            ng = 0;
+            aa = 0.0, mm = 1.0;
           }
         }
       }
       if (lane == 0) {
-        cur = c, at = next, gone = ng, path_len = len, done = state == 1;
+        cur = node, at = next, gone = ng, path_len = len, state = st, stale = 0;
         a = aa, mass = mm;
       }
     }
     __syncthreads();
-    if (done) break;
-    const float* pr = p.p + (q0 + cur) * p.ldp;
-    const float* qr = p.q + (q0 + cur) * p.ldq;
-    const double aa = a;
-    double sum = 0.0;
-    for (int64_t v = tid; v < V; v += kVerifyThreads) sum += row_weight(v, pr, qr, aa, 0);
-    sum = block_sum(sum);
+    // The sum of part k, the same bits whoever adds it up: first of this
+    // workgroup's own (at the end, its tiles' sums one by one), then, should the
+    // others not be seen to arrive, of each.
+    const bool end = state == 1;
+    const Row<kDraft> row{p.p + (q0 + cur) * p.ldp, kDraft ? p.q + (q0 + cur) * p.ldq : nullptr, a,
+                          gone_of, end ? gone : 0, static_cast<int>(p.vocab)};
+    double* round = partial + (arrivals & 1) * kParts;
+    ++arrivals;
+    bool alone = false;
+    double parts_l = 0.0;  // part `lane`
+    for (int k = c;;) {
+      double x = 0.0;
+      row.tiles(first_tile(k) + wave, first_tile(k + 1), kVerifyWaves, [&](int t, double y) {
+        x += y;
+        if (end && lane == 0) store_agent(tile_sums + t, y);
+      });
+      if (end) break;
+      __syncthreads();
+      if (lane == 0) part[wave] = x;
+      __syncthreads();
+      x = (part[0] + part[1]) + (part[2] + part[3]);
+      if (!alone) {
+        if (tid == 0) {
+          store_agent(round + c, x);
+          wave_stores_done();
+          int have = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT) + 1;
+          for (int64_t i = 0; have < arrivals * p.parts && i < p.spin_limit; ++i) {
+            __builtin_amdgcn_s_sleep(1);
+            have = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
+          seen = have >= arrivals * p.parts;
+        }
+        __syncthreads();
+        if (seen) {
+          parts_l = lane < p.parts ? load_agent(round + lane) : 0.0;
+          break;
+        }
+        alone = true;
+        k = 0;
+        continue;
+      }
+      if (k == lane) parts_l = x;
+      if (++k == p.parts) break;
+    }
+    if (end) break;
+    const double sum = wave_sum(parts_l);
+    __syncthreads();  // (everyone has read `mass` and the parts)
     if (tid == 0) mass = sum;
     __syncthreads();
   }
 
-  // the next token: sums of tiles of the row, the tile that holds it, its place
-  const float* pr = p.p + (q0 + cur) * p.ldp;
-  const float* qr = p.q ? p.q + (q0 + cur) * p.ldq : nullptr;
-  const int tiles_n = static_cast<int>((V + kTile - 1) / kTile);
-  double aa = a;
-  int ng = gone;
-  double total = 0.0;
-  for (int turn = 0; turn < 2; ++turn) {
-    for (int t = 0; t < tiles_n; ++t) {
-      double x = 0.0;
-      for (int k = 0; k < 4; ++k) {
-        const int64_t v = static_cast<int64_t>(t) * kTile + 4 * tid + k;
-        if (v < V) x += row_weight(v, pr, qr, aa, ng);
-      }
-      x = block_sum(x);
-      if (tid == 0) tiles[t] = x;
-    }
-    __syncthreads();
-    total = 0.0;
-    for (int t = 0; t < tiles_n; ++t) total += tiles[t];
-    if (total > 0.0) break;
-    qr = nullptr, ng = 0;  // nothing is left: the row itself
+  // the end of the walk: this part's tiles have been added up
+  if (c == 0) {
+    for (int j = path_len + tid; j < p.path_width; j += kVerifyThreads) path[j] = -1;
+    if (tid == 0) p.accept[r] = path_len;
   }
-  const double goal = p.u_final[r] * total;
-  double before = 0.0;
-  int tile = -1;
-  for (int t = 0; t < tiles_n && tile < 0; ++t) {
-    if (before + tiles[t] > goal) tile = t;
-    else before += tiles[t];
-  }
-  const bool beyond = tile < 0;  // by rounding: the last value that counts
-  for (int t = tiles_n - 1; t >= 0 && tile < 0; --t)
-    if (tiles[t] > 0.0) tile = t;
-  if (tid == 0) found = beyond ? -1 : INT32_MAX;
+  wave_stores_done();
   __syncthreads();
-  if (tile >= 0) {
-    double w[4], x = 0.0;
-    int last = -1;
-    const int64_t v0 = static_cast<int64_t>(tile) * kTile + 4 * tid;
-    for (int k = 0; k < 4; ++k) {
-      w[k] = v0 + k < V ? row_weight(v0 + k, pr, qr, aa, ng) : 0.0;
-      x += w[k];
-      if (w[k] > 0.0) last = static_cast<int>(v0 + k);
+  if (wave != 0) return;
+  int have = 0;
+  if (lane == 0)
+    have = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+  have = __builtin_amdgcn_readfirstlane(have);
+  if (have != arrivals * p.parts) return;
+  // The last to arrive, one wave of it: the tile where the running sum passes the
+  // goal, then the place in it.  Each lane takes a run of tiles, then of values;
+  // where rounding leaves none past the goal, it is the last one that counts.
+  if (lane == 0) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int run = (p.tiles + kWave - 1) / kWave;
+  const int t0 = min(lane * run, p.tiles), t1 = min(t0 + run, p.tiles);
+  auto next_token = [&](const Row<kDraft>& row, auto sum_of) -> int {
+    double x = 0.0;
+    for (int t = t0; t < t1; ++t) x += sum_of(t);
+    double incl = wave_prefix(x);
+    const double total = lane_value(incl, 63);
+    if (!(total > 0.0)) return -1;
+    const double goal = static_cast<double>(p.u_final[r]) * total;
+    unsigned long long past = __ballot(incl > goal && x > 0.0);
+    const unsigned long long some = __ballot(x > 0.0);
+    const bool beyond = past == 0;
+    int who = beyond ? 63 - __clzll(some) : __ffsll(past) - 1;
+    int tile = -1;
+    double below = incl - x;
+    if (lane == who) {
+      double sum = below;
+      for (int t = t0; t < t1; ++t) {
+        const double y = sum_of(t);
+        if (y > 0.0) {  // the last one that counts, or the first past the goal
+          tile = t;
+          below = sum;
+        }
+        sum += y;
+        if (!beyond && y > 0.0 && sum > goal) break;
+      }
     }
-    const double incl = wave_prefix(x);
-    if (lane == kWave - 1) part[wave] = incl;
-    __syncthreads();
-    double sum = before;
-    for (int k = 0; k < wave; ++k) sum += part[k];
-    sum += incl - x;
-    int first = INT32_MAX;
-    for (int k = 0; k < 4; ++k) {
+    tile = __builtin_amdgcn_readlane(tile, who);
+    below = lane_value(below, who);
+    const int v0 = tile * kTile + 16 * lane;
+    double w[16];
+    x = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Four pv = row.load(row.p, v0 + 4 * i);
+      row.weights(v0 + 4 * i, pv, kDraft ? row.load(row.q, v0 + 4 * i) : pv, w + 4 * i);
+      x += (w[4 * i] + w[4 * i + 1]) + (w[4 * i + 2] + w[4 * i + 3]);
+    }
+    incl = wave_prefix(x);
+    past = beyond ? 0 : __ballot(below + incl > goal && x > 0.0);
+    who = past ? __ffsll(past) - 1 : 63 - __clzll(__ballot(x > 0.0));
+    int token = -1;
+    bool done = false;
+    double sum = below + (incl - x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
       sum += w[k];
-      if (w[k] > 0.0 && sum > goal && first == INT32_MAX) first = static_cast<int>(v0 + k);
+      if (w[k] > 0.0 && !done) {
+        token = row.place(v0 + (k & ~3)) + (k & 3);
+        done = past != 0 && sum > goal;
+      }
     }
-    if (!beyond && first != INT32_MAX) atomicMin(&found, first);
-    __syncthreads();
-    if (found == INT32_MAX || found < 0) {  // rounding inside the tile: its last value
-      __syncthreads();
-      if (tid == 0) found = -1;
-      __syncthreads();
-      if (last >= 0) atomicMax(&found, last);
+    return __builtin_amdgcn_readlane(token, who);
+  };
+  Row<kDraft> row{p.p + (q0 + cur) * p.ldp, kDraft ? p.q + (q0 + cur) * p.ldq : nullptr, a,
+                  gone_of, gone, static_cast<int>(p.vocab)};
+  int token = -1;
+#pragma unroll 1
+  for (int turn = 0; token < 0 && turn < 2; ++turn) {
+    if (turn == 1) {  // nothing is left: the row itself
+      row.a = 0.0;
+      row.gone_n = 0;
+      row.tiles(0, p.tiles, 1, [&](int t, double y) {
+        if (lane == 0) store_agent(tile_sums + t, y);
+      });
+      wave_stores_done();
     }
-    __syncthreads();
+    token = next_token(row, [&](int t) { return load_agent(tile_sums + t); });
   }
-  if (tid == 0) {
-    p.next[r] = tile >= 0 ? found : -1;
-    p.accept[r] = path_len < p.path_width ? path_len : p.path_width;
-  }
+  if (lane == 0) p.next[r] = token;
+}
+
+constexpr int64_t kCounterRegion = int64_t{4} * kSpecMaxRequests;
+
+int tiles_of(int64_t vocab) { return static_cast<int>((vocab + kTile - 1) / kTile); }
+
+// Workgroups of a request: enough of them for four on every CU, each with at
+// least a tile a wave.  (64 requests of a 128256 vocabulary: 16.)
+int parts_of(int32_t bs, int64_t vocab) {
+  const int tiles = tiles_of(vocab);
+  int parts = bs < 1024 ? 1024 / bs : 1;
+  const int most = (tiles + kVerifyWaves - 1) / kVerifyWaves;
+  if (parts > most) parts = most;
+  if (parts > kParts) parts = kParts;
+  return parts;
 }
 
 }  // namespace
 
 int64_t verify_workspace_bytes(int32_t bs, int64_t vocab) {
-  (void)bs;
-  (void)vocab;
-  return 0;
+  if (bs <= 0 || vocab <= 0) return 0;
+  // the counters lie in a fixed region, apart from any call's sums
+  return kCounterRegion + static_cast<int64_t>(bs) * 8 * (2 * kParts + tiles_of(vocab));
 }
 
-hipError_t launch_verify(const VerifyParams& p, hipStream_t stream) {
-  verify_kernel<<<dim3(p.bs), dim3(kVerifyThreads), 0, stream>>>(p);
+hipError_t launch_verify(VerifyParams p, hipStream_t stream) {
+  p.parts = parts_of(p.bs, p.vocab);
+  p.tiles = tiles_of(p.vocab);
+  p.counters = static_cast<int32_t*>(p.workspace);
+  p.partials = reinterpret_cast<double*>(static_cast<char*>(p.workspace) + kCounterRegion);
+  p.tile_sums = p.partials + static_cast<int64_t>(p.bs) * 2 * kParts;
+  if (p.q) verify_kernel<true><<<dim3(p.bs * p.parts), dim3(kVerifyThreads), 0, stream>>>(p);
+  else verify_kernel<false><<<dim3(p.bs * p.parts), dim3(kVerifyThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -18,6 +18,7 @@
 #define SIG_spec_attention_workspace_bytes "iiiiiil"
 #define SIG_spec_attention "pllplliippliipppilpifppilplp"
 #define SIG_spec_verify_workspace_bytes "il"
+#define SIG_spec_set_option "pl"
 #define SIG_spec_verify "pppilplpllppplippplp"
 
 static PyObject* py_spec_kv_resize(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -95,6 +96,12 @@ static PyObject* py_spec_verify(PyObject* self, PyObject* const* args, Py_ssize_
       L(18), P(19)));
 }
 
+static PyObject* py_spec_set_option(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_set_option);
+  RETURN_INT(spec_set_option(
+      (const char*)P(0), L(1)));
+}
+
 static PyMethodDef methods[] = {
     ENTRY(spec_kv_resize),
     ENTRY(spec_kv_fork),
@@ -106,6 +113,7 @@ static PyMethodDef methods[] = {
     ENTRY(spec_attention),
     ENTRY(spec_verify_workspace_bytes),
     ENTRY(spec_verify),
+    ENTRY(spec_set_option),
     {NULL, NULL, 0, NULL},
 };
 
@@ -130,6 +138,7 @@ PyMODINIT_FUNC PyInit__sggspec(void) {
       {"spec_attention", SIG_spec_attention},
       {"spec_verify_workspace_bytes", SIG_spec_verify_workspace_bytes},
       {"spec_verify", SIG_spec_verify},
+      {"spec_set_option", SIG_spec_set_option},
   };
   int bad = sigs == NULL;
   for (size_t i = 0; !bad && i < sizeof(table) / sizeof(table[0]); ++i) {

@@ -328,6 +328,14 @@ def spec_verify(tokens, parents, q_indptr, target_probs, uniforms, final_uniform
     return path, accept, nxt
 
 
+def spec_set_option(name, value):
+    """Process-wide setting ("verify_spin_limit": polls); returns the previous value."""
+    old = spec_calls().spec_set_option(name.encode() + b"\0", int(value))
+    if old < 0:
+        raise ValueError(f"unknown option {name!r} or negative value {value}")
+    return old
+
+
 class PagedKVCache:
     """Keys and values of ``num_layers`` layers in pages, with the page tables of ``max_rows``
     sequences, all on the device.
@@ -396,4 +404,5 @@ class PagedKVCache:
 
 
 __all__ = ["PagedKVCache", "spec_attention", "spec_kv_compact", "spec_kv_copy_pages",
-           "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_tree_mask", "spec_verify"]
+           "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_set_option", "spec_tree_mask",
+           "spec_verify"]

@@ -178,9 +178,20 @@ def verify(tokens=F, parents=F, ind=F, bs=2, n=8, p=F, ldp=100, q=F, ldq=100, V=
     (dict(V=0), -2, "vocab"), (dict(V=(1 << 22) + 1, ldp=1 << 23, ldq=1 << 23), -2, "vocab"),
     (dict(ldp=99), -1, "ld_target"), (dict(ldq=99), -1, "ld_draft"), (dict(w=0), -1, "path_width"),
     (dict(w=5), -1, "path_width"), (dict(ind=0), -1, "q_indptr"), (dict(path=0), -1, "path"),
-    (dict(p=0), -1, "target_probs"), (dict(u=0), -1, "uniforms"), (dict(uf=0), -1, "final")])
+    (dict(p=0), -1, "target_probs"), (dict(u=0), -1, "uniforms"), (dict(uf=0), -1, "final"),
+    (dict(V=50000, ldp=50000, ldq=50000, ws=0), -1, "workspace"),
+    (dict(V=50000, ldp=50000, ldq=50000, wsb=16), -3, "workspace"),
+    (dict(V=50000, ldp=50000, ldq=50000, ws=F + 8), -2, "aligned")])
 def test_verify_refused(kw, code, text):
     assert verify(**kw) == code and text in _err()
+
+
+def test_set_option():
+    old = sgg.spec_set_option("verify_spin_limit", 7)
+    assert sgg.spec_set_option("verify_spin_limit", old) == 7
+    for name, value in (("spin", 1), ("verify_spin_limit", -1)):
+        with pytest.raises(ValueError):
+            sgg.spec_set_option(name, value)
 
 
 def test_empty_batches_are_nothing_to_do():

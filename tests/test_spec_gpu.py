@@ -447,7 +447,7 @@ def _verify_want(c, width=None):
         counts.append(len(path))
         nxt.append(x)
         at += n
-    return paths, counts, nxt
+    return (paths, counts, nxt)
 
 
 def _verify_check(c, width=None):
@@ -532,6 +532,32 @@ def test_verify_path_width_ends_the_walk():
     c["u"][:] = 0.0                                       # every candidate with mass is taken
     for w in (1, 2, 5, 10, 14):
         assert _verify_check(c, w) == [min(w, 10)]
+
+
+def test_verify_waits_end_without_the_others():
+    """With no poll allowed, every workgroup adds up its request's parts by itself: the same
+    results, and the same again afterwards (the counters are back at zero)."""
+    sgg = _sgg()
+    c = [_verify_case([9, 4, 12], 9000 + i, True, i, spread=2.0) for i in range(6)]
+    want = [tuple(x.tolist() for x in _verify_call(x)) for x in c]
+    assert want == [_verify_want(x) for x in c]
+    old = sgg.spec_set_option("verify_spin_limit", 0)
+    try:
+        for x, w in zip(c, want):
+            assert tuple(y.tolist() for y in _verify_call(x)) == w
+    finally:
+        sgg.spec_set_option("verify_spin_limit", old)
+    for x, w in zip(c, want):
+        assert tuple(y.tolist() for y in _verify_call(x)) == w
+
+
+@pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("bs", [1, 3, 300])
+def test_verify_batch_sizes(drawn, bs):
+    """One request over many workgroups, and more requests than workgroups."""
+    ql = [int(x) for x in np.random.default_rng(bs).integers(1, 9, bs)]
+    for seed in range(3):
+        _verify_check(_verify_case(ql, 30011 if bs < 10 else 1500, drawn, seed, spread=3.0))
 
 
 def test_verify_strided_rows_and_graph():
