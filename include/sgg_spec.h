@@ -197,7 +197,8 @@ int spec_attention(const void* q, int64_t q_token, int64_t q_head, void* out, in
  *   0 first, then -1; accept_lens [bs]: how many (path_width at most: the walk
  *   ends there); next_tokens [bs].  A request of no tokens gets 0 and -1.
  *   workspace: spec_verify_workspace_bytes(), 16-byte aligned, zero on first
- *   use (each call leaves its counters at zero), not shared by overlapping calls.
+ *   use (each call leaves its counters at zero), not shared by overlapping calls;
+ *   spec_attention() and spec_verify() may use the same one in turn.
  */
 int64_t spec_verify_workspace_bytes(int32_t bs, int64_t vocab);
 int spec_verify(const int32_t* tokens, const int32_t* parents, const int32_t* q_indptr,

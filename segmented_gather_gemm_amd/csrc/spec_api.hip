@@ -341,7 +341,7 @@ namespace {
 
 int64_t attention_bytes(const sgg::AttnShape& s) {
   // the counters; per slot block_rows rows of padded_dim floats and of (maximum, sum)
-  return s.slots ? sgg::kJoinBytes + s.slots * s.block_rows * (s.padded_dim * 4 + 8) : 0;
+  return s.slots ? sgg::kSpecZeroBytes + s.slots * s.block_rows * (s.padded_dim * 4 + 8) : 0;
 }
 
 int check_heads(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
@@ -432,8 +432,8 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.counters = static_cast<int32_t*>(workspace);
-  p.part = static_cast<char*>(workspace) + sgg::kJoinBytes;
-  p.part_bytes = static_cast<uint32_t>(need - (need ? sgg::kJoinBytes : 0));
+  p.part = static_cast<char*>(workspace) + sgg::kSpecZeroBytes;
+  p.part_bytes = static_cast<uint32_t>(need - (need ? sgg::kSpecZeroBytes : 0));
   p.num_tokens = num_tokens;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.bs = bs;

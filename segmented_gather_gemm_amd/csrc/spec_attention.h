@@ -12,10 +12,8 @@ namespace sgg {
 // The chunks of a unit are joined in groups of kJoin, level by level.
 constexpr int kJoin = 32;
 constexpr int kJoinLevels = 2;  // up to 1024 chunks
-// Arrival counters lie in a fixed region at the start of the workspace, so
-// that they never share memory with another call's partial results.
 constexpr int kJoinSlots = 32768;
-constexpr int64_t kJoinBytes = int64_t{4} * kJoinLevels * kJoinSlots;
+static_assert(int64_t{4} * kJoinLevels * kJoinSlots <= kSpecJoinBytes, "region too small");
 
 struct AttnParams {
   const char* q;

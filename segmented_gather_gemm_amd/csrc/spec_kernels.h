@@ -9,6 +9,15 @@ namespace sgg {
 
 constexpr int kSpecMaxRequests = 4096;  // SPEC_MAX_REQUESTS
 
+// What is zero between calls (arrival counters, the slots of a meeting's sums)
+// lies in a fixed region at the start of a workspace, attention's and then the
+// verification's, and partial results behind it: calls of both kinds and of any
+// sizes may follow one another on one workspace.
+constexpr int kSpecVerifyParts = 1024;  // workgroups of a verification that meet at sums
+constexpr int64_t kSpecJoinBytes = int64_t{4} * 2 * 32768;
+constexpr int64_t kSpecZeroBytes =
+    kSpecJoinBytes + 4 * kSpecMaxRequests + int64_t{8} * 3 * kSpecVerifyParts;
+
 // A paged cache with its strides in bytes.
 struct KvView {
   char* k;
@@ -114,7 +123,7 @@ struct VerifyParams {
   // set by launch_verify
   int32_t parts, tiles;  // workgroups, tiles of a row
   int32_t* counters;     // [SPEC_MAX_REQUESTS], zero between calls
-  double* partials;      // [bs][2][64]
+  double* partials;      // [bs][3][parts], zero between calls
   double* tile_sums;     // [bs][tiles]
 };
 int64_t verify_workspace_bytes(int32_t bs, int64_t vocab);

@@ -10,11 +10,12 @@
 // A row is cut among the workgroups of its request, so that a batch of few
 // requests uses the whole memory system; all of them walk the tree, each for
 // itself (the same steps on the same numbers), and meet where a sum over the
-// row is needed: each leaves its part's sum in the workspace, counts itself,
-// and waits until the count says that all parts are there.  A wait is bounded:
-// one that sees no end adds up the other parts itself, in the same order.  At
-// the end each leaves the sums of its tiles of 1024 values, and one wave of the
-// last to arrive finds the tile and the place in it.
+// row is needed: each leaves its part's sum in the workspace and reads the
+// others' until all are there.  A wait is bounded: one that sees no end adds up
+// the other parts itself, in the same order.  A wave keeps the values of its
+// first tiles in registers while the walk stays at a node.  At the end each
+// leaves the sums of its tiles of 1024 values and counts itself, and one wave of
+// the last to arrive finds the tile and the place in it.
 //
 // Sums and comparisons are in 64 bits.  The values that come out are whole
 // numbers: in 32 bits, a sum over a vocabulary moves a border by 1e-7 or so,
@@ -35,6 +36,7 @@ constexpr int kVerifyWaves = kVerifyThreads / kWave;
 constexpr int kVerifyNodes = 1024;  // nodes of a request that are visited
 constexpr int kTile = 1024;         // values of a tile: 16 a lane of one wave
 constexpr int kParts = 64;          // workgroups of a request at most
+constexpr int kHold = 2;            // tiles whose values a wave keeps
 
 // The value that lane (l - n) holds, by a shift within 16 lanes or a broadcast
 // of the last lane of one row of 16 (or two) to the next, 0 where there is none:
@@ -124,37 +126,32 @@ struct Row {
       }
     }
   }
-  // This wave's tiles first, first + step, .. below `stop`: use(t, sum of tile t).
-  // The next tile's values are under way while the sum of one is taken.
-  template <class Use>
-  __device__ __forceinline__ void tiles(int first, int stop, int step, const Use& use) const {
-    Four pv[4], qv[4];
-    const int lane4 = 4 * (threadIdx.x % kWave);
-    auto fetch = [&](int t) {
+  // A lane's values of a tile, and the tile's sum.
+  struct Held {
+    Four p[4], q[kDraft ? 4 : 1];
+  };
+  __device__ __forceinline__ void fetch(int t, Held* f) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pv[i] = load(p, t * kTile + i * 256 + lane4);
-        if (kDraft) qv[i] = load(q, t * kTile + i * 256 + lane4);
-      }
-    };
-    if (first < stop) fetch(first);
-#pragma unroll 1
-    for (int t = first; t < stop; t += step) {
-      double s = 0.0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        double w[4];
-        weights(t * kTile + i * 256 + lane4, pv[i], kDraft ? qv[i] : pv[i], w);
-        s += (w[0] + w[1]) + (w[2] + w[3]);
-      }
-      if (t + step < stop) fetch(t + step);
-      use(t, wave_sum(s));
+    for (int i = 0; i < 4; ++i) {
+      const int v = t * kTile + i * 256 + 4 * (threadIdx.x % kWave);
+      f->p[i] = load(p, v);
+      if (kDraft) f->q[i] = load(q, v);
     }
+  }
+  __device__ __forceinline__ double sum_of(int t, const Held& f) const {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      double w[4];
+      weights(t * kTile + i * 256 + 4 * (threadIdx.x % kWave), f.p[i], f.q[kDraft ? i : 0], w);
+      s += (w[0] + w[1]) + (w[2] + w[3]);
+    }
+    return wave_sum(s);
   }
 };
 
 template <bool kDraft>
-__global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams p) {
+__global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(VerifyParams p) {
   __shared__ struct {
     int32_t parent[kVerifyNodes];
     int32_t token[kVerifyNodes];
@@ -166,6 +163,7 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
   __shared__ double part[kVerifyWaves];
   __shared__ int cur, at, gone, path_len, state, stale, seen;
   __shared__ double a, mass;
+  __shared__ double parts_of_round[kWave];
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = blockIdx.x / p.parts, c = blockIdx.x % p.parts;
@@ -175,7 +173,7 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
                     ? 0
                     : static_cast<int>(q1 - q0 < kVerifyNodes ? q1 - q0 : kVerifyNodes);
   int32_t* counter = p.counters + r;
-  double* partial = p.partials + static_cast<int64_t>(r) * 2 * kParts;
+  double* partial = p.partials + static_cast<int64_t>(r) * 3 * p.parts;
   double* tile_sums = p.tile_sums + static_cast<int64_t>(r) * p.tiles;
   if (n == 0) {
     if (c == 0) {
@@ -209,7 +207,10 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
   // the tiles of part k are [first_tile(k), first_tile(k + 1))
   const int per = (p.tiles + p.parts - 1) / p.parts;
   auto first_tile = [&](int k) { return min(k * per, p.tiles); };
-  int arrivals = 0;  // of each workgroup of the request so far
+  int rounds = 0;      // sums of the row so far
+  bool alone = p.parts == 1;  // adds up every part itself, from the first wait that saw no end
+  int held_node = -1;  // the node whose values `held` has
+  typename Row<kDraft>::Held held[kHold];
   while (true) {
     // wave 0 walks on until a rejection needs the residual's mass, or the end
     if (wave == 0) {
@@ -282,44 +283,78 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
     const bool end = state == 1;
     const Row<kDraft> row{p.p + (q0 + cur) * p.ldp, kDraft ? p.q + (q0 + cur) * p.ldq : nullptr, a,
                           gone_of, end ? gone : 0, static_cast<int>(p.vocab)};
-    double* round = partial + (arrivals & 1) * kParts;
-    ++arrivals;
-    bool alone = false;
+    // Slots of parts' sums, three rounds in turn; a sum lies there negated, so
+    // that 0 is "not there".  The next round's slot is emptied before this round's
+    // is filled: whoever has seen this round's sums sees that one empty.  (Its
+    // last readers are done: they have filled the last round's slots since.)  A
+    // workgroup that is alone fills none, so nobody meets a later round's sum.
+    double* round = partial + (rounds % 3) * p.parts;
+    if (!end && !alone && tid == 0) store_agent(partial + (rounds + 1) % 3 * p.parts + c, 0.0);
+    ++rounds;
+    if (held_node != cur) {
+#pragma unroll
+      for (int k = 0; k < kHold; ++k)
+        if (first_tile(c) + wave + k * kVerifyWaves < first_tile(c + 1))
+          row.fetch(first_tile(c) + wave + k * kVerifyWaves, &held[k]);
+      held_node = cur;
+    }
     double parts_l = 0.0;  // part `lane`
-    for (int k = c;;) {
+    const int own = c;
+    for (int k = alone && !end ? 0 : own;;) {
       double x = 0.0;
-      row.tiles(first_tile(k) + wave, first_tile(k + 1), kVerifyWaves, [&](int t, double y) {
+      auto use = [&](int t, double y) {
         x += y;
         if (end && lane == 0) store_agent(tile_sums + t, y);
-      });
+      };
+      const int stop = first_tile(k + 1);
+      int t = first_tile(k) + wave;
+      if (k == own) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+          if (t < stop) use(t, row.sum_of(t, held[i]));
+          t += kVerifyWaves;
+        }
+      }
+#pragma unroll 1
+      for (; t < stop; t += kVerifyWaves) {
+        typename Row<kDraft>::Held f;
+        row.fetch(t, &f);
+        use(t, row.sum_of(t, f));
+      }
       if (end) break;
       __syncthreads();
       if (lane == 0) part[wave] = x;
       __syncthreads();
       x = (part[0] + part[1]) + (part[2] + part[3]);
-      if (!alone) {
-        if (tid == 0) {
-          store_agent(round + c, x);
-          wave_stores_done();
-          int have = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED,
-                                            __HIP_MEMORY_SCOPE_AGENT) + 1;
-          for (int64_t i = 0; have < arrivals * p.parts && i < p.spin_limit; ++i) {
-            __builtin_amdgcn_s_sleep(1);
-            have = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          }
-          seen = have >= arrivals * p.parts;
-        }
-        __syncthreads();
-        if (seen) {
-          parts_l = lane < p.parts ? load_agent(round + lane) : 0.0;
-          break;
-        }
-        alone = true;
-        k = 0;
+      if (alone) {
+        if (k == lane) parts_l = x;
+        if (++k == p.parts) break;
         continue;
       }
-      if (k == lane) parts_l = x;
-      if (++k == p.parts) break;
+      if (wave == 0) {
+        if (lane == 0) {
+          wave_stores_done();
+          store_agent(round + c, -x);
+        }
+        const unsigned long long all = p.parts < kWave ? (1ull << p.parts) - 1ull : ~0ull;
+        unsigned long long there = 0;
+        double y = lane == c ? -x : 0.0;
+        for (int64_t i = 0;; ++i) {
+          if (lane < p.parts && lane != c) y = load_agent(round + lane);
+          there = __ballot(__builtin_bit_cast(uint64_t, y) != 0) & all;
+          if (there == all || i >= p.spin_limit) break;
+          __builtin_amdgcn_s_sleep(1);
+        }
+        parts_of_round[lane] = y;
+        if (lane == 0) seen = there == all;
+      }
+      __syncthreads();
+      if (seen) {
+        parts_l = lane < p.parts ? -parts_of_round[lane] : 0.0;
+        break;
+      }
+      alone = true;
+      k = 0;
     }
     if (end) break;
     const double sum = wave_sum(parts_l);
@@ -340,16 +375,25 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
   if (lane == 0)
     have = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
   have = __builtin_amdgcn_readfirstlane(have);
-  if (have != arrivals * p.parts) return;
+  if (have != p.parts) return;
   // The last to arrive, one wave of it: the tile where the running sum passes the
   // goal, then the place in it.  Each lane takes a run of tiles, then of values;
   // where rounding leaves none past the goal, it is the last one that counts.
+  // (The counter and the slots of the sums are left at zero for the next call.)
   if (lane == 0) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (kDraft && p.parts > 1)
+    for (int i = lane; i < 3 * p.parts; i += kWave) store_agent(partial + i, 0.0);
   const int run = (p.tiles + kWave - 1) / kWave;
   const int t0 = min(lane * run, p.tiles), t1 = min(t0 + run, p.tiles);
-  auto next_token = [&](const Row<kDraft>& row, auto sum_of) -> int {
-    double x = 0.0;
-    for (int t = t0; t < t1; ++t) x += sum_of(t);
+  auto next_token = [&](const Row<kDraft>& row) -> int {
+    constexpr int kRun = 4;  // sums of a lane in registers (a vocabulary of 262144)
+    double first[kRun], x = 0.0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) first[i] = t0 + i < t1 ? load_agent(tile_sums + t0 + i) : 0.0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) x += first[i];
+#pragma unroll 1
+    for (int t = t0 + kRun; t < t1; ++t) x += load_agent(tile_sums + t);
     double incl = wave_prefix(x);
     const double total = lane_value(incl, 63);
     if (!(total > 0.0)) return -1;
@@ -360,17 +404,21 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
     int who = beyond ? 63 - __clzll(some) : __ffsll(past) - 1;
     int tile = -1;
     double below = incl - x;
-    if (lane == who) {
+    if (lane == who) {  // the last tile that counts, or the first past the goal
       double sum = below;
-      for (int t = t0; t < t1; ++t) {
-        const double y = sum_of(t);
-        if (y > 0.0) {  // the last one that counts, or the first past the goal
+      bool done = false;
+      auto take = [&](int t, double y) {
+        if (y > 0.0 && !done) {
           tile = t;
           below = sum;
+          done = !beyond && sum + y > goal;
         }
         sum += y;
-        if (!beyond && y > 0.0 && sum > goal) break;
-      }
+      };
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) take(t0 + i, first[i]);
+#pragma unroll 1
+      for (int t = t0 + kRun; t < t1 && !done; ++t) take(t, load_agent(tile_sums + t));
     }
     tile = __builtin_amdgcn_readlane(tile, who);
     below = lane_value(below, who);
@@ -407,26 +455,27 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void verify_kernel(VerifyParams 
     if (turn == 1) {  // nothing is left: the row itself
       row.a = 0.0;
       row.gone_n = 0;
-      row.tiles(0, p.tiles, 1, [&](int t, double y) {
+      for (int t = 0; t < p.tiles; ++t) {
+        typename Row<kDraft>::Held f;
+        row.fetch(t, &f);
+        const double y = row.sum_of(t, f);
         if (lane == 0) store_agent(tile_sums + t, y);
-      });
+      }
       wave_stores_done();
     }
-    token = next_token(row, [&](int t) { return load_agent(tile_sums + t); });
+    token = next_token(row);
   }
   if (lane == 0) p.next[r] = token;
 }
 
-constexpr int64_t kCounterRegion = int64_t{4} * kSpecMaxRequests;
-
 int tiles_of(int64_t vocab) { return static_cast<int>((vocab + kTile - 1) / kTile); }
 
-// Workgroups of a request: enough of them for four on every CU, each with at
-// least a tile a wave.  (64 requests of a 128256 vocabulary: 16.)
-int parts_of(int32_t bs, int64_t vocab) {
-  const int tiles = tiles_of(vocab);
-  int parts = bs < 1024 ? 1024 / bs : 1;
-  const int most = (tiles + kVerifyWaves - 1) / kVerifyWaves;
+// Workgroups of a request: for all of them four on a CU, or two that hold a
+// wave's tiles of two rows in registers, each with at least a tile a wave.
+int parts_of(int32_t bs, int64_t vocab, bool draft) {
+  const int budget = draft ? kSpecVerifyParts / 2 : kSpecVerifyParts;
+  int parts = bs < budget ? budget / bs : 1;
+  const int most = (tiles_of(vocab) + kVerifyWaves - 1) / kVerifyWaves;
   if (parts > most) parts = most;
   if (parts > kParts) parts = kParts;
   return parts;
@@ -436,16 +485,16 @@ int parts_of(int32_t bs, int64_t vocab) {
 
 int64_t verify_workspace_bytes(int32_t bs, int64_t vocab) {
   if (bs <= 0 || vocab <= 0) return 0;
-  // the counters lie in a fixed region, apart from any call's sums
-  return kCounterRegion + static_cast<int64_t>(bs) * 8 * (2 * kParts + tiles_of(vocab));
+  return kSpecZeroBytes + static_cast<int64_t>(bs) * 8 * tiles_of(vocab);
 }
 
 hipError_t launch_verify(VerifyParams p, hipStream_t stream) {
-  p.parts = parts_of(p.bs, p.vocab);
+  p.parts = parts_of(p.bs, p.vocab, p.q != nullptr);
   p.tiles = tiles_of(p.vocab);
-  p.counters = static_cast<int32_t*>(p.workspace);
-  p.partials = reinterpret_cast<double*>(static_cast<char*>(p.workspace) + kCounterRegion);
-  p.tile_sums = p.partials + static_cast<int64_t>(p.bs) * 2 * kParts;
+  char* zero = static_cast<char*>(p.workspace) + kSpecJoinBytes;
+  p.counters = reinterpret_cast<int32_t*>(zero);
+  p.partials = reinterpret_cast<double*>(zero + 4 * kSpecMaxRequests);
+  p.tile_sums = reinterpret_cast<double*>(static_cast<char*>(p.workspace) + kSpecZeroBytes);
   if (p.q) verify_kernel<true><<<dim3(p.bs * p.parts), dim3(kVerifyThreads), 0, stream>>>(p);
   else verify_kernel<false><<<dim3(p.bs * p.parts), dim3(kVerifyThreads), 0, stream>>>(p);
   return hipGetLastError();

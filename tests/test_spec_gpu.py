@@ -426,14 +426,15 @@ def _verify_case(ql, V, drawn, seed, chain=False, spread=5.0, flat=False):
     return dict(ql=ql, trees=trees, tokens=tokens, p=p, q=q if drawn else None, u=u, uf=uf)
 
 
-def _verify_call(c, width=None):
+def _verify_call(c, width=None, workspace=None):
     sgg = _sgg()
     par = np.concatenate([np.asarray(t, np.int64) for t in c["trees"]] or [np.zeros(0)])
     return sgg.spec_verify(
         _i32(c["tokens"]), _i32(par), _i32(np.concatenate([[0], np.cumsum(c["ql"])])),
         torch.from_numpy(c["p"]).to(DEV), torch.from_numpy(c["u"]).to(DEV),
         torch.from_numpy(c["uf"]).to(DEV), width or max(max(c["ql"]), 1),
-        draft_probs=None if c["q"] is None else torch.from_numpy(c["q"]).to(DEV))
+        draft_probs=None if c["q"] is None else torch.from_numpy(c["q"]).to(DEV),
+        workspace=workspace)
 
 
 def _verify_want(c, width=None):
@@ -450,8 +451,8 @@ def _verify_want(c, width=None):
     return (paths, counts, nxt)
 
 
-def _verify_check(c, width=None):
-    path, count, nxt = _verify_call(c, width)
+def _verify_check(c, width=None, workspace=None):
+    path, count, nxt = _verify_call(c, width, workspace)
     want = _verify_want(c, width)
     assert path.tolist() == want[0]
     assert count.tolist() == want[1]
@@ -558,6 +559,24 @@ def test_verify_batch_sizes(drawn, bs):
     ql = [int(x) for x in np.random.default_rng(bs).integers(1, 9, bs)]
     for seed in range(3):
         _verify_check(_verify_case(ql, 30011 if bs < 10 else 1500, drawn, seed, spread=3.0))
+
+
+def test_attention_and_verify_share_a_workspace():
+    """Calls of both kinds in turn on one workspace: what has to be zero for one is not where
+    the other leaves its partial results."""
+    sgg = _sgg()
+    s = Setup([40001, 700], [3, 2], 2, 1, 64, ps=64, trees=[tree(3, None, True), tree(2, None, True)],
+              seed=4)
+    want = s.call()
+    s.check(want)
+    many = _verify_case([int(x) for x in np.random.default_rng(1).integers(1, 5, 300)], 1500, True,
+                        5, spread=3.0)
+    few = _verify_case([9, 4, 12], 30011, True, 6, spread=2.0)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for c in (many, few):
+            _verify_check(c, workspace=ws)
+            assert torch.equal(s.call(workspace=ws), want)
 
 
 def test_verify_strided_rows_and_graph():
