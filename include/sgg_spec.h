@@ -80,7 +80,8 @@ int spec_kv_resize(int32_t* page_table, int64_t ld_table, int32_t max_pages, int
  * spec_kv_fork -- row dst_rows[i] gets the kv_lens[src] tokens of row
  * src_rows[i]: the full pages are shared (count + 1), the partial last page is
  * copied into a fresh one in every layer, so that both rows may go on.  A dst
- * row has to hold no page and must not be a src row of the same call.
+ * row has to hold no page and must be neither a dst twice nor a src row of the
+ * same call.
  *   workspace: 12 * n bytes.  status as above: [0] pages missing (then nothing
  *   was done), [1] pairs left alone (row out of range or equal, dst not empty,
  *   src holding fewer pages than its length needs).

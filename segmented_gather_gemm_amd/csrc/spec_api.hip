@@ -248,7 +248,7 @@ extern "C" int spec_kv_copy_pages(const SpecKvCache* cache, const int32_t* src_p
   SGG_CHECK(src_pages && dst_pages, SGG_ERR_INVALID, "src_pages or dst_pages is NULL");
   SGG_CHECK(n <= INT32_MAX / (2 * static_cast<int64_t>(v.layers)), SGG_ERR_UNSUPPORTED,
             "%" PRId64 " pages of %d layers are above the grid", n, v.layers);
-  return launch_status(sgg::launch_kv_copy(v, src_pages, dst_pages, nullptr, n,
+  return launch_status(sgg::launch_kv_copy(v, src_pages, dst_pages, n,
                                            static_cast<hipStream_t>(stream)),
                        "kv_copy_pages");
 }

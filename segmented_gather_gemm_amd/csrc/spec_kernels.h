@@ -58,15 +58,14 @@ struct ForkParams {
   const int32_t* src;
   const int32_t* dst;
   int32_t* status;
-  int32_t* list;  // [3][n]: source page, destination page, tokens (0: nothing)
+  int32_t* list;  // [3][n]: partial page, its copy, length (-1: left alone)
   int64_t num_pages;
   int32_t n, page_shift;
 };
 hipError_t launch_kv_fork(const ForkParams& p, const KvView& c, hipStream_t stream);
 
-// tokens null: whole pages.
-hipError_t launch_kv_copy(const KvView& c, const int32_t* src, const int32_t* dst,
-                          const int32_t* tokens, int64_t n, hipStream_t stream);
+hipError_t launch_kv_copy(const KvView& c, const int32_t* src, const int32_t* dst, int64_t n,
+                          hipStream_t stream);
 
 struct WriteParams {
   const char* k;

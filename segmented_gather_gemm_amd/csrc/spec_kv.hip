@@ -5,9 +5,8 @@
 // Page state is a table of page ids per cache row and a count per page; a free
 // page is one whose count is not positive.  There is no free list to keep in
 // step with the counts: taking pages scans the counts for the lowest free ids,
-// a prefix sum over 4096 counts at a time, which one workgroup does in about a
-// microsecond for a pool of a few thousand pages, and giving back is one
-// atomic per page in any order.  The result is the same on every run.
+// up to 32 a thread of one workgroup, and giving back is one atomic per page in
+// any order.  The result is the same on every run.
 #include "sgg_device.h"
 #include "spec_kernels.h"
 
@@ -19,6 +18,15 @@ constexpr int kPoolWaves = kPoolThreads / kWave;
 
 __device__ __forceinline__ int load_agent(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// A store past the L2.  Of what is written once and read much later nothing is
+// gained by a place there, and what lies there unwritten at a kernel's end is
+// written then, while nothing else runs: 16384 workgroups that copy 268 MB take
+// 61 us with these stores and 97 with plain ones, the moves of 29 MB 9.4 and 22.
+__device__ __forceinline__ void store_past(char* p, const uint4& v) {
+  typedef uint32_t Words __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(__builtin_bit_cast(Words, v), reinterpret_cast<Words*>(p));
 }
 
 // Cache row of request i, or -1.
@@ -61,48 +69,57 @@ __device__ int block_prefix(int v, int* scratch, int* total) {
   return before + x - v;
 }
 
-// The free pages among ids [4096 b + 4 t, + 4) as bits, for thread t.
-__device__ __forceinline__ int free_bits(const int32_t* refs, int64_t num_pages, int64_t base) {
-  const int64_t id = base + 4 * threadIdx.x;
-  int bits = 0;
+// The free pages among ids [base + per t, + per) as bits, for thread t.
+constexpr int kScanIds = 32;
+__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t num_pages,
+                                              int64_t base, int per) {
+  const int64_t id = base + static_cast<int64_t>(per) * threadIdx.x;
+  uint32_t bits = 0;
+  for (int k = 0; k < per; k += 4) {
+    int v[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (id + k < num_pages && load_agent(refs + id + k) <= 0) bits |= 1 << k;
+    for (int j = 0; j < 4; ++j) v[j] = id + k + j < num_pages ? load_agent(refs + id + k + j) : 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bits |= static_cast<uint32_t>(v[j] <= 0) << (k + j);
+  }
   return bits;
 }
 
-// Whether `want` pages are free: the number missing.
-__device__ int pages_missing(const int32_t* refs, int64_t num_pages, int want, int* scratch) {
-  int found = 0;
-  for (int64_t base = 0; base < num_pages && found < want; base += 4 * kPoolThreads) {
-    int total;
-    block_prefix(__popc(free_bits(refs, num_pages, base)), scratch, &total);
-    found += total;
-  }
-  return found < want ? want - found : 0;
-}
-
-// Hands the lowest `want` free pages out: take(rank, page) for each.
+// Hands the lowest `want` free pages out, take(rank, page) for each, or none if
+// fewer are free; returns the number missing.  A thread looks at up to 32 ids
+// that follow one another, so a pool of 32768 pages takes one scan and one
+// prefix; a larger one is counted first, if its first 32768 do not suffice.
 template <class Take>
-__device__ void take_pages(int32_t* refs, int64_t num_pages, int want, int* scratch,
-                           const Take& take) {
-  int found = 0;
-  for (int64_t base = 0; base < num_pages && found < want; base += 4 * kPoolThreads) {
-    const int bits = free_bits(refs, num_pages, base);
-    int total;
-    int rank = found + block_prefix(__popc(bits), scratch, &total);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (bits >> k & 1) {
-        if (rank < want) {
-          const int64_t page = base + 4 * threadIdx.x + k;
-          refs[page] = 1;
-          take(rank, static_cast<int32_t>(page));
-        }
-        ++rank;
-      }
+__device__ int take_pages(int32_t* refs, int64_t num_pages, int want, int* scratch,
+                          const Take& take) {
+  const int64_t share = (num_pages + kPoolThreads - 1) / kPoolThreads;
+  const int per = share < kScanIds ? (static_cast<int>(share) + 3) & ~3 : kScanIds;
+  const int64_t step = static_cast<int64_t>(per) * kPoolThreads;
+  uint32_t bits = free_bits(refs, num_pages, 0, per);
+  int total;
+  int rank = block_prefix(__popc(bits), scratch, &total);
+  int found = total;
+  for (int64_t base = step; base < num_pages && found < want; base += step) {
+    int more;
+    block_prefix(__popc(free_bits(refs, num_pages, base, per)), scratch, &more);
+    found += more;
+  }
+  if (found < want) return want - found;
+  int64_t base = 0;
+  for (int before = 0;;) {
+    int64_t page = base + static_cast<int64_t>(per) * threadIdx.x;
+    for (; bits && rank < want; bits >>= 1, ++page) {
+      const int skip = __builtin_ctz(bits);
+      bits >>= skip;
+      page += skip;
+      refs[page] = 1;
+      take(rank++, static_cast<int32_t>(page));
     }
-    found += total;
+    before += total;
+    base += step;
+    if (before >= want) return 0;
+    bits = free_bits(refs, num_pages, base, per);
+    rank = before + block_prefix(__popc(bits), scratch, &total);
   }
 }
 
@@ -132,149 +149,202 @@ __device__ int prefix_in_place(int* cnt, int n, int* scratch) {
   return sum;
 }
 
+// Both kernels of one workgroup take their rows a thread a row, so that the
+// chains of dependent loads (the row's id, its numbers, its table, a page's
+// count) run once for all rows; what a row has many of (pages given back, pages
+// taken) is dealt out over the threads by a prefix sum over the rows.  A chain is
+// what bounds them: 4 loads and 2 to 4 prefix sums.
 __global__ __launch_bounds__(kPoolThreads) void kv_resize_kernel(ResizeParams p) {
-  __shared__ int start[kSpecMaxRequests];
+  __shared__ int more[kSpecMaxRequests];  // pages to take, then their prefix
+  __shared__ int less[kSpecMaxRequests];  // pages to give back
+  __shared__ int held[kSpecMaxRequests];
+  __shared__ int row_l[kSpecMaxRequests];
   __shared__ int scratch[kPoolWaves];
   __shared__ int refused;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x;
   if (tid == 0) refused = 0;
   __syncthreads();
-  // rows that shrink: one wave a row, one lane a page
-  for (int i = wave; i < p.n; i += kPoolWaves) {
+  for (int i = tid; i < p.n; i += kPoolThreads) {
     const int row = row_of(p.t, i);
     const int64_t len = p.new_lens[i];
     const int64_t need = (len + (int64_t{1} << p.page_shift) - 1) >> p.page_shift;
-    const bool ok = row >= 0 && len >= 0 && need <= p.t.max_pages;
-    int more = 0;
-    if (!ok) {
-      if (lane == 0) atomicAdd(&refused, 1);
+    int grow = 0, shrink = 0, have = 0;
+    if (row < 0 || len < 0 || need > p.t.max_pages) {
+      atomicAdd(&refused, 1);
     } else {
-      const int have = min(max(p.counts[row], 0), p.t.max_pages);
-      for (int64_t s = need + lane; s < have; s += kWave) {
-        const int64_t page = p.t.table[row * p.t.ld + s];
-        if (page >= 0 && page < p.num_pages) atomicSub(p.refs + page, 1);
-      }
-      more = max(static_cast<int>(need) - have, 0);
-      if (lane == 0 && more == 0) {
-        p.counts[row] = static_cast<int>(need);
+      const int count = p.counts[row];
+      have = min(max(count, 0), p.t.max_pages);
+      grow = max(static_cast<int>(need) - have, 0);
+      shrink = max(have - static_cast<int>(need), 0);
+      if (grow == 0) {
+        if (count != need) p.counts[row] = static_cast<int>(need);
         if (p.kv_lens) p.kv_lens[row] = static_cast<int32_t>(len);
       }
     }
-    if (lane == 0) start[i] = more;
+    more[i] = grow;
+    less[i] = shrink;
+    held[i] = have;
+    row_l[i] = row;
   }
-  __threadfence();
   __syncthreads();
-  const int want = prefix_in_place(start, p.n, scratch);
-  const int missing = want > 0 ? pages_missing(p.refs, p.num_pages, want, scratch) : 0;
+  const int back = prefix_in_place(less, p.n, scratch);
+  if (back > 0) {
+    for (int64_t k = tid; k < back; k += kPoolThreads) {
+      const int i = owner_of(less, p.n, static_cast<int>(k));
+      const int slot = held[i] - 1 - (static_cast<int>(k) - less[i]);
+      const int64_t page = p.t.table[row_l[i] * p.t.ld + slot];
+      if (page >= 0 && page < p.num_pages) atomicSub(p.refs + page, 1);
+    }
+    __threadfence();  // (before the counts are looked through)
+  }
+  const int want = prefix_in_place(more, p.n, scratch);
+  int missing = 0;
+  if (want > 0) {
+    __syncthreads();
+    missing = take_pages(p.refs, p.num_pages, want, scratch, [&](int rank, int32_t page) {
+      const int i = owner_of(more, p.n, rank);
+      p.t.table[row_l[i] * p.t.ld + held[i] + rank - more[i]] = page;
+    });
+  }
   if (tid == 0) {
     p.status[0] = missing;
     p.status[1] = refused;
   }
   if (want == 0 || missing > 0) return;
-  __syncthreads();
-  take_pages(p.refs, p.num_pages, want, scratch, [&](int rank, int32_t page) {
-    const int i = owner_of(start, p.n, rank);
-    const int row = row_of(p.t, i);
-    p.t.table[row * p.t.ld + max(p.counts[row], 0) + rank - start[i]] = page;
-  });
-  __syncthreads();
   for (int i = tid; i < p.n; i += kPoolThreads) {
-    const int more = (i + 1 < p.n ? start[i + 1] : want) - start[i];
-    if (more > 0) {
-      const int row = row_of(p.t, i);
-      p.counts[row] = max(p.counts[row], 0) + more;
-      if (p.kv_lens) p.kv_lens[row] = p.new_lens[i];
+    const int grow = (i + 1 < p.n ? more[i + 1] : want) - more[i];
+    if (grow > 0) {
+      p.counts[row_l[i]] = held[i] + grow;
+      if (p.kv_lens) p.kv_lens[row_l[i]] = p.new_lens[i];
     }
   }
 }
 
+// Fresh pages for the partial last pages of the pairs, and the list of the pairs
+// for the kernel that follows, which has the whole GPU for the rest.
 __global__ __launch_bounds__(kPoolThreads) void kv_fork_kernel(ForkParams p) {
   __shared__ int start[kSpecMaxRequests];
+  __shared__ int fresh[kSpecMaxRequests];
   __shared__ int scratch[kPoolWaves];
   __shared__ int refused;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  constexpr int kMine = kSpecMaxRequests / kPoolThreads;
+  const int tid = threadIdx.x;
   const int part_mask = (1 << p.page_shift) - 1;
-  auto rows = [&](int i, int* src, int* dst) {
-    *src = p.src[i];
-    *dst = p.dst[i];
-    if (*src < 0 || *src >= p.t.num_rows || *dst < 0 || *dst >= p.t.num_rows || *src == *dst)
-      return false;
-    const int len = p.kv_lens[*src];
-    const int64_t need = (static_cast<int64_t>(len) + part_mask) >> p.page_shift;
-    return len >= 0 && p.counts[*dst] <= 0 && need <= p.counts[*src] && need <= p.t.max_pages;
-  };
   if (tid == 0) refused = 0;
   __syncthreads();
-  for (int i = tid; i < p.n; i += kPoolThreads) {
-    int src, dst;
-    const bool ok = rows(i, &src, &dst);
+  int len[kMine], dst[kMine], last[kMine];  // -1: left alone
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = tid + k * kPoolThreads;
+    len[k] = dst[k] = last[k] = -1;
+    if (i >= p.n) continue;
+    const int s = p.src[i], d = p.dst[i];
+    bool ok = s >= 0 && s < p.t.num_rows && d >= 0 && d < p.t.num_rows && s != d;
+    if (ok) {
+      const int x = p.kv_lens[s], held = p.counts[s];
+      const int64_t need = (static_cast<int64_t>(x) + part_mask) >> p.page_shift;
+      ok = x >= 0 && p.counts[d] <= 0 && need <= held && need <= p.t.max_pages;
+      if (ok) {
+        len[k] = x;
+        dst[k] = d;
+        if (x & part_mask) last[k] = p.t.table[s * p.t.ld + (x >> p.page_shift)];
+      }
+    }
     if (!ok) atomicAdd(&refused, 1);
-    start[i] = ok && (p.kv_lens[src] & part_mask) ? 1 : 0;
-    p.list[2 * static_cast<int64_t>(p.n) + i] = 0;
+    start[i] = ok && (len[k] & part_mask) ? 1 : 0;
   }
   __syncthreads();
   const int want = prefix_in_place(start, p.n, scratch);
-  const int missing = want > 0 ? pages_missing(p.refs, p.num_pages, want, scratch) : 0;
+  int missing = 0;
+  if (want > 0)
+    missing = take_pages(p.refs, p.num_pages, want, scratch,
+                         [&](int rank, int32_t page) { fresh[rank] = page; });
+  __syncthreads();
   if (tid == 0) {
     p.status[0] = missing;
     p.status[1] = refused;
   }
-  if (missing > 0) return;
-  __syncthreads();
-  // fresh pages for the partial last pages; the owner of rank k is the pair
-  // whose prefix is the last one at or below k
-  take_pages(p.refs, p.num_pages, want, scratch, [&](int rank, int32_t page) {
-    const int i = owner_of(start, p.n, rank);
-    const int src = p.src[i], dst = p.dst[i], len = p.kv_lens[src];
-    const int full = len >> p.page_shift;
-    p.t.table[dst * p.t.ld + full] = page;
-    p.list[i] = p.t.table[src * p.t.ld + full];
-    p.list[p.n + i] = page;
-    p.list[2 * static_cast<int64_t>(p.n) + i] = len & part_mask;
-  });
-  __syncthreads();
-  // shared full pages: one wave a pair, one lane a page
-  for (int i = wave; i < p.n; i += kPoolWaves) {
-    int src, dst;
-    if (!rows(i, &src, &dst)) continue;
-    const int len = p.kv_lens[src], full = len >> p.page_shift;
-    for (int s = lane; s < full; s += kWave) {
-      const int32_t page = p.t.table[src * p.t.ld + s];
-      p.t.table[dst * p.t.ld + s] = page;
-      if (page >= 0 && page < p.num_pages) atomicAdd(p.refs + page, 1);
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = tid + k * kPoolThreads;
+    if (i >= p.n) continue;
+    int to = -1;
+    if (missing == 0 && len[k] >= 0 && (len[k] & part_mask)) {
+      to = fresh[start[i]];
+      p.t.table[dst[k] * p.t.ld + (len[k] >> p.page_shift)] = to;
     }
-    if (lane == 0) {
-      p.kv_lens[dst] = len;
-      p.counts[dst] = full + ((len & part_mask) ? 1 : 0);
-    }
+    p.list[i] = last[k];
+    p.list[p.n + i] = to;
+    p.list[2 * static_cast<int64_t>(p.n) + i] = missing == 0 ? len[k] : -1;
   }
 }
 
-// One workgroup per (entry, layer, keys or values), 16 bytes a thread and
-// turn, in the order in which the page lies in memory.
+// The full pages of pair i, which the rows share from now on, and dst's numbers.
+__device__ void share_pages(const ForkParams& p, int64_t i, int len) {
+  const int src = p.src[i], dst = p.dst[i], full = len >> p.page_shift;
+  for (int s = threadIdx.x; s < full; s += blockDim.x) {
+    const int32_t page = p.t.table[src * p.t.ld + s];
+    p.t.table[dst * p.t.ld + s] = page;
+    if (page >= 0 && page < p.num_pages) atomicAdd(p.refs + page, 1);
+  }
+  if (threadIdx.x == 0) {
+    p.kv_lens[dst] = len;
+    p.counts[dst] = full + ((len & ((1 << p.page_shift) - 1)) ? 1 : 0);
+  }
+}
+
+// An entry's layers are dealt out in `groups` ranges of (layer, keys or values),
+// one workgroup each, 16 bytes a thread and turn in the order in which a page lies
+// in memory, four turns' loads before their stores.  A workgroup's own work starts
+// after three dependent loads, so the GPU is filled eight times over (256 pairs of
+// half pages in 32 layers: 61 us by 16384 workgroups, 77 by 2048).  kFork: the pairs of a fork,
+// whose partial pages are copied as far as they are filled; the first workgroup of
+// a pair shares its full pages too.
 constexpr int kCopyThreads = 256;
+constexpr int kCopyBatch = 4;
+constexpr int kCopyBlocks = 16384;
+template <bool kFork>
 __global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(KvView c, const int32_t* src,
-                                                               const int32_t* dst,
-                                                               const int32_t* tokens, int64_t n) {
-  const int64_t b = blockIdx.x;
-  const int64_t i = b / (2 * c.layers);
-  const int l = static_cast<int>(b / 2 % c.layers), is_v = static_cast<int>(b & 1);
-  if (i >= n) return;
-  const int count = tokens ? tokens[i] : 1 << c.page_shift;
+                                                               const int32_t* dst, int64_t n,
+                                                               int groups, ForkParams f) {
+  const int64_t i = blockIdx.x / groups;
+  const int g = blockIdx.x % groups;
+  int count = 1 << c.page_shift;
+  if constexpr (kFork) {
+    const int len = f.list[2 * n + i];
+    if (len < 0) return;
+    if (g == 0) share_pages(f, i, len);
+    count = len & (count - 1);
+    if (count == 0) return;
+  }
   const int64_t from = src[i], to = dst[i];
-  if (count <= 0 || from < 0 || to < 0 || from >= c.num_pages || to >= c.num_pages) return;
-  const int64_t* st = is_v ? c.vs : c.ks;
-  char* base = (is_v ? c.v : c.k) + l * st[0];
-  const char* s = base + from * st[1];
-  char* d = base + to * st[1];
-  const bool token_first = st[2] >= st[3];
-  const uint32_t vecs = c.row_bytes / 16, inner = token_first ? c.heads : count;
+  if (from < 0 || to < 0 || from >= c.num_pages || to >= c.num_pages) return;
+  const uint32_t vecs = c.row_bytes / 16;
   const uint32_t total = vecs * c.heads * count;
-  const int64_t so = token_first ? st[2] : st[3], si = token_first ? st[3] : st[2];
-  for (uint32_t e = threadIdx.x; e < total; e += kCopyThreads) {
-    const uint32_t row = e / vecs, x = e - row * vecs, outer = row / inner;
-    const int64_t off = outer * so + (row - outer * inner) * si + 16 * x;
-    *reinterpret_cast<uint4*>(d + off) = *reinterpret_cast<const uint4*>(s + off);
+  const int u0 = static_cast<int>(static_cast<int64_t>(g) * 2 * c.layers / groups);
+  const int u1 = static_cast<int>(static_cast<int64_t>(g + 1) * 2 * c.layers / groups);
+  for (int u = u0; u < u1; ++u) {
+    const int64_t* st = u & 1 ? c.vs : c.ks;
+    char* base = (u & 1 ? c.v : c.k) + (u >> 1) * st[0];
+    const char* s = base + from * st[1];
+    char* d = base + to * st[1];
+    const bool token_first = st[2] >= st[3];
+    const uint32_t inner = token_first ? c.heads : count;
+    const int64_t so = token_first ? st[2] : st[3], si = token_first ? st[3] : st[2];
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += kCopyBatch * kCopyThreads) {
+      uint4 v[kCopyBatch];
+      int64_t off[kCopyBatch];
+#pragma unroll
+      for (int k = 0; k < kCopyBatch; ++k) {
+        const uint32_t e = e0 + k * kCopyThreads;
+        const uint32_t row = e / vecs, x = e - row * vecs, outer = row / inner;
+        off[k] = outer * so + (row - outer * inner) * si + 16 * x;
+        if (e < total) v[k] = *reinterpret_cast<const uint4*>(s + off[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kCopyBatch; ++k)
+        if (e0 + k * kCopyThreads < total) store_past(d + off[k], v[k]);
+    }
   }
 }
 
@@ -313,7 +383,7 @@ __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(WriteParams p, 
       char* d = (is_v ? c.v : c.k) + page * st[1] + off * st[2] + h * st[3];
       const uint4 w = *reinterpret_cast<const uint4*>(s + 16 * d8);
       if constexpr (!kE4M3) {
-        *reinterpret_cast<uint4*>(d + 16 * d8) = w;
+        store_past(d + 16 * d8, w);
       } else {
         const float scale = (is_v ? p.v_scale : p.k_scale)[h];
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -334,57 +404,87 @@ __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(WriteParams p, 
   }
 }
 
-// One workgroup per (request, layer, keys or values); a thread carries its 16
-// bytes of a token's row through the path.  The path ascends strictly, so
-// path[j] >= j, and a row written is never one still to be read: each thread
-// may have several loads under way before their stores.
+// A request's layers are dealt out in `groups` ranges of (layer, keys or values),
+// one workgroup each; its first wave finds the moves, 64 entries of the path at a
+// time, and every thread then carries its 16 bytes of a token's row through them.
+// A move is taken if its entry lies at or past its place and past every such
+// entry before it, so a row written is never one still to be read: a thread may
+// have several loads under way before their stores.  What bounds it: the chain
+// row, length, path, page before the first byte, and then the moved bytes (58 MB
+// read and written in 9.4 us, 64 requests in 32 layers).
 constexpr int kCompactThreads = 128;
 constexpr int kCompactBatch = 4;
-__global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactParams p, KvView c) {
-  const int64_t b = blockIdx.x;
-  const int r = static_cast<int>(b / (2 * c.layers));
-  const int l = static_cast<int>(b / 2 % c.layers), is_v = static_cast<int>(b & 1);
+constexpr int kCompactBlocks = 4096;  // 16 of 2 waves on every CU
+__global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactParams p, KvView c,
+                                                                     int groups) {
+  __shared__ int4 moves[kWave];  // page and token in it, from and to
+  __shared__ int moves_n;
+  const int r = blockIdx.x / groups, g = blockIdx.x % groups;
+  const int lane = threadIdx.x % kWave;
+  const bool first_wave = threadIdx.x < kWave;
   const int row = row_of(p.t, r);
   const int n = min(max(p.accept[r], 0), p.path_width);
   const int64_t kv = row < 0 ? 0 : p.t.kv_lens[row];
-  if (threadIdx.x == 0 && l == 0 && !is_v) p.new_lens[r] = static_cast<int32_t>(kv + n);
+  if (threadIdx.x == 0 && g == 0) p.new_lens[r] = static_cast<int32_t>(kv + n);
   if (row < 0) return;
   const int32_t* path = p.path + r * p.ld_path;
-  const int64_t* st = is_v ? c.vs : c.ks;
-  char* base = (is_v ? c.v : c.k) + l * st[0];
-  const int vecs = c.row_bytes / 16, total = vecs * c.heads;
-  const int64_t low = (int64_t{1} << c.page_shift) - 1;
-  // the place of position pos, or -1
-  auto place = [&](int64_t pos) -> int64_t {
-    const int64_t page = page_at(p.t, row, pos, c.page_shift, c.num_pages);
-    return page < 0 ? -1 : page * st[1] + (pos & low) * st[2];
-  };
-  for (int e = threadIdx.x; e < total; e += kCompactThreads) {
-    const int h = e / vecs;
-    char* at = base + h * st[3] + 16 * (e - h * vecs);
-    int last = -1;
-    for (int j0 = 0; j0 < n; j0 += kCompactBatch) {
-      uint4 v[kCompactBatch];
-      int64_t to[kCompactBatch];
+  const uint32_t vecs = c.row_bytes / 16, total = vecs * c.heads;
+  const int u0 = static_cast<int>(static_cast<int64_t>(g) * 2 * c.layers / groups);
+  const int u1 = static_cast<int>(static_cast<int64_t>(g + 1) * 2 * c.layers / groups);
+  const int low = (1 << c.page_shift) - 1;
+  int last = -1;
+  for (int j0 = 0; j0 < n; j0 += kWave) {
+    if (j0 > 0) __syncthreads();
+    if (first_wave) {
+      const int j = j0 + lane;
+      const int i = j < n ? path[j] : -1;
+      int high = i >= j ? i : -1;  // the largest entry so far
 #pragma unroll
-      for (int k = 0; k < kCompactBatch; ++k) {
-        const int j = j0 + k;
-        to[k] = -1;
-        if (j < n) {
-          const int i = path[j];
-          if (i > last && i >= j) {
-            last = i;
-            if (i != j) {
-              const int64_t from = place(kv + i);
-              to[k] = from < 0 ? -1 : place(kv + j);
-              if (to[k] >= 0) v[k] = *reinterpret_cast<const uint4*>(at + from);
-            }
+      for (int d = 1; d < kWave; d *= 2) {
+        const int y = __shfl_up(high, d);
+        if (lane >= d) high = max(high, y);
+      }
+      high = max(high, last);
+      const int before = lane == 0 ? last : __shfl_up(high, 1);
+      last = __shfl(high, kWave - 1);
+      bool move = j < n && i > j && i > before;
+      int4 m{};
+      if (move) {
+        const int64_t from = page_at(p.t, row, kv + i, c.page_shift, c.num_pages);
+        const int64_t to = page_at(p.t, row, kv + j, c.page_shift, c.num_pages);
+        move = from >= 0 && to >= 0;
+        m = make_int4(static_cast<int>(from), static_cast<int>((kv + i) & low),
+                      static_cast<int>(to), static_cast<int>((kv + j) & low));
+      }
+      const unsigned long long all = __ballot(move);
+      if (move) moves[__popcll(all & ((1ull << lane) - 1ull))] = m;
+      if (lane == 0) moves_n = __popcll(all);
+    }
+    __syncthreads();
+    const int count = moves_n;
+    if (count == 0) continue;
+    for (uint32_t e = threadIdx.x; e < total * (u1 - u0); e += kCompactThreads) {
+      const uint32_t u = e / total, x = e - u * total, h = x / vecs;
+      const int unit = u0 + static_cast<int>(u);
+      const int64_t* st = unit & 1 ? c.vs : c.ks;
+      char* at = (unit & 1 ? c.v : c.k) + (unit >> 1) * st[0] + h * st[3] + 16 * (x - h * vecs);
+      for (int k0 = 0; k0 < count; k0 += kCompactBatch) {
+        uint4 v[kCompactBatch];
+#pragma unroll
+        for (int k = 0; k < kCompactBatch; ++k) {
+          if (k0 + k < count) {
+            const int4 m = moves[k0 + k];
+            v[k] = *reinterpret_cast<const uint4*>(at + m.x * st[1] + m.y * st[2]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kCompactBatch; ++k) {
+          if (k0 + k < count) {
+            const int4 m = moves[k0 + k];
+            store_past(at + m.z * st[1] + m.w * st[2], v[k]);
           }
         }
       }
-#pragma unroll
-      for (int k = 0; k < kCompactBatch; ++k)
-        if (to[k] >= 0) *reinterpret_cast<uint4*>(at + to[k]) = v[k];
     }
   }
 }
@@ -431,19 +531,27 @@ hipError_t launch_kv_resize(const ResizeParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_kv_copy(const KvView& c, const int32_t* src, const int32_t* dst,
-                          const int32_t* tokens, int64_t n, hipStream_t stream) {
-  kv_copy_kernel<<<dim3(static_cast<uint32_t>(n * 2 * c.layers)), dim3(kCopyThreads), 0,
-                   stream>>>(c, src, dst, tokens, n);
+static int groups_of(int64_t entries, int units, int blocks) {
+  const int64_t groups = entries < blocks ? blocks / entries : 1;
+  return groups < units ? static_cast<int>(groups) : units;
+}
+
+hipError_t launch_kv_copy(const KvView& c, const int32_t* src, const int32_t* dst, int64_t n,
+                          hipStream_t stream) {
+  const int groups = groups_of(n, 2 * c.layers, kCopyBlocks);
+  kv_copy_kernel<false><<<dim3(static_cast<uint32_t>(n * groups)), dim3(kCopyThreads), 0,
+                          stream>>>(c, src, dst, n, groups, ForkParams{});
   return hipGetLastError();
 }
 
 hipError_t launch_kv_fork(const ForkParams& p, const KvView& c, hipStream_t stream) {
   kv_fork_kernel<<<dim3(1), dim3(kPoolThreads), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_kv_copy(c, p.list, p.list + p.n, p.list + 2 * static_cast<int64_t>(p.n), p.n,
-                        stream);
+  if (e != hipSuccess || p.n == 0) return e;
+  const int groups = groups_of(p.n, 2 * c.layers, kCopyBlocks);
+  kv_copy_kernel<true><<<dim3(p.n * groups), dim3(kCopyThreads), 0, stream>>>(
+      c, p.list, p.list + p.n, p.n, groups, p);
+  return hipGetLastError();
 }
 
 hipError_t launch_kv_write(const WriteParams& p, const KvView& c, int dtype, bool to_e4m3,
@@ -461,9 +569,8 @@ hipError_t launch_kv_write(const WriteParams& p, const KvView& c, int dtype, boo
 }
 
 hipError_t launch_kv_compact(const CompactParams& p, const KvView& c, hipStream_t stream) {
-  const int64_t grid = static_cast<int64_t>(p.bs) * 2 * c.layers;
-  kv_compact_kernel<<<dim3(static_cast<uint32_t>(grid)), dim3(kCompactThreads), 0, stream>>>(p,
-                                                                                             c);
+  const int groups = groups_of(p.bs, 2 * c.layers, kCompactBlocks);
+  kv_compact_kernel<<<dim3(p.bs * groups), dim3(kCompactThreads), 0, stream>>>(p, c, groups);
   return hipGetLastError();
 }
 

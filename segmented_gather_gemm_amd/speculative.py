@@ -74,34 +74,37 @@ def _f32(name, t, dev, shape):
 
 
 def _strides(name, t):
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] != 1:
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return [0 if n == 1 else s for n, s in zip(t.shape, st)]
+    return [0 if n == 1 else s for n, s in zip(shape, st)] if 1 in shape else st
 
 
 def _cache(k, v):
     """SpecKvCache of keys and values (pages, page_size, kv heads, head_dim), with a leading
     layer dimension or without; returns it with the shape as five numbers."""
-    shape = k.shape
-    if v.shape != shape or v.dtype is not k.dtype:
-        raise ValueError(f"k_cache {tuple(shape)} {k.dtype} and v_cache {tuple(v.shape)} "
+    shape, dtype = k.shape, k.dtype
+    if v.shape != shape or v.dtype is not dtype:
+        raise ValueError(f"k_cache {tuple(shape)} {dtype} and v_cache {tuple(v.shape)} "
                          f"{v.dtype} differ")
-    code = _CODES.get(k.dtype)
+    code = _CODES.get(dtype)
     if code is None:
-        raise TypeError(f"the cache must be bfloat16, float16 or float8_e4m3fn, got {k.dtype}")
-    if not k.is_cuda or v.get_device() != k.get_device():
+        raise TypeError(f"the cache must be bfloat16, float16 or float8_e4m3fn, got {dtype}")
+    dev = k.get_device()
+    if dev < 0 or v.get_device() != dev:
         raise ValueError("k_cache and v_cache must be on one ROCm device")
     if len(shape) == 4:
-        shape = (1, *shape)
-        ks, vs = [0] + _strides("k_cache", k), [0] + _strides("v_cache", v)
+        P, ps, H, D = shape
+        (k1, k2, k3, _), (v1, v2, v3, _) = _strides("k_cache", k), _strides("v_cache", v)
+        L = 1
+        k0 = v0 = 0
     elif len(shape) == 5:
-        ks, vs = _strides("k_cache", k), _strides("v_cache", v)
+        L, P, ps, H, D = shape
+        (k0, k1, k2, k3, _), (v0, v1, v2, v3, _) = _strides("k_cache", k), _strides("v_cache", v)
     else:
         raise ValueError(f"the cache must have 4 or 5 dimensions, got {tuple(shape)}")
-    L, P, ps, H, D = shape
-    return _CACHE.pack(k.data_ptr(), v.data_ptr(), *ks[:4], *vs[:4], P, L, ps, H, D, code, 0), \
-        (L, P, ps, H, D)
+    return _CACHE.pack(k.data_ptr(), v.data_ptr(), k0, k1, k2, k3, v0, v1, v2, v3,
+                       P, L, ps, H, D, code, 0), (L, P, ps, H, D)
 
 
 def _table(t, dev):
