@@ -4,13 +4,13 @@
 CPython module ``_sggcall`` with the hot entry points (plan upload, shrink,
 expand, qkv, embedding), which take integer arguments and cost far less per
 call than ctypes.  ``spec_calls()`` is the like module ``_sggspec`` with the
-entry points of include/sgg_spec.h.
+entry points of include/sgg_spec.h, and ``tensor_args()`` checks their tensors.
 """
 
 import ctypes
 import os
 
-from .build import CALLMOD, LIB, SPECMOD
+from .build import CALLMOD, LIB, SPECMOD, TENSORMOD
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _pi32, _pi64 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)
@@ -126,6 +126,17 @@ def spec_calls():
         from . import _sggspec
         _spec = _sggspec
     return _spec
+
+
+def tensor_args():
+    """The CPython module that checks the tensor arguments of those calls.  Raises if it has
+    not been built."""
+    if not os.path.exists(TENSORMOD):
+        raise ImportError(
+            f"{TENSORMOD} is missing: build it with `python segmented_gather_gemm_amd/build.py`")
+    import torch  # noqa: F401  (its libraries, which the module needs)
+    from . import _sggtensor
+    return _sggtensor
 
 
 def check(rc):

@@ -12,6 +12,7 @@ LIB = os.path.join(PKG, "libsgg_lora.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 CALLMOD = os.path.join(PKG, "_sggcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SPECMOD = os.path.join(PKG, "_sggspec" + sysconfig.get_config_var("EXT_SUFFIX"))
+TENSORMOD = os.path.join(PKG, "_sggtensor" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["spec_attention_bf16_same.hip", "spec_attention_bf16_e4m3.hip",
            "spec_attention_fp16_same.hip", "spec_attention_fp16_e4m3.hip", "plan.cpp",
            "tiling.cpp", "plan_device.hip", "shrink.hip", "shrink_gemm.hip", "expand.hip", "fused.hip",
@@ -41,6 +42,20 @@ def _run(cmd, verbose, what):
         raise RuntimeError(f"{what} failed with status {res.returncode}")
 
 
+def _tensor_module(verbose):
+    """Checks of tensor arguments, over torch's C++ tensors (host code only)."""
+    import importlib.util
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    libs = os.path.join(torch_dir, "lib")
+    tmp = TENSORMOD + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+          "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+          "-isystem", os.path.join(torch_dir, "include"),
+          os.path.join(CSRC, "tensorargs.cpp"), "-L", libs,
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp], verbose, "c++ tensorargs.cpp")
+    os.replace(tmp, TENSORMOD)
+
+
 def build(verbose=False):
     """Build the shared library and the CPython call modules; always
     recompiles (one hipcc per source, in parallel, then one link).  Returns
@@ -56,7 +71,9 @@ def build(verbose=False):
 
     workers = max(1, min(len(SOURCES), os.cpu_count() or 1, 8))
     with ThreadPoolExecutor(workers) as pool:
+        tensor_module = pool.submit(_tensor_module, verbose)
         list(pool.map(compile_one, range(len(SOURCES))))
+        tensor_module.result()
     tmp = LIB + ".tmp"
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC"] + objs + ["-o", tmp], verbose,
          "hipcc link")

@@ -11,15 +11,17 @@ request (None: request r is row r).  Index arrays are contiguous int32 tensors
 on the device; the host never reads them.
 """
 
-import struct
-
 import torch
 
-from ._lib import check, spec_calls
+from ._lib import check, spec_calls, tensor_args
 from .binding import _stream
 
 _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
-_CACHE = struct.Struct("=QQ4q4qq6i")   # SpecKvCache
+
+# the checks of one tensor argument each (csrc/tensorargs.cpp)
+_args = tensor_args()
+_i32, _f32, _table, _cache, _heads = _args.i32, _args.f32, _args.table, _args.cache, _args.heads
+_new_i32 = _args.new_i32
 
 
 _workspaces = {}
@@ -51,91 +53,13 @@ def _workspace(t, nbytes):
     return ws.data_ptr(), ws.numel(), ws
 
 
-def _i32(name, t, dev, shape=None):
-    """Address of a contiguous int32 tensor on device `dev` (of `shape`, if given)."""
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be on the cache's ROCm device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _f32(name, t, dev, shape):
-    if t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.get_device() != dev or dev < 0 or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on the "
-                         f"ROCm device, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _strides(name, t):
-    st, shape = t.stride(), t.shape
-    if st[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
-    return [0 if n == 1 else s for n, s in zip(shape, st)] if 1 in shape else st
-
-
-def _cache(k, v):
-    """SpecKvCache of keys and values (pages, page_size, kv heads, head_dim), with a leading
-    layer dimension or without; returns it with the shape as five numbers."""
-    shape, dtype = k.shape, k.dtype
-    if v.shape != shape or v.dtype is not dtype:
-        raise ValueError(f"k_cache {tuple(shape)} {dtype} and v_cache {tuple(v.shape)} "
-                         f"{v.dtype} differ")
-    code = _CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"the cache must be bfloat16, float16 or float8_e4m3fn, got {dtype}")
-    dev = k.get_device()
-    if dev < 0 or v.get_device() != dev:
-        raise ValueError("k_cache and v_cache must be on one ROCm device")
-    if len(shape) == 4:
-        P, ps, H, D = shape
-        (k1, k2, k3, _), (v1, v2, v3, _) = _strides("k_cache", k), _strides("v_cache", v)
-        L = 1
-        k0 = v0 = 0
-    elif len(shape) == 5:
-        L, P, ps, H, D = shape
-        (k0, k1, k2, k3, _), (v0, v1, v2, v3, _) = _strides("k_cache", k), _strides("v_cache", v)
-    else:
-        raise ValueError(f"the cache must have 4 or 5 dimensions, got {tuple(shape)}")
-    return _CACHE.pack(k.data_ptr(), v.data_ptr(), k0, k1, k2, k3, v0, v1, v2, v3,
-                       P, L, ps, H, D, code, 0), (L, P, ps, H, D)
-
-
-def _table(t, dev):
-    """Address, row stride, width and rows of a page table."""
-    if t.dtype is not torch.int32:
-        raise TypeError(f"page_table must be int32, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError("page_table must be on the cache's ROCm device")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
-        raise ValueError("page_table must be (rows, pages) with unit stride in its last dimension")
-    rows, width = t.shape
-    return t.data_ptr(), t.stride(0) if rows > 1 else width, width, rows
-
-
 def _batch(q_indptr, rows, dev):
     """Requests of the batch, addresses of q_indptr and rows."""
     p = _i32("q_indptr", q_indptr, dev)
     bs = q_indptr.numel() - 1
     if bs < 0 or q_indptr.dim() != 1:
         raise ValueError("q_indptr must hold bs + 1 entries")
-    return bs, p, 0 if rows is None else _i32("rows", rows, dev, (bs,))
-
-
-def _heads(name, t, dtype_of=None):
-    """(tokens, heads, head_dim) rows of a 16-bit type: address, token and head strides."""
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be (tokens, heads, head_dim), got {tuple(t.shape)}")
-    st = _strides(name, t)
-    return t.data_ptr(), st[0], st[1]
+    return bs, p, 0 if rows is None else _i32("rows", rows, dev, bs)
 
 
 def spec_kv_resize(page_table, page_counts, ref_counts, rows, new_lens, page_size, kv_lens=None,
@@ -148,14 +72,14 @@ def spec_kv_resize(page_table, page_counts, ref_counts, rows, new_lens, page_siz
     t, ld, width, num_rows = _table(page_table, dev)
     n = new_lens.numel()
     if status is None:
-        status = torch.empty(2, dtype=torch.int32, device=page_table.device)
+        status = _new_i32(page_table, 2)
     check(spec_calls().spec_kv_resize(
-        t, ld, width, num_rows, _i32("page_counts", page_counts, dev, (num_rows,)),
+        t, ld, width, num_rows, _i32("page_counts", page_counts, dev, num_rows),
         _i32("ref_counts", ref_counts, dev), ref_counts.numel(),
-        0 if rows is None else _i32("rows", rows, dev, (n,)),
-        _i32("new_lens", new_lens, dev, (n,)), n, int(page_size),
-        0 if kv_lens is None else _i32("kv_lens", kv_lens, dev, (num_rows,)),
-        _i32("status", status, dev, (2,)), _stream(page_table)))
+        0 if rows is None else _i32("rows", rows, dev, n),
+        _i32("new_lens", new_lens, dev, n), n, int(page_size),
+        0 if kv_lens is None else _i32("kv_lens", kv_lens, dev, num_rows),
+        _i32("status", status, dev, 2), _stream(page_table)))
     return status
 
 
@@ -169,13 +93,13 @@ def spec_kv_fork(k_cache, v_cache, page_table, page_counts, ref_counts, kv_lens,
     t, ld, width, num_rows = _table(page_table, dev)
     n = src_rows.numel()
     if status is None:
-        status = torch.empty(2, dtype=torch.int32, device=page_table.device)
-    ws = torch.empty(3 * n, dtype=torch.int32, device=page_table.device)
+        status = _new_i32(page_table, 2)
+    ws = _new_i32(page_table, 3 * n)
     check(spec_calls().spec_kv_fork(
-        c, t, ld, width, num_rows, _i32("page_counts", page_counts, dev, (num_rows,)),
-        _i32("ref_counts", ref_counts, dev, (P,)), _i32("kv_lens", kv_lens, dev, (num_rows,)),
-        _i32("src_rows", src_rows, dev, (n,)), _i32("dst_rows", dst_rows, dev, (n,)), n,
-        _i32("status", status, dev, (2,)), ws.data_ptr(), 12 * n, _stream(page_table)))
+        c, t, ld, width, num_rows, _i32("page_counts", page_counts, dev, num_rows),
+        _i32("ref_counts", ref_counts, dev, P), _i32("kv_lens", kv_lens, dev, num_rows),
+        _i32("src_rows", src_rows, dev, n), _i32("dst_rows", dst_rows, dev, n), n,
+        _i32("status", status, dev, 2), ws.data_ptr(), 12 * n, _stream(page_table)))
     return status
 
 
@@ -185,7 +109,7 @@ def spec_kv_copy_pages(k_cache, v_cache, src_pages, dst_pages):
     c, _ = _cache(k_cache, v_cache)
     n = src_pages.numel()
     check(spec_calls().spec_kv_copy_pages(
-        c, _i32("src_pages", src_pages, dev, (n,)), _i32("dst_pages", dst_pages, dev, (n,)), n,
+        c, _i32("src_pages", src_pages, dev, n), _i32("dst_pages", dst_pages, dev, n), n,
         _stream(k_cache)))
 
 
@@ -207,9 +131,9 @@ def spec_kv_write(k, v, k_cache, v_cache, page_table, kv_lens, q_indptr, rows=No
     bs, ind, rp = _batch(q_indptr, rows, dev)
     check(spec_calls().spec_kv_write(
         kp, kt, kh, vp, vt, vh, _CODES[k.dtype], c, t, ld, width, num_rows,
-        _i32("kv_lens", kv_lens, dev, (num_rows,)), rp, ind, bs, n,
-        0 if k_scale is None else _f32("k_scale", k_scale, dev, (H,)),
-        0 if v_scale is None else _f32("v_scale", v_scale, dev, (H,)), _stream(k_cache)))
+        _i32("kv_lens", kv_lens, dev, num_rows), rp, ind, bs, n,
+        0 if k_scale is None else _f32("k_scale", k_scale, dev, H),
+        0 if v_scale is None else _f32("v_scale", v_scale, dev, H), _stream(k_cache)))
 
 
 def spec_kv_compact(k_cache, v_cache, page_table, kv_lens, path, accept_lens, rows=None,
@@ -223,11 +147,11 @@ def spec_kv_compact(k_cache, v_cache, page_table, kv_lens, path, accept_lens, ro
         raise ValueError(f"path must be (requests, width), got {tuple(path.shape)}")
     bs, w = path.shape
     if new_lens is None:
-        new_lens = torch.empty(bs, dtype=torch.int32, device=k_cache.device)
+        new_lens = _new_i32(k_cache, bs)
     check(spec_calls().spec_kv_compact(
-        c, t, ld, width, num_rows, _i32("kv_lens", kv_lens, dev, (num_rows,)),
-        0 if rows is None else _i32("rows", rows, dev, (bs,)), _i32("path", path, dev), w, w,
-        _i32("accept_lens", accept_lens, dev, (bs,)), _i32("new_lens", new_lens, dev, (bs,)), bs,
+        c, t, ld, width, num_rows, _i32("kv_lens", kv_lens, dev, num_rows),
+        0 if rows is None else _i32("rows", rows, dev, bs), _i32("path", path, dev), w, w,
+        _i32("accept_lens", accept_lens, dev, bs), _i32("new_lens", new_lens, dev, bs), bs,
         _stream(k_cache)))
     return new_lens
 
@@ -241,7 +165,7 @@ def spec_tree_mask(parents, q_indptr, kv_lens, mask_words, rows=None):
     bs, ind, rp = _batch(q_indptr, rows, dev)
     n = parents.numel()
     mask = torch.empty((n, int(mask_words)), dtype=torch.int64, device=parents.device)
-    positions = torch.empty(n, dtype=torch.int32, device=parents.device)
+    positions = _new_i32(parents, n)
     check(spec_calls().spec_tree_mask(p, ind, bs, n, _i32("kv_lens", kv_lens, dev), rp,
                                       kv_lens.numel(), mask.data_ptr(), int(mask_words),
                                       positions.data_ptr(), _stream(parents)))
@@ -287,10 +211,10 @@ def spec_attention(q, k_cache, v_cache, page_table, kv_lens, q_indptr, max_q_len
         wp, wn = workspace.data_ptr(), workspace.numel()
     check(calls.spec_attention(
         qp, qt, qh, op, ot, oh, _CODES[q.dtype], hq, c, t, ld, width, num_rows,
-        _i32("kv_lens", kv_lens, dev, (num_rows,)), rp, ind, bs, n, mp, words,
+        _i32("kv_lens", kv_lens, dev, num_rows), rp, ind, bs, n, mp, words,
         D ** -0.5 if scale is None else scale,
-        0 if k_scale is None else _f32("k_scale", k_scale, dev, (H,)),
-        0 if v_scale is None else _f32("v_scale", v_scale, dev, (H,)), max_q_len, max_kv_len, wp, wn,
+        0 if k_scale is None else _f32("k_scale", k_scale, dev, H),
+        0 if v_scale is None else _f32("v_scale", v_scale, dev, H), max_q_len, max_kv_len, wp, wn,
         _stream(q)))
     return out
 
@@ -312,20 +236,19 @@ def spec_verify(tokens, parents, q_indptr, target_probs, uniforms, final_uniform
             raise ValueError(f"{name} must be float32 (tokens, vocab) rows, got "
                              f"{tuple(x.shape)} {x.dtype}")
     V = target_probs.shape[1]
-    path = torch.empty((bs, int(max_q_len)), dtype=torch.int32, device=target_probs.device)
-    got = torch.empty((2, bs), dtype=torch.int32, device=target_probs.device)
-    accept, nxt = got[0], got[1]
+    path = _new_i32(target_probs, bs, int(max_q_len))
+    accept, nxt = _new_i32(target_probs, bs), _new_i32(target_probs, bs)
     calls = spec_calls()
     if workspace is None:
         wp, wn, _held = _workspace(target_probs, calls.spec_verify_workspace_bytes(bs, V))
     else:   # the library checks its size
         wp, wn = workspace.data_ptr(), workspace.numel()
     check(calls.spec_verify(
-        _i32("tokens", tokens, dev, (n,)), _i32("parents", parents, dev, (n,)), ind, bs, n,
+        _i32("tokens", tokens, dev, n), _i32("parents", parents, dev, n), ind, bs, n,
         target_probs.data_ptr(), target_probs.stride(0) if n > 1 else V,
         0 if draft_probs is None else draft_probs.data_ptr(),
         0 if draft_probs is None else (draft_probs.stride(0) if n > 1 else V), V,
-        _f32("uniforms", uniforms, dev, (n,)), _f32("final_uniforms", final_uniforms, dev, (bs,)),
+        _f32("uniforms", uniforms, dev, n), _f32("final_uniforms", final_uniforms, dev, bs),
         path.data_ptr(), int(max_q_len), int(max_q_len), accept.data_ptr(), nxt.data_ptr(), wp, wn,
         _stream(target_probs)))
     return path, accept, nxt
