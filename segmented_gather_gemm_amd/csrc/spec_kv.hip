@@ -13,8 +13,11 @@
 namespace sgg {
 namespace {
 
+// The kernels of one workgroup: 1024 threads, or 256 where each has at most one
+// row and its share of the pool's counts is one scan (5 rows: 3.3 us with 256, 5.1
+// with 1024; 64 rows of 900 pages 4.5 and 5.8).
 constexpr int kPoolThreads = 1024;
-constexpr int kPoolWaves = kPoolThreads / kWave;
+constexpr int kFewThreads = 256;
 
 __device__ __forceinline__ int load_agent(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -45,28 +48,35 @@ __device__ __forceinline__ int64_t page_at(const KvRows& t, int row, int64_t pos
   return page >= 0 && page < num_pages ? page : -1;
 }
 
+// The value that a lane below holds, by register moves (0 where there is none).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int from_below(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xf, false);
+}
+__device__ __forceinline__ int row_prefix(int v) {  // inclusive, over 16 lanes
+  v += from_below<0x111, 0xf>(v);
+  v += from_below<0x112, 0xf>(v);
+  v += from_below<0x114, 0xf>(v);
+  v += from_below<0x118, 0xf>(v);
+  return v;
+}
+
 // Exclusive prefix of v over the workgroup, and the total.  `scratch` holds
-// kPoolWaves values; all threads call.
+// 16 values; all threads call.
+template <int kT>
 __device__ int block_prefix(int v, int* scratch, int* total) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  int x = v;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  int x = row_prefix(v);
+  x += from_below<0x142, 0xa>(x);
+  x += from_below<0x143, 0xc>(x);
   __syncthreads();
   if (lane == kWave - 1) scratch[wave] = x;
   __syncthreads();
-  int before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kPoolWaves; ++w) {
-    const int c = scratch[w];
-    if (w < wave) before += c;
-    sum += c;
-  }
-  *total = sum;
-  return before + x - v;
+  const int w = lane < kT / kWave ? scratch[lane] : 0;
+  const int sums = row_prefix(w);
+  *total = __builtin_amdgcn_readlane(sums, 15);
+  return __builtin_amdgcn_readlane(sums - w, wave) + x - v;
 }
 
 // The free pages among ids [base + per t, + per) as bits, for thread t.
@@ -87,21 +97,21 @@ __device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t num_p
 
 // Hands the lowest `want` free pages out, take(rank, page) for each, or none if
 // fewer are free; returns the number missing.  A thread looks at up to 32 ids
-// that follow one another, so a pool of 32768 pages takes one scan and one
-// prefix; a larger one is counted first, if its first 32768 do not suffice.
-template <class Take>
+// that follow one another, so a pool of 32 a thread takes one scan and one
+// prefix; a larger one is counted first, if those do not suffice.
+template <int kT, class Take>
 __device__ int take_pages(int32_t* refs, int64_t num_pages, int want, int* scratch,
                           const Take& take) {
-  const int64_t share = (num_pages + kPoolThreads - 1) / kPoolThreads;
+  const int64_t share = (num_pages + kT - 1) / kT;
   const int per = share < kScanIds ? (static_cast<int>(share) + 3) & ~3 : kScanIds;
-  const int64_t step = static_cast<int64_t>(per) * kPoolThreads;
+  const int64_t step = static_cast<int64_t>(per) * kT;
   uint32_t bits = free_bits(refs, num_pages, 0, per);
   int total;
-  int rank = block_prefix(__popc(bits), scratch, &total);
+  int rank = block_prefix<kT>(__popc(bits), scratch, &total);
   int found = total;
   for (int64_t base = step; base < num_pages && found < want; base += step) {
     int more;
-    block_prefix(__popc(free_bits(refs, num_pages, base, per)), scratch, &more);
+    block_prefix<kT>(__popc(free_bits(refs, num_pages, base, per)), scratch, &more);
     found += more;
   }
   if (found < want) return want - found;
@@ -119,7 +129,7 @@ __device__ int take_pages(int32_t* refs, int64_t num_pages, int want, int* scrat
     base += step;
     if (before >= want) return 0;
     bits = free_bits(refs, num_pages, base, per);
-    rank = before + block_prefix(__popc(bits), scratch, &total);
+    rank = before + block_prefix<kT>(__popc(bits), scratch, &total);
   }
 }
 
@@ -135,13 +145,14 @@ __device__ __forceinline__ int owner_of(const int* start, int n, int rank) {
 }
 
 // Exclusive prefix of cnt[0..n) in place over the workgroup; returns the total.
+template <int kT>
 __device__ int prefix_in_place(int* cnt, int n, int* scratch) {
   int sum = 0;
-  for (int base = 0; base < n; base += kPoolThreads) {
+  for (int base = 0; base < n; base += kT) {
     const int i = base + threadIdx.x;
     const int v = i < n ? cnt[i] : 0;
     int total;
-    const int before = block_prefix(v, scratch, &total);
+    const int before = block_prefix<kT>(v, scratch, &total);
     if (i < n) cnt[i] = sum + before;
     sum += total;
   }
@@ -154,17 +165,19 @@ __device__ int prefix_in_place(int* cnt, int n, int* scratch) {
 // count) run once for all rows; what a row has many of (pages given back, pages
 // taken) is dealt out over the threads by a prefix sum over the rows.  A chain is
 // what bounds them: 4 loads and 2 to 4 prefix sums.
-__global__ __launch_bounds__(kPoolThreads) void kv_resize_kernel(ResizeParams p) {
-  __shared__ int more[kSpecMaxRequests];  // pages to take, then their prefix
-  __shared__ int less[kSpecMaxRequests];  // pages to give back
-  __shared__ int held[kSpecMaxRequests];
-  __shared__ int row_l[kSpecMaxRequests];
-  __shared__ int scratch[kPoolWaves];
+template <int kT>
+__global__ __launch_bounds__(kT) void kv_resize_kernel(ResizeParams p) {
+  constexpr int kRows = kT == kFewThreads ? kT : kSpecMaxRequests;
+  __shared__ int more[kRows];  // pages to take, then their prefix
+  __shared__ int less[kRows];  // pages to give back
+  __shared__ int held[kRows];
+  __shared__ int row_l[kRows];
+  __shared__ int scratch[16];
   __shared__ int refused;
   const int tid = threadIdx.x;
   if (tid == 0) refused = 0;
   __syncthreads();
-  for (int i = tid; i < p.n; i += kPoolThreads) {
+  for (int i = tid; i < p.n; i += kT) {
     const int row = row_of(p.t, i);
     const int64_t len = p.new_lens[i];
     const int64_t need = (len + (int64_t{1} << p.page_shift) - 1) >> p.page_shift;
@@ -187,21 +200,32 @@ __global__ __launch_bounds__(kPoolThreads) void kv_resize_kernel(ResizeParams p)
     row_l[i] = row;
   }
   __syncthreads();
-  const int back = prefix_in_place(less, p.n, scratch);
+  const int back = prefix_in_place<kT>(less, p.n, scratch);
   if (back > 0) {
-    for (int64_t k = tid; k < back; k += kPoolThreads) {
-      const int i = owner_of(less, p.n, static_cast<int>(k));
-      const int slot = held[i] - 1 - (static_cast<int>(k) - less[i]);
-      const int64_t page = p.t.table[row_l[i] * p.t.ld + slot];
-      if (page >= 0 && page < p.num_pages) atomicSub(p.refs + page, 1);
+    constexpr int kTurns = 4;  // loads under way
+    for (int64_t k0 = tid; k0 < back; k0 += kTurns * kT) {
+      int64_t page[kTurns];
+#pragma unroll
+      for (int j = 0; j < kTurns; ++j) {
+        const int64_t k = k0 + j * kT;
+        page[j] = -1;
+        if (k < back) {
+          const int i = owner_of(less, p.n, static_cast<int>(k));
+          const int slot = held[i] - 1 - (static_cast<int>(k) - less[i]);
+          page[j] = p.t.table[row_l[i] * p.t.ld + slot];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kTurns; ++j)
+        if (page[j] >= 0 && page[j] < p.num_pages) atomicSub(p.refs + page[j], 1);
     }
     __threadfence();  // (before the counts are looked through)
   }
-  const int want = prefix_in_place(more, p.n, scratch);
+  const int want = prefix_in_place<kT>(more, p.n, scratch);
   int missing = 0;
   if (want > 0) {
     __syncthreads();
-    missing = take_pages(p.refs, p.num_pages, want, scratch, [&](int rank, int32_t page) {
+    missing = take_pages<kT>(p.refs, p.num_pages, want, scratch, [&](int rank, int32_t page) {
       const int i = owner_of(more, p.n, rank);
       p.t.table[row_l[i] * p.t.ld + held[i] + rank - more[i]] = page;
     });
@@ -211,7 +235,7 @@ __global__ __launch_bounds__(kPoolThreads) void kv_resize_kernel(ResizeParams p)
     p.status[1] = refused;
   }
   if (want == 0 || missing > 0) return;
-  for (int i = tid; i < p.n; i += kPoolThreads) {
+  for (int i = tid; i < p.n; i += kT) {
     const int grow = (i + 1 < p.n ? more[i + 1] : want) - more[i];
     if (grow > 0) {
       p.counts[row_l[i]] = held[i] + grow;
@@ -222,12 +246,14 @@ __global__ __launch_bounds__(kPoolThreads) void kv_resize_kernel(ResizeParams p)
 
 // Fresh pages for the partial last pages of the pairs, and the list of the pairs
 // for the kernel that follows, which has the whole GPU for the rest.
-__global__ __launch_bounds__(kPoolThreads) void kv_fork_kernel(ForkParams p) {
-  __shared__ int start[kSpecMaxRequests];
-  __shared__ int fresh[kSpecMaxRequests];
-  __shared__ int scratch[kPoolWaves];
+template <int kT>
+__global__ __launch_bounds__(kT) void kv_fork_kernel(ForkParams p) {
+  constexpr int kRows = kT == kFewThreads ? kT : kSpecMaxRequests;
+  __shared__ int start[kRows];
+  __shared__ int fresh[kRows];
+  __shared__ int scratch[16];
   __shared__ int refused;
-  constexpr int kMine = kSpecMaxRequests / kPoolThreads;
+  constexpr int kMine = kRows / kT;
   const int tid = threadIdx.x;
   const int part_mask = (1 << p.page_shift) - 1;
   if (tid == 0) refused = 0;
@@ -235,7 +261,7 @@ __global__ __launch_bounds__(kPoolThreads) void kv_fork_kernel(ForkParams p) {
   int len[kMine], dst[kMine], last[kMine];  // -1: left alone
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
-    const int i = tid + k * kPoolThreads;
+    const int i = tid + k * kT;
     len[k] = dst[k] = last[k] = -1;
     if (i >= p.n) continue;
     const int s = p.src[i], d = p.dst[i];
@@ -254,10 +280,10 @@ __global__ __launch_bounds__(kPoolThreads) void kv_fork_kernel(ForkParams p) {
     start[i] = ok && (len[k] & part_mask) ? 1 : 0;
   }
   __syncthreads();
-  const int want = prefix_in_place(start, p.n, scratch);
+  const int want = prefix_in_place<kT>(start, p.n, scratch);
   int missing = 0;
   if (want > 0)
-    missing = take_pages(p.refs, p.num_pages, want, scratch,
+    missing = take_pages<kT>(p.refs, p.num_pages, want, scratch,
                          [&](int rank, int32_t page) { fresh[rank] = page; });
   __syncthreads();
   if (tid == 0) {
@@ -266,7 +292,7 @@ __global__ __launch_bounds__(kPoolThreads) void kv_fork_kernel(ForkParams p) {
   }
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
-    const int i = tid + k * kPoolThreads;
+    const int i = tid + k * kT;
     if (i >= p.n) continue;
     int to = -1;
     if (missing == 0 && len[k] >= 0 && (len[k] & part_mask)) {
@@ -526,8 +552,15 @@ __global__ __launch_bounds__(kMaskThreads) void tree_mask_kernel(TreeMaskParams 
 
 }  // namespace
 
+static bool few(int64_t n, int64_t num_pages) {
+  return n <= kFewThreads && num_pages <= kScanIds * kFewThreads;
+}
+
 hipError_t launch_kv_resize(const ResizeParams& p, hipStream_t stream) {
-  kv_resize_kernel<<<dim3(1), dim3(kPoolThreads), 0, stream>>>(p);
+  if (few(p.n, p.num_pages))
+    kv_resize_kernel<kFewThreads><<<dim3(1), dim3(kFewThreads), 0, stream>>>(p);
+  else
+    kv_resize_kernel<kPoolThreads><<<dim3(1), dim3(kPoolThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -545,7 +578,10 @@ hipError_t launch_kv_copy(const KvView& c, const int32_t* src, const int32_t* ds
 }
 
 hipError_t launch_kv_fork(const ForkParams& p, const KvView& c, hipStream_t stream) {
-  kv_fork_kernel<<<dim3(1), dim3(kPoolThreads), 0, stream>>>(p);
+  if (few(p.n, p.num_pages))
+    kv_fork_kernel<kFewThreads><<<dim3(1), dim3(kFewThreads), 0, stream>>>(p);
+  else
+    kv_fork_kernel<kPoolThreads><<<dim3(1), dim3(kPoolThreads), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.n == 0) return e;
   const int groups = groups_of(p.n, 2 * c.layers, kCopyBlocks);

@@ -654,6 +654,48 @@ def test_resize_follows_the_oracle(pages, ps):
         _same(pool, table, counts, lens, refs)
 
 
+@pytest.mark.parametrize("R,pages", [(300, 600), (3, 70000), (1500, 70000), (4096, 9000)])
+def test_resize_many_rows_and_large_pools(R, pages):
+    """The lowest free pages lie behind 32768 taken ones, or few are left."""
+    sgg = _sgg()
+    rng = np.random.default_rng(R)
+    table, counts, lens, refs = _pool(R, 40, pages, 4, rng, np.zeros(R, int))
+    refs[:] = 1                                   # held by nobody here
+    refs[rng.permutation(pages)[:2 * R + 5] if pages < 10000 else
+         np.r_[10:20, pages - 2 * R - 5:pages]] = 0
+    pool = osp.Pool(table, counts, lens, refs, 4)
+    table, counts, lens, refs = (_i32(x) for x in (table, counts, lens, refs))
+    order = rng.permutation(R)
+    for top, commit in ((9, True), (13, False), (5, True), (9, False), (1, True)):
+        new = rng.integers(0, top, R)
+        st = sgg.spec_kv_resize(table, counts, refs, _i32(order), _i32(new), 4,
+                                kv_lens=lens if commit else None)
+        assert st.tolist() == list(pool.resize(order, new, commit))
+        _same(pool, table, counts, lens, refs)
+
+
+@pytest.mark.parametrize("n,pages", [(2, 9000), (300, 2000), (1100, 5000)])
+def test_fork_many_pairs(n, pages):
+    sgg = _sgg()
+    rng = np.random.default_rng(n)
+    R, ps, d = 20 + n, 4, 8
+    state = _pool(R, 30, pages, ps, rng, np.r_[rng.integers(0, 60, 20), np.zeros(n, int)])
+    pool = osp.Pool(state[0], state[1], state[2], state[3], ps)
+    table, counts, lens, refs = (_i32(x) for x in state)
+    k, v = (torch.randint(-9, 9, (2, pages, ps, 1, d), device=DEV).to(torch.bfloat16)
+            for _ in range(2))
+    before = [x.cpu().clone() for x in (k, v)]
+    src, dst = rng.integers(0, 20, n), 20 + rng.permutation(n)
+    st = sgg.spec_kv_fork(k, v, table, counts, refs, lens, _i32(src), _i32(dst))
+    missing, refused, copies = pool.fork(src, dst)
+    assert st.tolist() == [missing, refused] == [0, 0]
+    _same(pool, table, counts, lens, refs)
+    for x, want in zip((k, v), before):
+        for a, b, m in copies:
+            want[:, b, :m] = want[:, a, :m]
+        assert torch.equal(x.cpu(), want)
+
+
 def test_resize_whole_rows_and_exhaustion():
     sgg = _sgg()
     rng = np.random.default_rng(1)
