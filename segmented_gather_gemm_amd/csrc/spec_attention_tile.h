@@ -463,6 +463,9 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
     const int T = u.q.tokens, kv = u.q.context;
     const int32_t* table = p.t.table + u.q.row * p.t.ld;
     const int first_row = u.mb * D::kRows;
+    // keys that all rows of the block see: the context, and in a causal call the
+    // drafted tokens up to the block's first
+    const int open_end = p.mask ? kv : min(kv + uniform(first_row / p.group) + 1, u.keys);
     const int end = u.keys, tiles = (end + D::kKeys - 1) / D::kKeys;
     int tile0 = 0, tile1 = tiles, chunk = 0, chunks = 1;
     uint32_t range0 = range;  // the range that holds the unit's first tile
@@ -636,7 +639,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
             }
           }
           // scores, and what the row does not see
-          const bool open = key0 + 32 <= kv;  // the whole step is context
+          const bool open = key0 + 32 <= open_end;  // every row sees the whole step
           if (!open) {
 #pragma unroll 1
             for (int e = 0; e < 2 * MF; ++e) {
@@ -708,8 +711,9 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
             }
           };
           // A key hidden from a row has weight 0 there, but 0 times an infinity
-          // or NaN in its value is NaN: past the context, such values go through
-          // the product as 0, and are added to the rows that see them at the end.
+          // or NaN in its value is NaN: in a step that a row does not see in full,
+          // such values go through the product as 0, and are added to the rows that
+          // see them at the end.
           constexpr int kGroup = 4;
 #pragma unroll
           for (int d0 = 0; d0 < kDT; d0 += kGroup) {
@@ -922,7 +926,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
     }
     __syncthreads();  // LDS is free for the next item, but for `patch`
     if (__builtin_expect(last && patch != 0, 0)) {
-      // infinities and NaN among the values of the steps past the context, left out above
+      // infinities and NaN among the values of the steps not seen in full, left out above
       for (int e = tid; e < D::kRows * p.head_dim; e += kThreads) {
         const int row = first_row + e / p.head_dim, col = e % p.head_dim, tok = row / p.group;
         if (tok >= T) continue;
@@ -930,7 +934,7 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
             p.out + (q0 + tok) * p.o_token +
             (h * p.group + row - tok * p.group) * p.o_head) + col;
         float y = widen16<kFp16>(*op);
-        for (int j = -(kv & 31); j < end - kv; ++j) {  // from the first such step on
+        for (int j = (open_end & ~31) - kv; j < end - kv; ++j) {  // from the first such step on
           if (!(seen4(tok, j) & 1u)) continue;
           const int slot = min((kv + j) >> p.c.page_shift, p.t.max_pages - 1);
           const int64_t page = min(max(table[slot], 0), static_cast<int>(p.c.num_pages) - 1);

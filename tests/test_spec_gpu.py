@@ -318,6 +318,29 @@ def test_attention_values_with_infinities_in_sight(dtype):
     assert np.isfinite(rest).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("kv", [0, 70])
+def test_attention_causal_rows_before_an_infinity(dtype, kv):
+    """A causal call over several row blocks: an infinity in a drafted token's value and a NaN in
+    its key reach the rows from that token on and no other, whichever steps a block sees in full."""
+    s = Setup([kv], [200], 8, 2, 128, ps=16, dtype=dtype, seed=kv)
+    want = s.call()
+    s.check(want)
+    for tok in (0, 31, 32, 150, 199):
+        held = [x.clone() for x in s.dev]
+        page, at = int(s.table[0, (kv + tok) // 16]), (kv + tok) % 16
+        s.dev[1][page, at, 1, 5] = float("inf")
+        s.dev[0][page, at, 0, 7] = float("nan")
+        got = s.call()
+        assert torch.equal(got[:tok], want[:tok])
+        assert not torch.isfinite(got[tok, 4:, 5]).any()
+        assert torch.isnan(got[tok:, :4]).all()
+        keep = [c for c in range(128) if c != 5]
+        assert torch.equal(got[:, 4:][..., keep], want[:, 4:][..., keep])
+        s.dev = held
+    assert torch.equal(s.call(), want)
+
+
 def test_attention_large_scores():
     """Scores of thousands: the running maximum keeps the exponentials in range."""
     s = Setup([300], [4], 8, 2, 128, trees=[[-1, 0, 0, 1]], seed=3)
