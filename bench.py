@@ -89,12 +89,14 @@ def algo_counts(b, proj, emb_rank):
 
 
 def kernel_source_hash():
-    """First 16 hex digits of sha256 over the sources of libsgg_lora.so (the
-    planner, kernels and launch code; not the CPython call module)."""
+    """First 16 hex digits of sha256 over the LoRA sources of libsgg_lora.so
+    (the planner, kernels and launch code; not the CPython call modules, nor
+    the speculative decoding step, which no workload here runs)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "segmented_gather_gemm_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if not f.endswith((".hip", ".cpp", ".h")):
+        if not f.endswith((".hip", ".cpp", ".h")) or f.startswith("spec_") or \
+                f in ("tensorargs.cpp", "pycall_args.h"):
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
