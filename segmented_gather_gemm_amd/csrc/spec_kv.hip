@@ -386,7 +386,8 @@ __device__ __forceinline__ float scaled_e4m3(float x, float scale) {
 }
 
 // One workgroup per (request, token slab); 8 values of a key or value row a
-// thread and turn.
+// thread and turn.  (The rows are read next, by attention: stores past the L2
+// save 0.3 us here and cost a reader of 8 MB 3 us.)
 constexpr int kWriteThreads = 256;
 template <bool kFp16, bool kE4M3>
 __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(WriteParams p, KvView c) {
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(WriteParams p, 
       char* d = (is_v ? c.v : c.k) + page * st[1] + off * st[2] + h * st[3];
       const uint4 w = *reinterpret_cast<const uint4*>(s + 16 * d8);
       if constexpr (!kE4M3) {
-        store_past(d + 16 * d8, w);
+        *reinterpret_cast<uint4*>(d + 16 * d8) = w;
       } else {
         const float scale = (is_v ? p.v_scale : p.k_scale)[h];
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
