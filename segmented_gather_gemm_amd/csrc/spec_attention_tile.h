@@ -23,7 +23,7 @@
 // requests of one token behind up to 2048, 1.6 GB, 302 us, 5.3 TB/s; 64 requests
 // of 16 behind up to 4096, 0.82 GB, 162 us), and the vector unit's issue beside
 // the matrix unit where it has many (8 causal chunks of 512 tokens behind 1536,
-// 81 GFLOP, 131 us: a step of 32 rows by 32 keys takes a wave 34 matrix and about
+// 81 GFLOP, 118 us: a step of 32 rows by 32 keys takes a wave 34 matrix and about
 // 150 vector instructions, and the matrix unit is busy a third of the time).
 #pragma once
 

@@ -26,8 +26,8 @@
 // memory, and the chain of dependent round trips around it (nodes and their
 // probabilities 2 us, the walk 2, the row, the count 1, the tile and the token in
 // it 3 to 5; per rejection a meeting of 2 and a walk of 1; per new node its rows).
-// 64 requests of 16 candidates take 20 us for 33 MB, 48 of 9 drawn drafts 40 for
-// 49 MB, a vocabulary of 128256; one request of 5, 32000 values, 8.4.
+// 64 requests of 16 candidates take 20 us for 33 MB, 48 of 9 drawn drafts 38 for
+// 49 MB, a vocabulary of 128256; one request of 5, 32000 values, 8.6.
 #include "sgg_device.h"
 #include "spec_kernels.h"
 
