@@ -344,13 +344,11 @@ template <bool kFp16>
 constexpr u32x4_t kOnes = kFp16 ? u32x4_t{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}
                                 : u32x4_t{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 
-// The largest of three; a NaN gives way to a number.  (Plain fmaxf first
-// quiets each operand, an instruction of its own.)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
+// The largest of three, one instruction; a NaN gives way to a number.  (Scores come
+// from matrix instructions, and the waits between those and what reads them are the
+// compiler's: it keeps 8 states ahead of an instruction that it knows, and none ahead
+// of one written in inline assembly.)
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // Whether a 16-bit value of a packed pair is an infinity or NaN (bits of its exponent).
 template <bool kFp16>
