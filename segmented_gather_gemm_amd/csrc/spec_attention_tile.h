@@ -910,6 +910,10 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
               }
             }
           }
+          // The statistics of a slot are left by one wave and read by every wave that
+          // shares its rows: all have read before the next level writes into a slot of
+          // this one.
+          __syncthreads();
         }
         c = first;
       }
