@@ -53,6 +53,15 @@ def _workspace(t, nbytes):
     return ws.data_ptr(), ws.numel(), ws
 
 
+def _given_workspace(workspace, dev):
+    """(address, bytes) of a caller's workspace; the library checks its size and alignment."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError(f"workspace must be a tensor, got {type(workspace).__name__}")
+    if dev < 0 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the call's ROCm device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
 def _batch(q_indptr, rows, dev):
     """Requests of the batch, addresses of q_indptr and rows."""
     p = _i32("q_indptr", q_indptr, dev)
@@ -180,7 +189,9 @@ def spec_attention(q, k_cache, v_cache, page_table, kv_lens, q_indptr, max_q_len
     context and the drafted tokens of its row of ``tree_mask`` (spec_tree_mask; None: those up to
     itself).  ``max_q_len`` / ``max_kv_len`` bound the batch's tokens per request and keys per
     request (context and drafts); they shape the launch, not the result.  ``scale`` defaults to
-    head_dim ** -0.5.  Returns ``out`` (like q)."""
+    head_dim ** -0.5.  ``workspace``: a contiguous tensor on q's device that is zero on first use,
+    for calls that follow one another (None: scratch of the stream's own).  Returns ``out``
+    (like q)."""
     dev = q.get_device()
     c, (L, _, _, H, D) = _cache(k_cache, v_cache)
     qp, qt, qh = _heads("q", q)
@@ -207,8 +218,8 @@ def spec_attention(q, k_cache, v_cache, page_table, kv_lens, q_indptr, max_q_len
     if workspace is None:
         need = calls.spec_attention_workspace_bytes(bs, hq, H, D, code, max_q_len, max_kv_len)
         wp, wn, _held = _workspace(q, need)
-    else:   # the library checks its size
-        wp, wn = workspace.data_ptr(), workspace.numel()
+    else:
+        wp, wn = _given_workspace(workspace, dev)
     check(calls.spec_attention(
         qp, qt, qh, op, ot, oh, _CODES[q.dtype], hq, c, t, ld, width, num_rows,
         _i32("kv_lens", kv_lens, dev, num_rows), rp, ind, bs, n, mp, words,
@@ -225,7 +236,7 @@ def spec_verify(tokens, parents, q_indptr, target_probs, uniforms, final_uniform
     (path (bs, max_q_len): accepted nodes' local indexes, node 0 first, then -1; accept_lens
     (bs); next_tokens (bs)).  Row n of ``target_probs`` (tokens, vocab) float32 is the target's
     distribution after node n; row n of ``draft_probs`` the one its children were drawn from
-    (None: the candidates were chosen, not drawn)."""
+    (None: the candidates were chosen, not drawn).  ``workspace`` as in spec_attention."""
     dev = target_probs.get_device()
     bs, ind, _ = _batch(q_indptr, None, dev)
     n = tokens.numel()
@@ -241,8 +252,8 @@ def spec_verify(tokens, parents, q_indptr, target_probs, uniforms, final_uniform
     calls = spec_calls()
     if workspace is None:
         wp, wn, _held = _workspace(target_probs, calls.spec_verify_workspace_bytes(bs, V))
-    else:   # the library checks its size
-        wp, wn = workspace.data_ptr(), workspace.numel()
+    else:
+        wp, wn = _given_workspace(workspace, dev)
     check(calls.spec_verify(
         _i32("tokens", tokens, dev, n), _i32("parents", parents, dev, n), ind, bs, n,
         target_probs.data_ptr(), target_probs.stride(0) if n > 1 else V,

@@ -1,0 +1,30 @@
+"""Arguments of the speculative decoding calls on the GPU: refused before anything is enqueued."""
+
+import pytest
+import torch
+
+from test_spec_gpu import DEV, Setup, _verify_call, _verify_case, _verify_check, tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(64 << 20, dtype=torch.uint8), "strided", "expanded"],
+                         ids=["host", "strided", "expanded"])
+def test_workspace_refused(ws):
+    if isinstance(ws, str):
+        ws = torch.zeros(1 << 24, dtype=torch.uint8, device=DEV)[::2] if ws == "strided" else \
+            torch.zeros(1, dtype=torch.uint8, device=DEV).expand(1 << 24)
+    s = Setup([3000], [2], 2, 1, 64, trees=[tree(2, None, True)], seed=1)
+    with pytest.raises(ValueError, match="workspace"):
+        s.call(workspace=ws)
+    c = _verify_case([3, 2], 9000, True, 1)
+    with pytest.raises(ValueError, match="workspace"):
+        _verify_call(c, workspace=ws)
+
+
+def test_workspace_of_any_type_counts_its_bytes():
+    ws = torch.zeros(1 << 20, device=DEV)                   # 4 MiB of floats
+    s = Setup([3000], [2], 2, 1, 64, trees=[tree(2, None, True)], seed=1)
+    need = s.call()
+    assert torch.equal(s.call(workspace=ws), need)
+    _verify_check(_verify_case([3, 2], 9000, True, 1), workspace=ws)
