@@ -210,7 +210,7 @@ def spec_attention(q, k_cache, v_cache, page_table, kv_lens, q_indptr, max_q_len
     if tree_mask is not None:
         if tree_mask.dtype is not torch.int64 or tree_mask.get_device() != dev \
                 or tree_mask.dim() != 2 or tree_mask.shape[0] != n \
-                or not tree_mask.is_contiguous():
+                or not tree_mask.is_contiguous() or (n > 0 and tree_mask.shape[1] == 0):
             raise ValueError(f"tree_mask must be a contiguous int64 (tokens, words) tensor, got "
                              f"{tuple(tree_mask.shape)} {tree_mask.dtype}")
         mp, words = tree_mask.data_ptr(), tree_mask.shape[1]

@@ -28,3 +28,10 @@ def test_workspace_of_any_type_counts_its_bytes():
     need = s.call()
     assert torch.equal(s.call(workspace=ws), need)
     _verify_check(_verify_case([3, 2], 9000, True, 1), workspace=ws)
+
+
+def test_mask_of_no_words_is_refused():
+    """An empty tensor has no address, and no address stands for a causal call."""
+    s = Setup([30], [4], 2, 1, 64, trees=[tree(4, None, True)], seed=1)
+    with pytest.raises(ValueError, match="tree_mask"):
+        s.call(tree_mask=torch.zeros((4, 0), dtype=torch.int64, device=DEV))
