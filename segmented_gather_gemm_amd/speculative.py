@@ -99,6 +99,8 @@ def spec_kv_fork(k_cache, v_cache, page_table, page_counts, ref_counts, kv_lens,
     (int32 [2]): pages missing (not 0: nothing was done), pairs left alone."""
     dev = page_table.get_device()
     c, (_, P, _, _, _) = _cache(k_cache, v_cache)
+    if k_cache.get_device() != dev:
+        raise ValueError("the cache must be on the page table's device")
     t, ld, width, num_rows = _table(page_table, dev)
     n = src_rows.numel()
     if status is None:
