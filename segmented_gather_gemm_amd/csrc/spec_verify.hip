@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / kWave;
-constexpr int kVerifyNodes = 1024;  // nodes of a request that are visited
+constexpr int kVerifyNodes = 1024;  // nodes of a request in LDS, and rejected tokens of a node
 constexpr int kTile = 1024;         // values of a tile: 16 a lane of one wave
 constexpr int kParts = 64;          // workgroups of a request at most
 constexpr int kHold = 2;            // tiles whose values a wave keeps
@@ -93,13 +93,22 @@ struct __attribute__((packed, aligned(4))) Four {
   float x[4];
 };
 
+// Rejected tokens that the list of kVerifyNodes has no room for: those of children
+// of `node` among the request's nodes [first, end).
+struct Unlisted {
+  const int32_t* parents;
+  const int32_t* tokens;
+  int node, first, end;
+};
+
 template <bool kDraft>
 struct Row {
   const float* p;
   const float* q;  // kDraft
   double a;
   const int32_t* gone;  // rejected tokens (not kDraft)
-  int gone_n;
+  int gone_n;           // kVerifyNodes + 1: that many, and those of `rest`
+  const Unlisted* rest;
   int vocab;
 
   // Four values of the row for a lane whose values begin at v: the last four of
@@ -121,11 +130,20 @@ struct Row {
     }
     if (!kDraft) {
 #pragma unroll 1
-      for (int i = 0; i < gone_n; ++i) {
+      for (int i = 0; i < min(gone_n, kVerifyNodes); ++i) {
         const int hit = gone[i] - at;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (hit == k) w[k] = 0.0;
+      }
+      if (__builtin_expect(gone_n > kVerifyNodes, 0)) {
+#pragma unroll 1
+        for (int i = rest->first; i < rest->end; ++i) {
+          const int hit = rest->parents[i] == rest->node ? rest->tokens[i] - at : -1;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (hit == k) w[k] = 0.0;
+        }
       }
     }
   }
@@ -153,6 +171,23 @@ struct Row {
   }
 };
 
+// Node i of the request whose tokens begin at q0.
+struct Node {
+  int parent, token;  // parent: -1 for none
+  float px, qx, u;    // the token's probability in the rows of its parent
+};
+__device__ __forceinline__ Node node_at(const VerifyParams& p, int64_t q0, int i) {
+  Node x;
+  x.parent = p.parents[q0 + i];
+  x.token = p.tokens[q0 + i];
+  x.u = p.u[q0 + i];
+  if (x.parent < 0 || x.parent >= i) x.parent = -1;
+  const bool in = x.token >= 0 && x.token < p.vocab && x.parent >= 0;
+  x.px = in ? p.p[(q0 + x.parent) * p.ldp + x.token] : 0.0f;
+  x.qx = in && p.q ? p.q[(q0 + x.parent) * p.ldq + x.token] : 0.0f;
+  return x;
+}
+
 template <bool kDraft>
 __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(VerifyParams p) {
   __shared__ struct {
@@ -163,6 +198,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
     float u[kVerifyNodes];
   } s;
   __shared__ int32_t gone_of[kVerifyNodes];  // rejected tokens of the current node (no draft row)
+  __shared__ Unlisted rest;
   __shared__ double part[kVerifyWaves];
   __shared__ int cur, at, gone, path_len, state, stale, seen;
   __shared__ double a, mass;
@@ -172,9 +208,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
   const int r = blockIdx.x / p.parts, c = blockIdx.x % p.parts;
   const int64_t q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
   int32_t* path = p.path + r * p.ld_path;
-  const int n = q0 < 0 || q1 > p.num_tokens || q1 <= q0
-                    ? 0
-                    : static_cast<int>(q1 - q0 < kVerifyNodes ? q1 - q0 : kVerifyNodes);
+  const int n = q0 < 0 || q1 > p.num_tokens || q1 <= q0 ? 0 : static_cast<int>(q1 - q0);
   int32_t* counter = p.counters + r;
   double* partial = p.partials + static_cast<int64_t>(r) * 3 * p.parts;
   double* tile_sums = p.tile_sums + static_cast<int64_t>(r) * p.tiles;
@@ -188,17 +222,14 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
     }
     return;
   }
-  for (int i = tid; i < n; i += kVerifyThreads) {
-    int par = p.parents[q0 + i];
-    const int tok = p.tokens[q0 + i];
-    const float u = p.u[q0 + i];
-    if (par < 0 || par >= i) par = -1;
-    const bool in = tok >= 0 && tok < p.vocab && par >= 0;
-    s.parent[i] = par;
-    s.token[i] = tok;
-    s.px[i] = in ? p.p[(q0 + par) * p.ldp + tok] : 0.0f;
-    s.qx[i] = in && p.q ? p.q[(q0 + par) * p.ldq + tok] : 0.0f;
-    s.u[i] = u;
+  // (the nodes of a longer request past these are read where the walk meets them)
+  for (int i = tid; i < min(n, kVerifyNodes); i += kVerifyThreads) {
+    const Node x = node_at(p, q0, i);
+    s.parent[i] = x.parent;
+    s.token[i] = x.token;
+    s.px[i] = x.px;
+    s.qx[i] = x.qx;
+    s.u[i] = x.u;
   }
   if (tid == 0) {
     cur = 0, at = 1, gone = 0, path_len = 1, stale = 0;
@@ -218,6 +249,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
     // wave 0 walks on until a rejection needs the residual's mass, or the end
     if (wave == 0) {
       int node = cur, next = at, ng = gone, len = path_len, old = stale;
+      int unlisted = n;  // the first rejected child that `gone_of` has no room for (n: none)
       double aa = a, mm = mass;
       int st = 0;  // 1: at the end, 2: the mass of the residual is wanted
       // a node's numbers: of up to 64 nodes lane i holds node i
@@ -230,7 +262,10 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
         if (len < p.path_width) {
           for (int base = next & ~(kWave - 1); base < n && child < 0; base += kWave) {
             const int i = base + lane;
-            const int par = held ? parent_l : i < n ? s.parent[i] : -2;
+            const int par = held ? parent_l
+                            : i >= n ? -2
+                            : i < kVerifyNodes ? s.parent[i]
+                                               : p.parents[q0 + i];
             const unsigned long long hit = __ballot(i >= next && par == node);
             if (hit) child = base + __ffsll(hit) - 1;
           }
@@ -242,12 +277,19 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
           st = 2;
           next = child;
         } else {
-          const double px = weight(held ? lane_value(px_l, child) : s.px[child]);
-          const double u = held ? lane_value(u_l, child) : s.u[child];
-          const int token = held ? __builtin_amdgcn_readlane(token_l, child) : s.token[child];
+          const bool far = child >= kVerifyNodes;
+          Node x{};
+          if (far) x = node_at(p, q0, child);
+          const double px =
+              weight(held ? lane_value(px_l, child) : far ? x.px : s.px[child]);
+          const double u = held ? lane_value(u_l, child) : far ? x.u : s.u[child];
+          const int token = held ? __builtin_amdgcn_readlane(token_l, child)
+                            : far ? x.token
+                                  : s.token[child];
           bool ok;
           if (kDraft) {
-            const double qx = weight(held ? lane_value(qx_l, child) : s.qx[child]);
+            const double qx =
+                weight(held ? lane_value(qx_l, child) : far ? x.qx : s.qx[child]);
             ok = u * (mm * qx) < left_of(px, aa, qx);
             if (!ok) {
               aa += mm;
@@ -255,13 +297,23 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
             }
           } else {
             bool spent = false;
-            for (int k = 0; k < ng; ++k) spent |= gone_of[k] == token;
+            for (int k = 0; k < min(ng, kVerifyNodes); ++k) spent |= gone_of[k] == token;
+            for (int base = unlisted; base < child && !spent; base += kWave) {
+              const int i = base + lane;
+              spent = __ballot(i < child && p.parents[q0 + i] == node &&
+                               p.tokens[q0 + i] == token) != 0;
+            }
             ok = !spent && u * mm < px;
             if (!ok && !spent) {
               mm -= px;
-              if (lane == 0) gone_of[ng] = token;
-              __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-              ++ng;
+              if (ng < kVerifyNodes) {
+                if (lane == 0) gone_of[ng] = token;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                ++ng;
+              } else if (ng == kVerifyNodes) {
+                unlisted = child;
+                ++ng;
+              }
             }
           }
           next = child + 1;
@@ -270,12 +322,14 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
             ++len;
             node = child;
             ng = 0;
+            unlisted = n;
             aa = 0.0, mm = 1.0;
           }
         }
       }
       if (lane == 0) {
         cur = node, at = next, gone = ng, path_len = len, state = st, stale = 0;
+        if (!kDraft) rest = {p.parents + q0, p.tokens + q0, node, unlisted, next};
         a = aa, mass = mm;
       }
     }
@@ -285,7 +339,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
     // others not be seen to arrive, of each.
     const bool end = state == 1;
     const Row<kDraft> row{p.p + (q0 + cur) * p.ldp, kDraft ? p.q + (q0 + cur) * p.ldq : nullptr, a,
-                          gone_of, end ? gone : 0, static_cast<int>(p.vocab)};
+                          gone_of, end ? gone : 0, &rest, static_cast<int>(p.vocab)};
     // Slots of parts' sums, three rounds in turn; a sum lies there negated, so
     // that 0 is "not there".  The next round's slot is emptied before this round's
     // is filled: whoever has seen this round's sums sees that one empty.  (Its
@@ -451,7 +505,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
     return __builtin_amdgcn_readlane(token, who);
   };
   Row<kDraft> row{p.p + (q0 + cur) * p.ldp, kDraft ? p.q + (q0 + cur) * p.ldq : nullptr, a,
-                  gone_of, gone, static_cast<int>(p.vocab)};
+                  gone_of, gone, &rest, static_cast<int>(p.vocab)};
   int token = -1;
 #pragma unroll 1
   for (int turn = 0; token < 0 && turn < 2; ++turn) {
