@@ -25,8 +25,9 @@
  * max_pages <= ld_table entries in use, page_counts [num_rows] pages held,
  * kv_lens [num_rows] tokens held, ref_counts [num_pages].  A page is free iff
  * its count is 0 (or less); the lowest-numbered free pages are handed out
- * first.  Table entries past page_counts are left as they are.  A call that
- * names one row twice gives unspecified contents (and no fault).
+ * first.  Table entries past page_counts are left as they are, so they may name
+ * pages that other rows hold by now.  A call that names one row twice gives
+ * unspecified contents (and no fault).
  */
 #ifndef SGG_SPEC_H_
 #define SGG_SPEC_H_
@@ -106,6 +107,10 @@ int spec_kv_copy_pages(const SpecKvCache* cache, const int32_t* src_pages,
  * +-448 and rounded to nearest even (NaN stays NaN), with k_scale, v_scale
  * float32 [num_kv_heads].  Strides in elements, multiples of 8.  Tokens whose
  * position has no page (past max_pages, page id out of range) are skipped.
+ * spec_kv_write takes every table entry below max_pages for the row's own: for
+ * callers that know each position to have a page.  spec_kv_write_held skips
+ * tokens past the page_counts[row] pages that the row holds as well: after a
+ * resize that found pages missing, nothing is written into other rows' pages.
  */
 int spec_kv_write(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
                   int64_t v_head, int32_t dtype, const SpecKvCache* cache,
@@ -113,19 +118,32 @@ int spec_kv_write(const void* k, int64_t k_token, int64_t k_head, const void* v,
                   int32_t num_rows, const int32_t* kv_lens, const int32_t* rows,
                   const int32_t* q_indptr, int32_t bs, int64_t num_tokens, const float* k_scale,
                   const float* v_scale, void* stream);
+int spec_kv_write_held(const void* k, int64_t k_token, int64_t k_head, const void* v,
+                       int64_t v_token, int64_t v_head, int32_t dtype, const SpecKvCache* cache,
+                       const int32_t* page_table, int64_t ld_table, int32_t max_pages,
+                       int32_t num_rows, const int32_t* page_counts, const int32_t* kv_lens,
+                       const int32_t* rows, const int32_t* q_indptr, int32_t bs,
+                       int64_t num_tokens, const float* k_scale, const float* v_scale,
+                       void* stream);
 
 /*
  * spec_kv_compact -- in every layer, the token at position kv_len + path[r][j]
  * moves to kv_len + j, for j < accept_lens[r] (at most path_width), and
  * new_lens[r] = kv_len + accept_lens[r].  path rows ascend strictly (as
  * spec_verify gives them); entries that do not, or whose page is out of range,
- * are skipped.
+ * are skipped; by spec_kv_compact_held also those that lie or would come to lie
+ * past the page_counts[row] pages of the row (see spec_kv_write).
  */
 int spec_kv_compact(const SpecKvCache* cache, const int32_t* page_table, int64_t ld_table,
                     int32_t max_pages, int32_t num_rows, const int32_t* kv_lens,
                     const int32_t* rows, const int32_t* path, int64_t ld_path,
                     int32_t path_width, const int32_t* accept_lens, int32_t* new_lens,
                     int32_t bs, void* stream);
+int spec_kv_compact_held(const SpecKvCache* cache, const int32_t* page_table, int64_t ld_table,
+                         int32_t max_pages, int32_t num_rows, const int32_t* page_counts,
+                         const int32_t* kv_lens, const int32_t* rows, const int32_t* path,
+                         int64_t ld_path, int32_t path_width, const int32_t* accept_lens,
+                         int32_t* new_lens, int32_t bs, void* stream);
 
 /*
  * spec_tree_mask -- from the drafted tokens' parents (local index in the

@@ -118,7 +118,7 @@ int check_rows16(const void* p, int64_t token, int64_t head, int32_t head_dim, c
 
 sgg::KvRows rows_of(const int32_t* table, int64_t ld, int32_t max_pages, int32_t num_rows,
                     const int32_t* rows, const int32_t* kv_lens) {
-  return sgg::KvRows{const_cast<int32_t*>(table), ld, max_pages, num_rows, rows, kv_lens};
+  return sgg::KvRows{const_cast<int32_t*>(table), ld, max_pages, num_rows, rows, kv_lens, nullptr};
 }
 
 }  // namespace
@@ -253,13 +253,13 @@ extern "C" int spec_kv_copy_pages(const SpecKvCache* cache, const int32_t* src_p
                        "kv_copy_pages");
 }
 
-extern "C" int spec_kv_write(const void* k, int64_t k_token, int64_t k_head, const void* v,
-                             int64_t v_token, int64_t v_head, int32_t dtype,
-                             const SpecKvCache* cache, const int32_t* page_table,
-                             int64_t ld_table, int32_t max_pages, int32_t num_rows,
-                             const int32_t* kv_lens, const int32_t* rows,
-                             const int32_t* q_indptr, int32_t bs, int64_t num_tokens,
-                             const float* k_scale, const float* v_scale, void* stream) {
+namespace {
+
+int write_rows(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+               int64_t v_head, int32_t dtype, const SpecKvCache* cache, const int32_t* page_table,
+               int64_t ld_table, int32_t max_pages, int32_t num_rows, const int32_t* held,
+               const int32_t* kv_lens, const int32_t* rows, const int32_t* q_indptr, int32_t bs,
+               int64_t num_tokens, const float* k_scale, const float* v_scale, void* stream) {
   sgg::KvView c{};
   SGG_TRY(check_cache(cache, &c));
   SGG_TRY(check_table(page_table, ld_table, max_pages, num_rows));
@@ -281,6 +281,7 @@ extern "C" int spec_kv_write(const void* k, int64_t k_token, int64_t k_head, con
   p.v = static_cast<const char*>(v);
   p.kt = 2 * k_token, p.kh = 2 * k_head, p.vt = 2 * v_token, p.vh = 2 * v_head;
   p.t = rows_of(page_table, ld_table, max_pages, num_rows, rows, kv_lens);
+  p.t.held = held;
   p.q_indptr = q_indptr;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
@@ -291,11 +292,10 @@ extern "C" int spec_kv_write(const void* k, int64_t k_token, int64_t k_head, con
       sgg::launch_kv_write(p, c, dtype, e4m3, static_cast<hipStream_t>(stream)), "kv_write");
 }
 
-extern "C" int spec_kv_compact(const SpecKvCache* cache, const int32_t* page_table,
-                               int64_t ld_table, int32_t max_pages, int32_t num_rows,
-                               const int32_t* kv_lens, const int32_t* rows, const int32_t* path,
-                               int64_t ld_path, int32_t path_width, const int32_t* accept_lens,
-                               int32_t* new_lens, int32_t bs, void* stream) {
+int compact_rows(const SpecKvCache* cache, const int32_t* page_table, int64_t ld_table,
+                 int32_t max_pages, int32_t num_rows, const int32_t* held, const int32_t* kv_lens,
+                 const int32_t* rows, const int32_t* path, int64_t ld_path, int32_t path_width,
+                 const int32_t* accept_lens, int32_t* new_lens, int32_t bs, void* stream) {
   sgg::KvView c{};
   SGG_TRY(check_cache(cache, &c));
   SGG_TRY(check_table(page_table, ld_table, max_pages, num_rows));
@@ -309,6 +309,7 @@ extern "C" int spec_kv_compact(const SpecKvCache* cache, const int32_t* page_tab
             "%d requests of %d layers are above the grid", bs, c.layers);
   sgg::CompactParams p{};
   p.t = rows_of(page_table, ld_table, max_pages, num_rows, rows, kv_lens);
+  p.t.held = held;
   p.path = path;
   p.ld_path = ld_path;
   p.accept = accept_lens;
@@ -317,6 +318,54 @@ extern "C" int spec_kv_compact(const SpecKvCache* cache, const int32_t* page_tab
   p.path_width = path_width;
   return launch_status(sgg::launch_kv_compact(p, c, static_cast<hipStream_t>(stream)),
                        "kv_compact");
+}
+
+}  // namespace
+
+extern "C" int spec_kv_write(const void* k, int64_t k_token, int64_t k_head, const void* v,
+                             int64_t v_token, int64_t v_head, int32_t dtype,
+                             const SpecKvCache* cache, const int32_t* page_table,
+                             int64_t ld_table, int32_t max_pages, int32_t num_rows,
+                             const int32_t* kv_lens, const int32_t* rows,
+                             const int32_t* q_indptr, int32_t bs, int64_t num_tokens,
+                             const float* k_scale, const float* v_scale, void* stream) {
+  return write_rows(k, k_token, k_head, v, v_token, v_head, dtype, cache, page_table, ld_table,
+                    max_pages, num_rows, nullptr, kv_lens, rows, q_indptr, bs, num_tokens, k_scale,
+                    v_scale, stream);
+}
+
+extern "C" int spec_kv_write_held(const void* k, int64_t k_token, int64_t k_head, const void* v,
+                                  int64_t v_token, int64_t v_head, int32_t dtype,
+                                  const SpecKvCache* cache, const int32_t* page_table,
+                                  int64_t ld_table, int32_t max_pages, int32_t num_rows,
+                                  const int32_t* page_counts, const int32_t* kv_lens,
+                                  const int32_t* rows, const int32_t* q_indptr, int32_t bs,
+                                  int64_t num_tokens, const float* k_scale, const float* v_scale,
+                                  void* stream) {
+  SGG_CHECK(page_counts != nullptr, SGG_ERR_INVALID, "page_counts is NULL");
+  return write_rows(k, k_token, k_head, v, v_token, v_head, dtype, cache, page_table, ld_table,
+                    max_pages, num_rows, page_counts, kv_lens, rows, q_indptr, bs, num_tokens,
+                    k_scale, v_scale, stream);
+}
+
+extern "C" int spec_kv_compact(const SpecKvCache* cache, const int32_t* page_table,
+                               int64_t ld_table, int32_t max_pages, int32_t num_rows,
+                               const int32_t* kv_lens, const int32_t* rows, const int32_t* path,
+                               int64_t ld_path, int32_t path_width, const int32_t* accept_lens,
+                               int32_t* new_lens, int32_t bs, void* stream) {
+  return compact_rows(cache, page_table, ld_table, max_pages, num_rows, nullptr, kv_lens, rows,
+                      path, ld_path, path_width, accept_lens, new_lens, bs, stream);
+}
+
+extern "C" int spec_kv_compact_held(const SpecKvCache* cache, const int32_t* page_table,
+                                    int64_t ld_table, int32_t max_pages, int32_t num_rows,
+                                    const int32_t* page_counts, const int32_t* kv_lens,
+                                    const int32_t* rows, const int32_t* path, int64_t ld_path,
+                                    int32_t path_width, const int32_t* accept_lens,
+                                    int32_t* new_lens, int32_t bs, void* stream) {
+  SGG_CHECK(page_counts != nullptr, SGG_ERR_INVALID, "page_counts is NULL");
+  return compact_rows(cache, page_table, ld_table, max_pages, num_rows, page_counts, kv_lens, rows,
+                      path, ld_path, path_width, accept_lens, new_lens, bs, stream);
 }
 
 extern "C" int spec_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t bs,

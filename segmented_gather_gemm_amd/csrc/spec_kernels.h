@@ -36,6 +36,7 @@ struct KvRows {
   int32_t max_pages, num_rows;
   const int32_t* rows;     // cache row of request r (null: r)
   const int32_t* kv_lens;  // by cache row
+  const int32_t* held;     // pages that each cache row holds (null: max_pages)
 };
 
 struct ResizeParams {

@@ -38,12 +38,18 @@ __device__ __forceinline__ int row_of(const KvRows& t, int i) {
   return r >= 0 && r < t.num_rows ? r : -1;
 }
 
-// Page of position `pos` in cache row `row`, or -1 where there is none.
-__device__ __forceinline__ int64_t page_at(const KvRows& t, int row, int64_t pos, int shift,
-                                           int64_t num_pages) {
+// Pages of cache row `row` that may be written: entries past those that a row
+// holds may name pages of other rows.
+__device__ __forceinline__ int slots_of(const KvRows& t, int row) {
+  return t.held ? min(t.held[row], t.max_pages) : t.max_pages;
+}
+
+// Page of position `pos` in cache row `row` of `slots` pages, or -1 where there is none.
+__device__ __forceinline__ int64_t page_at(const KvRows& t, int row, int slots, int64_t pos,
+                                           int shift, int64_t num_pages) {
   if (pos < 0) return -1;
   const int64_t slot = pos >> shift;
-  if (slot >= t.max_pages) return -1;
+  if (slot >= slots) return -1;
   const int64_t page = t.table[row * t.ld + slot];
   return page >= 0 && page < num_pages ? page : -1;
 }
@@ -396,10 +402,11 @@ __global__ __launch_bounds__(kWriteThreads) void kv_write_kernel(WriteParams p, 
   const int row = row_of(p.t, r);
   if (row < 0 || q0 < 0 || q1 > p.num_tokens) return;
   const int64_t kv = p.t.kv_lens[row];
+  const int slots = slots_of(p.t, row);
   const int per_row = p.head_dim / 8, per = per_row * c.heads;
   for (int64_t i = blockIdx.y; i < q1 - q0; i += gridDim.y) {
     const int64_t pos = kv + i;
-    const int64_t page = page_at(p.t, row, pos, c.page_shift, c.num_pages);
+    const int64_t page = page_at(p.t, row, slots, pos, c.page_shift, c.num_pages);
     if (page < 0) continue;
     const int64_t off = pos & ((int64_t{1} << c.page_shift) - 1);
     for (int e = threadIdx.x; e < 2 * per; e += kWriteThreads) {
@@ -452,6 +459,7 @@ __global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactPara
   const int row = row_of(p.t, r);
   const int n = min(max(p.accept[r], 0), p.path_width);
   const int64_t kv = row < 0 ? 0 : p.t.kv_lens[row];
+  const int slots = row < 0 ? 0 : slots_of(p.t, row);
   if (threadIdx.x == 0 && g == 0) p.new_lens[r] = static_cast<int32_t>(kv + n);
   if (row < 0) return;
   const int32_t* path = p.path + r * p.ld_path;
@@ -477,8 +485,8 @@ __global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactPara
       bool move = j < n && i > j && i > before;
       int4 m{};
       if (move) {
-        const int64_t from = page_at(p.t, row, kv + i, c.page_shift, c.num_pages);
-        const int64_t to = page_at(p.t, row, kv + j, c.page_shift, c.num_pages);
+        const int64_t from = page_at(p.t, row, slots, kv + i, c.page_shift, c.num_pages);
+        const int64_t to = page_at(p.t, row, slots, kv + j, c.page_shift, c.num_pages);
         move = from >= 0 && to >= 0;
         m = make_int4(static_cast<int>(from), static_cast<int>((kv + i) & low),
                       static_cast<int>(to), static_cast<int>((kv + j) & low));

@@ -13,7 +13,9 @@
 #define SIG_spec_kv_fork "ppliipppppipplp"
 #define SIG_spec_kv_copy_pages "ppplp"
 #define SIG_spec_kv_write "pllpllippliipppilppp"
+#define SIG_spec_kv_write_held "pllpllippliippppilppp"
 #define SIG_spec_kv_compact "ppliippplippip"
+#define SIG_spec_kv_compact_held "ppliipppplippip"
 #define SIG_spec_tree_mask "ppilppipipp"
 #define SIG_spec_attention_workspace_bytes "iiiiiil"
 #define SIG_spec_attention "pllplliippliipppilpifppilplp"
@@ -57,6 +59,23 @@ static PyObject* py_spec_kv_compact(PyObject* self, PyObject* const* args, Py_ss
       (const SpecKvCache*)P(0), (const int32_t*)P(1), L(2), I(3), I(4), (const
       int32_t*)P(5), (const int32_t*)P(6), (const int32_t*)P(7), L(8), I(9), (const
       int32_t*)P(10), (int32_t*)P(11), I(12), P(13)));
+}
+
+static PyObject* py_spec_kv_write_held(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_kv_write_held);
+  RETURN_INT(spec_kv_write_held(
+      P(0), L(1), L(2), P(3), L(4), L(5), I(6), (const SpecKvCache*)P(7), (const
+      int32_t*)P(8), L(9), I(10), I(11), (const int32_t*)P(12), (const int32_t*)P(13),
+      (const int32_t*)P(14), (const int32_t*)P(15), I(16), L(17), (const float*)P(18), (const
+      float*)P(19), P(20)));
+}
+
+static PyObject* py_spec_kv_compact_held(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_kv_compact_held);
+  RETURN_INT(spec_kv_compact_held(
+      (const SpecKvCache*)P(0), (const int32_t*)P(1), L(2), I(3), I(4), (const
+      int32_t*)P(5), (const int32_t*)P(6), (const int32_t*)P(7), (const int32_t*)P(8), L(9),
+      I(10), (const int32_t*)P(11), (int32_t*)P(12), I(13), P(14)));
 }
 
 static PyObject* py_spec_tree_mask(PyObject* self, PyObject* const* args, Py_ssize_t n) {
@@ -107,7 +126,9 @@ static PyMethodDef methods[] = {
     ENTRY(spec_kv_fork),
     ENTRY(spec_kv_copy_pages),
     ENTRY(spec_kv_write),
+    ENTRY(spec_kv_write_held),
     ENTRY(spec_kv_compact),
+    ENTRY(spec_kv_compact_held),
     ENTRY(spec_tree_mask),
     ENTRY(spec_attention_workspace_bytes),
     ENTRY(spec_attention),
@@ -132,7 +153,9 @@ PyMODINIT_FUNC PyInit__sggspec(void) {
       {"spec_kv_fork", SIG_spec_kv_fork},
       {"spec_kv_copy_pages", SIG_spec_kv_copy_pages},
       {"spec_kv_write", SIG_spec_kv_write},
+      {"spec_kv_write_held", SIG_spec_kv_write_held},
       {"spec_kv_compact", SIG_spec_kv_compact},
+      {"spec_kv_compact_held", SIG_spec_kv_compact_held},
       {"spec_tree_mask", SIG_spec_tree_mask},
       {"spec_attention_workspace_bytes", SIG_spec_attention_workspace_bytes},
       {"spec_attention", SIG_spec_attention},

@@ -125,9 +125,12 @@ def spec_kv_copy_pages(k_cache, v_cache, src_pages, dst_pages):
 
 
 def spec_kv_write(k, v, k_cache, v_cache, page_table, kv_lens, q_indptr, rows=None, k_scale=None,
-                  v_scale=None):
+                  v_scale=None, page_counts=None):
     """Keys and values (tokens, kv heads, head_dim) of one layer into that layer's cache, token i
-    of request r at position kv_lens[row] + i.  A float8_e4m3fn cache takes x / scale[head]."""
+    of request r at position kv_lens[row] + i.  A float8_e4m3fn cache takes x / scale[head].
+    With ``page_counts`` (rows of the table) tokens past the pages that their row holds are
+    skipped; without it every position has to have a page, for table entries past a row's count
+    may name other rows' pages."""
     dev = k_cache.get_device()
     c, (_, _, _, H, D) = _cache(k_cache, v_cache)
     kp, kt, kh = _heads("k", k)
@@ -140,17 +143,22 @@ def spec_kv_write(k, v, k_cache, v_cache, page_table, kv_lens, q_indptr, rows=No
         raise ValueError("k and v must be on the cache's device")
     t, ld, width, num_rows = _table(page_table, dev)
     bs, ind, rp = _batch(q_indptr, rows, dev)
-    check(spec_calls().spec_kv_write(
-        kp, kt, kh, vp, vt, vh, _CODES[k.dtype], c, t, ld, width, num_rows,
-        _i32("kv_lens", kv_lens, dev, num_rows), rp, ind, bs, n,
-        0 if k_scale is None else _f32("k_scale", k_scale, dev, H),
-        0 if v_scale is None else _f32("v_scale", v_scale, dev, H), _stream(k_cache)))
+    new = (kp, kt, kh, vp, vt, vh, _CODES[k.dtype], c, t, ld, width, num_rows)
+    batch = (_i32("kv_lens", kv_lens, dev, num_rows), rp, ind, bs, n,
+             0 if k_scale is None else _f32("k_scale", k_scale, dev, H),
+             0 if v_scale is None else _f32("v_scale", v_scale, dev, H), _stream(k_cache))
+    if page_counts is None:
+        check(spec_calls().spec_kv_write(*new, *batch))
+    else:
+        check(spec_calls().spec_kv_write_held(
+            *new, _i32("page_counts", page_counts, dev, num_rows), *batch))
 
 
 def spec_kv_compact(k_cache, v_cache, page_table, kv_lens, path, accept_lens, rows=None,
-                    new_lens=None):
+                    new_lens=None, page_counts=None):
     """After a verification, in every layer, the accepted tokens' rows move together: position
-    kv_len + path[r, j] to kv_len + j.  Returns the requests' new lengths (bs)."""
+    kv_len + path[r, j] to kv_len + j.  ``page_counts`` as in spec_kv_write.  Returns the requests'
+    new lengths (bs)."""
     dev = k_cache.get_device()
     c, _ = _cache(k_cache, v_cache)
     t, ld, width, num_rows = _table(page_table, dev)
@@ -159,11 +167,16 @@ def spec_kv_compact(k_cache, v_cache, page_table, kv_lens, path, accept_lens, ro
     bs, w = path.shape
     if new_lens is None:
         new_lens = _new_i32(k_cache, bs)
-    check(spec_calls().spec_kv_compact(
-        c, t, ld, width, num_rows, _i32("kv_lens", kv_lens, dev, num_rows),
-        0 if rows is None else _i32("rows", rows, dev, bs), _i32("path", path, dev), w, w,
-        _i32("accept_lens", accept_lens, dev, bs), _i32("new_lens", new_lens, dev, bs), bs,
-        _stream(k_cache)))
+    table = (c, t, ld, width, num_rows)
+    batch = (_i32("kv_lens", kv_lens, dev, num_rows),
+             0 if rows is None else _i32("rows", rows, dev, bs), _i32("path", path, dev), w, w,
+             _i32("accept_lens", accept_lens, dev, bs), _i32("new_lens", new_lens, dev, bs), bs,
+             _stream(k_cache))
+    if page_counts is None:
+        check(spec_calls().spec_kv_compact(*table, *batch))
+    else:
+        check(spec_calls().spec_kv_compact_held(
+            *table, _i32("page_counts", page_counts, dev, num_rows), *batch))
     return new_lens
 
 
@@ -283,6 +296,11 @@ class PagedKVCache:
     (max_rows, max_pages_per_row), ``page_counts``, ``kv_lens`` (max_rows) and ``ref_counts``
     (pages) are int32.  The float8_e4m3fn cache has ``k_scale`` / ``v_scale`` (layers, kv heads),
     one unless set.
+
+    Pages can run out: ``status[0]`` of ``reserve`` then counts the missing ones, and no row has
+    grown.  Nothing is written past the pages that a row holds, so the other rows keep their
+    contents; the results of the rows that needed pages are worthless, and the step is not to be
+    committed for them: look at the status before ``commit``, make room and reserve again.
     """
 
     def __init__(self, num_layers, num_pages, page_size, num_kv_heads, head_dim, max_rows,
@@ -328,7 +346,7 @@ class PagedKVCache:
 
     def write(self, layer, k, v, q_indptr, rows=None):
         spec_kv_write(k, v, self.k[layer], self.v[layer], self.page_table, self.kv_lens,
-                      q_indptr, rows, **self._scales(layer))
+                      q_indptr, rows, page_counts=self.page_counts, **self._scales(layer))
 
     def attention(self, layer, q, q_indptr, max_q_len, max_kv_len, tree_mask=None, rows=None,
                   scale=None, out=None):
@@ -339,7 +357,7 @@ class PagedKVCache:
     def compact(self, path, accept_lens, rows=None):
         """Moves the accepted rows together; returns the lengths to ``commit``."""
         return spec_kv_compact(self.k, self.v, self.page_table, self.kv_lens, path, accept_lens,
-                               rows)
+                               rows, page_counts=self.page_counts)
 
 
 __all__ = ["PagedKVCache", "spec_attention", "spec_kv_compact", "spec_kv_copy_pages",
