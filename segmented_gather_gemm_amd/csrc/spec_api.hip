@@ -107,12 +107,11 @@ int check_tokens(int64_t num_tokens) {
   return SGG_OK;
 }
 
-int check_rows16(const void* p, int64_t token, int64_t head, int32_t head_dim, const char* what) {
+int check_rows16(const void* p, int64_t token, int64_t head, const char* what) {
   SGG_CHECK(p != nullptr, SGG_ERR_INVALID, "%s is NULL", what);
   SGG_CHECK(token >= 0 && head >= 0, SGG_ERR_INVALID, "%s strides must not be negative", what);
   SGG_CHECK(token % 8 == 0 && head % 8 == 0 && sgg::aligned16(p), SGG_ERR_UNSUPPORTED,
             "%s must be 16-byte aligned with strides in multiples of 8", what);
-  (void)head_dim;
   return SGG_OK;
 }
 
@@ -142,7 +141,7 @@ AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head
                      int32_t cache_bytes, int32_t max_q_len, int64_t max_kv_len) {
   AttnShape s{};
   const int64_t rows = static_cast<int64_t>(max_q_len) * (q_heads / kv_heads);
-  int64_t resident = 256;  // workgroups that the GPU holds at once
+  int64_t resident = 256;  // workgroups that the GPU holds at once: 512 at most
   s.padded_dim = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
   s.nw = 4;
   if (s.padded_dim == 256) {
@@ -171,6 +170,7 @@ AttnShape attn_shape(int32_t bs, int32_t q_heads, int32_t kv_heads, int32_t head
     int64_t n = resident / kv_heads;
     if (n > most) n = most;
     s.ranges = static_cast<int32_t>(n < 1 ? 1 : n);
+    // (at most 2 * resident, far below kJoinSlots)
     if (s.ranges > 1) s.slots = 2 * s.ranges * static_cast<int64_t>(kv_heads);
     // (the kernel may take the batch by units)
     s.grid = (units > s.ranges ? units : s.ranges) * kv_heads;
@@ -273,8 +273,8 @@ int write_rows(const void* k, int64_t k_token, int64_t k_head, const void* v, in
   SGG_CHECK(!e4m3 || (k_scale && v_scale), SGG_ERR_INVALID,
             "an e4m3 cache needs k_scale and v_scale");
   if (bs == 0 || num_tokens == 0) return sgg::ok();
-  SGG_TRY(check_rows16(k, k_token, k_head, cache->head_dim, "k"));
-  SGG_TRY(check_rows16(v, v_token, v_head, cache->head_dim, "v"));
+  SGG_TRY(check_rows16(k, k_token, k_head, "k"));
+  SGG_TRY(check_rows16(v, v_token, v_head, "v"));
   SGG_CHECK(kv_lens && q_indptr, SGG_ERR_INVALID, "kv_lens or q_indptr is NULL");
   sgg::WriteParams p{};
   p.k = static_cast<const char*>(k);
@@ -453,8 +453,8 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   SGG_CHECK((reinterpret_cast<uintptr_t>(tree_mask) & 7) == 0, SGG_ERR_UNSUPPORTED,
             "tree_mask must be 8-byte aligned");
   if (bs == 0 || num_tokens == 0) return sgg::ok();
-  SGG_TRY(check_rows16(q, q_token, q_head, cache->head_dim, "q"));
-  SGG_TRY(check_rows16(out, out_token, out_head, cache->head_dim, "out"));
+  SGG_TRY(check_rows16(q, q_token, q_head, "q"));
+  SGG_TRY(check_rows16(out, out_token, out_head, "out"));
   SGG_CHECK(kv_lens && q_indptr, SGG_ERR_INVALID, "kv_lens or q_indptr is NULL");
   const sgg::AttnShape s =
       sgg::attn_shape(bs, num_q_heads, cache->num_kv_heads, cache->head_dim, e4m3 ? 1 : 2,
@@ -464,8 +464,6 @@ extern "C" int spec_attention(const void* q, int64_t q_token, int64_t q_head, vo
   SGG_CHECK(workspace_bytes >= need, SGG_ERR_CAPACITY,
             "workspace of %" PRId64 " bytes, the call needs %" PRId64, workspace_bytes, need);
   SGG_CHECK(sgg::aligned16(workspace), SGG_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
-  SGG_CHECK(s.slots <= sgg::kJoinSlots, SGG_ERR_UNSUPPORTED,
-            "%d kv heads are above %d", cache->num_kv_heads, sgg::kJoinSlots / 4);
   SGG_CHECK(num_tokens * (num_q_heads / cache->num_kv_heads) < (1 << 30), SGG_ERR_UNSUPPORTED,
             "%" PRId64 " tokens of %d heads a kv head are 2^30 rows or more", num_tokens,
             num_q_heads / cache->num_kv_heads);

@@ -286,11 +286,6 @@ __device__ __forceinline__ void wait_vm() {
   static_assert(N < 64, "vmcnt holds 6 bits");
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void wait_lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // Shape constants of an instance: NW waves, WR of them over the rows, and a
 // ring of NST stages of keys and values.
@@ -517,7 +512,9 @@ __global__ __launch_bounds__(NW* kWave, (kAttnWavesPerSimd<DP, MF>)) void attent
         }
       }
     };
-    // wait until at most n tiles of this wave's loads are under way
+    // wait until at most n tiles of this wave's loads are under way, and at most two: a
+    // wave of a ring of four that owns its keys could leave three, which gains nothing
+    // (two documents of 100003 keys in 8 bits 85 us both ways)
     auto wait_tiles = [&](int n) {
       if (n <= 0) wait_vm<0>();
       else if (n == 1) wait_vm<2 * D::kLoads>();

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
   __shared__ int32_t gone_of[kVerifyNodes];  // rejected tokens of the current node (no draft row)
   __shared__ Unlisted rest;
   __shared__ double part[kVerifyWaves];
-  __shared__ int cur, at, gone, path_len, state, stale, seen;
+  __shared__ int cur, at, gone, path_len, state, seen;
   __shared__ double a, mass;
   __shared__ double parts_of_round[kWave];
   const int tid = threadIdx.x, lane = tid % kWave;
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
     s.u[i] = x.u;
   }
   if (tid == 0) {
-    cur = 0, at = 1, gone = 0, path_len = 1, stale = 0;
+    cur = 0, at = 1, gone = 0, path_len = 1;
     a = 0.0, mass = 1.0;
     if (c == 0) path[0] = 0;
   }
@@ -248,7 +248,8 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
   while (true) {
     // wave 0 walks on until a rejection needs the residual's mass, or the end
     if (wave == 0) {
-      int node = cur, next = at, ng = gone, len = path_len, old = stale;
+      int node = cur, next = at, ng = gone, len = path_len;
+      bool old = false;  // the residual's mass is of an earlier rejection
       int unlisted = n;  // the first rejected child that `gone_of` has no room for (n: none)
       double aa = a, mm = mass;
       int st = 0;  // 1: at the end, 2: the mass of the residual is wanted
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
             ok = u * (mm * qx) < left_of(px, aa, qx);
             if (!ok) {
               aa += mm;
-              old = 1;
+              old = true;
             }
           } else {
             bool spent = false;
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(kVerifyThreads, kDraft ? 2 : 4) void verify_kernel(
         }
       }
       if (lane == 0) {
-        cur = node, at = next, gone = ng, path_len = len, state = st, stale = 0;
+        cur = node, at = next, gone = ng, path_len = len, state = st;
         if (!kDraft) rest = {p.parents + q0, p.tokens + q0, node, unlisted, next};
         a = aa, mass = mm;
       }
