@@ -82,7 +82,9 @@ int spec_kv_resize(int32_t* page_table, int64_t ld_table, int32_t max_pages, int
  * src_rows[i]: the full pages are shared (count + 1), the partial last page is
  * copied into a fresh one in every layer, so that both rows may go on.  A dst
  * row has to hold no page and must be neither a dst twice nor a src row of the
- * same call.
+ * same call.  A row that is cut back to an end inside a shared page must not be
+ * written there (the other rows read it): fork it after the cut, which gives the
+ * new row a page of its own for its end, and release it.
  *   workspace: 12 * n bytes.  status as above: [0] pages missing (then nothing
  *   was done), [1] pairs left alone (row out of range or equal, dst not empty,
  *   src holding fewer pages than its length needs).
@@ -170,6 +172,8 @@ int spec_tree_mask(const int32_t* parents, const int32_t* q_indptr, int32_t bs,
  *   Key j of request r, j < kv_len + T_r, is seen by token i if j < kv_len or
  *   bit j - kv_len of its mask row is set (tree_mask NULL: if j - kv_len <= i).
  *   out = sum_j softmax_j(scale * q.k_j) v_j; a token that sees no key gets 0.
+ *   Scores, maxima and sums are in 32 bits; the weights exp(s_j - m) are rounded to
+ *   q's type for the product with v, and their sum is taken of the rounded ones.
  *   Keys outside the mask have no part in it, whatever their rows hold.  Page
  *   ids outside the pool are read as the nearest page inside.
  *   max_q_len, max_kv_len (context and drafted tokens together): bounds that

@@ -95,7 +95,8 @@ def spec_kv_resize(page_table, page_counts, ref_counts, rows, new_lens, page_siz
 def spec_kv_fork(k_cache, v_cache, page_table, page_counts, ref_counts, kv_lens, src_rows,
                  dst_rows, status=None):
     """Row dst_rows[i], which holds no page, goes on from row src_rows[i]: full pages are shared,
-    the partial last page is copied into a fresh one in every layer.  Returns ``status``
+    the partial last page is copied into a fresh one in every layer.  A row that is cut back into a
+    shared page is not to be written there: fork it then, and release it.  Returns ``status``
     (int32 [2]): pages missing (not 0: nothing was done), pairs left alone."""
     dev = page_table.get_device()
     c, (_, P, _, _, _) = _cache(k_cache, v_cache)
@@ -203,7 +204,8 @@ def spec_attention(q, k_cache, v_cache, page_table, kv_lens, q_indptr, max_q_len
     holds their own keys and values already (spec_kv_write).  Token i of a request sees its
     context and the drafted tokens of its row of ``tree_mask`` (spec_tree_mask; None: those up to
     itself).  ``max_q_len`` / ``max_kv_len`` bound the batch's tokens per request and keys per
-    request (context and drafts); they shape the launch, not the result.  ``scale`` defaults to
+    request (context and drafts); they shape the launch, not the result.  The softmax's weights are
+    rounded to q's type for the product with the values, all else is float32.  ``scale`` defaults to
     head_dim ** -0.5.  ``workspace``: a contiguous tensor on q's device that is zero on first use,
     for calls that follow one another (None: scratch of the stream's own).  Returns ``out``
     (like q)."""
