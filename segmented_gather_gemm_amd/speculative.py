@@ -133,7 +133,10 @@ def spec_kv_write(k, v, k_cache, v_cache, page_table, kv_lens, q_indptr, rows=No
     skipped; without it every position has to have a page, for table entries past a row's count
     may name other rows' pages."""
     dev = k_cache.get_device()
-    c, (_, _, _, H, D) = _cache(k_cache, v_cache)
+    c, (L, _, _, H, D) = _cache(k_cache, v_cache)
+    if L != 1:
+        raise ValueError(f"k and v belong to one layer, the cache has {L}: "
+                         f"{tuple(k_cache.shape)}")
     kp, kt, kh = _heads("k", k)
     vp, vt, vh = _heads("v", v)
     n = k.shape[0]

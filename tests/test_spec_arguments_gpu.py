@@ -3,7 +3,8 @@
 import pytest
 import torch
 
-from test_spec_gpu import DEV, Setup, _verify_call, _verify_case, _verify_check, tree
+from test_spec_gpu import (DEV, Setup, _i32, _sgg, _verify_call, _verify_case, _verify_check,
+                           tree)
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,15 @@ def test_mask_of_no_words_is_refused():
     s = Setup([30], [4], 2, 1, 64, trees=[tree(4, None, True)], seed=1)
     with pytest.raises(ValueError, match="tree_mask"):
         s.call(tree_mask=torch.zeros((4, 0), dtype=torch.int64, device=DEV))
+
+
+def test_write_takes_one_layer():
+    """A cache of several layers is not taken for its first one."""
+    k = torch.zeros((2, 3, 4, 1, 64), dtype=torch.bfloat16, device=DEV)
+    x = torch.ones((2, 1, 64), dtype=torch.bfloat16, device=DEV)
+    args = (_i32([[1, 2]]), _i32([0]), _i32([0, 2]))
+    with pytest.raises(ValueError, match="layer"):
+        _sgg().spec_kv_write(x, x, k, k.clone(), *args)
+    assert not k.any()
+    _sgg().spec_kv_write(x, x, k[1:], k.clone()[1:], *args)
+    assert k[1, 1, :2].eq(1).all() and k.sum() == 128
