@@ -20,11 +20,13 @@
 // as they leave LDS; the scales go to the scores and to the result.
 //
 // What bounds it: the read of keys and values while a request has few rows (256
-// requests of one token behind up to 2048, 1.6 GB, 302 us, 5.3 TB/s; 64 requests
-// of 16 behind up to 4096, 0.82 GB, 162 us), and the vector unit's issue beside
-// the matrix unit where it has many (8 causal chunks of 512 tokens behind 1536,
-// 81 GFLOP, 118 us: a step of 32 rows by 32 keys takes a wave 34 matrix and about
-// 150 vector instructions, and the matrix unit is busy a third of the time).
+// requests of one token behind up to 2048, 1.6 GB, 300 us, 5.4 TB/s; 64 requests
+// of 16 behind up to 4096, 0.82 GB, 162 us), and where it has many the order of a
+// step within a wave, products with K, then the weights, then products with V, each
+// waiting for the one before, with two waves a SIMD (8 causal chunks of 512 tokens
+// behind 1536, 81 GFLOP, 123 to 133 us: a step of 32 rows by 32 keys takes a wave 34
+// matrix and about 150 vector instructions; the matrix unit is busy a third of the
+// time, the vector unit half of it).
 #pragma once
 
 #include "sgg_device.h"
