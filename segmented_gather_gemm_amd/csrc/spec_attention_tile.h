@@ -24,7 +24,7 @@
 // of 16 behind up to 4096, 0.82 GB, 162 us), and where it has many the order of a
 // step within a wave, products with K, then the weights, then products with V, each
 // waiting for the one before, with two waves a SIMD (8 causal chunks of 512 tokens
-// behind 1536, 81 GFLOP, 123 to 133 us: a step of 32 rows by 32 keys takes a wave 34
+// behind 1536, 81 GFLOP, 122 to 133 us: a step of 32 rows by 32 keys takes a wave 34
 // matrix and about 150 vector instructions; the matrix unit is busy a third of the
 // time, the vector unit half of it).
 #pragma once
