@@ -232,6 +232,173 @@ int spec_verify(const int32_t* tokens, const int32_t* parents, const int32_t* q_
                 int64_t workspace_bytes, void* stream);
 
 /*
+ * spec_rope_write -- spec_kv_write_held (page_counts NULL: spec_kv_write) with the
+ * rotation of queries and keys on the way.  q, q_out (num_tokens, num_q_heads,
+ * head_dim) and k, v (num_tokens, num_kv_heads, head_dim) of dtype SPEC_BF16 /
+ * SPEC_FP16, strides in elements, multiples of 8; q_out may be q itself, else it
+ * overlaps nothing.  num_q_heads 0: no queries.
+ *   Columns rope_start .. rope_start + rotary_dim of every head of q and k (even,
+ *   up to 256) are rotary_dim / 2 pairs (a, b): columns 2i, 2i + 1 from
+ *   rope_start on (interleaved != 0) or i, i + rotary_dim / 2.  With the angle
+ *   t = position * inv_freq[i] (float32 [rotary_dim / 2]),
+ *     a' = factor * (a cos t - b sin t),  b' = factor * (b cos t + a sin t).
+ *   The angle and its fraction of a turn are in 64 bits, all else in 32; a' and b'
+ *   are rounded once, to q's type or the cache's.  Other columns are copied.
+ *   positions: int32 [num_tokens], as spec_tree_mask gives them; NULL: the
+ *   token's place in the cache, kv_lens[row] + i.  The token is written at that
+ *   place in either case.
+ *   Tokens of no request, and of one whose row is out of range, are left alone in
+ *   q_out too; a token without a page has its queries rotated.
+ */
+int spec_rope_write(const void* q, int64_t q_token, int64_t q_head, void* q_out,
+                    int64_t out_token, int64_t out_head, int32_t num_q_heads, const void* k,
+                    int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                    int64_t v_head, int32_t dtype, const float* inv_freq, int32_t rotary_dim,
+                    int32_t rope_start, int32_t interleaved, float factor,
+                    const int32_t* positions, const SpecKvCache* cache, const int32_t* page_table,
+                    int64_t ld_table, int32_t max_pages, int32_t num_rows,
+                    const int32_t* page_counts, const int32_t* kv_lens, const int32_t* rows,
+                    const int32_t* q_indptr, int32_t bs, int64_t num_tokens, const float* k_scale,
+                    const float* v_scale, void* stream);
+
+/* One layer of latent vectors in pages: a token's row is latent_dim values and the
+ * rope_dim values of the rotated key part behind them.  Strides in elements, from
+ * page to page and token to token.  data and both strides in bytes are multiples of
+ * 16, and so are latent_dim and rope_dim in bytes; latent_dim up to 512, rope_dim up
+ * to 64; page_size is a power of two. */
+typedef struct {
+  void* data;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t dtype;  /* SPEC_BF16, SPEC_FP16 or SPEC_E4M3 */
+} SpecLatentCache;
+
+/*
+ * spec_latent_write -- new rows of a cache of latents, with the rotation on the
+ * way: latent (num_tokens, latent_dim) as it is, k_pe (num_tokens, rope_dim) and
+ * the queries' parts q_pe (num_tokens, num_q_heads, rope_dim), into q_out, rotated
+ * over their whole width.  An SPEC_E4M3 cache takes x / cache_scale[0].  All else
+ * as in spec_rope_write.
+ */
+int spec_latent_write(const void* q_pe, int64_t q_token, int64_t q_head, void* q_out,
+                      int64_t out_token, int64_t out_head, int32_t num_q_heads,
+                      const void* latent, int64_t latent_token, const void* k_pe,
+                      int64_t k_pe_token, int32_t dtype, const float* inv_freq,
+                      int32_t interleaved, float factor, const int32_t* positions,
+                      const SpecLatentCache* cache, const int32_t* page_table, int64_t ld_table,
+                      int32_t max_pages, int32_t num_rows, const int32_t* page_counts,
+                      const int32_t* kv_lens, const int32_t* rows, const int32_t* q_indptr,
+                      int32_t bs, int64_t num_tokens, const float* cache_scale, void* stream);
+
+/*
+ * spec_latent_gather -- rows of a cache of latents next to each other: row
+ * kv_indptr[r] + j of out (num_tokens, latent_dim + rope_dim) becomes position j of
+ * request r, for j < kv_indptr[r + 1] - kv_indptr[r].  out has the cache's dtype, or
+ * SPEC_BF16 / SPEC_FP16 where the cache is SPEC_E4M3: then times cache_scale[0]
+ * (NULL: 1).  Positions without a page (past max_pages, past the page_counts[row]
+ * pages of the row where that is given, page id out of range) become zeros; rows of
+ * no request, and of one whose row is out of range, are left as they were.
+ */
+int spec_latent_gather(const SpecLatentCache* cache, const int32_t* page_table, int64_t ld_table,
+                       int32_t max_pages, int32_t num_rows, const int32_t* page_counts,
+                       const int32_t* rows, const int32_t* kv_indptr, int32_t bs,
+                       int64_t num_tokens, void* out, int64_t out_token, int32_t dtype,
+                       const float* cache_scale, void* stream);
+
+/*
+ * spec_latent_attention -- attention over a cache of latents (the absorbed form):
+ * of every token the row [c, kr] is the key of all heads and c their value.
+ *   q (num_tokens, num_heads, latent_dim + rope_dim), out (num_tokens, num_heads,
+ *   latent_dim) of q_dtype (SPEC_BF16 or SPEC_FP16), strides in elements, multiples
+ *   of 8.  out = sum_j softmax_j(scale * q.[c_j, kr_j]) c_j over the keys that the
+ *   token sees, which are those of spec_attention, as are page ids, max_q_len,
+ *   max_kv_len and the roundings; an SPEC_E4M3 cache holds values / cache_scale[0]
+ *   (NULL: 1).  Rows that a token does not see have no part in its result; one that
+ *   sees a row with an infinity or NaN has no particular result.
+ *   workspace: spec_latent_attention_workspace_bytes(), 16-byte aligned, not shared
+ *   by overlapping calls; it may be the one of spec_attention() and spec_verify().
+ *   The same inputs give the same bits on every run.
+ */
+int64_t spec_latent_attention_workspace_bytes(int32_t bs, int32_t num_heads, int32_t latent_dim,
+                                              int32_t cache_dtype, int32_t max_q_len,
+                                              int64_t max_kv_len);
+int spec_latent_attention(const void* q, int64_t q_token, int64_t q_head, void* out,
+                          int64_t out_token, int64_t out_head, int32_t q_dtype,
+                          int32_t num_heads, const SpecLatentCache* cache,
+                          const int32_t* page_table, int64_t ld_table, int32_t max_pages,
+                          int32_t num_rows, const int32_t* kv_lens, const int32_t* rows,
+                          const int32_t* q_indptr, int32_t bs, int64_t num_tokens,
+                          const int64_t* tree_mask, int32_t mask_words, float scale,
+                          const float* cache_scale, int32_t max_q_len, int64_t max_kv_len,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * spec_latent_prefill -- causal attention over expanded latents: request r has the
+ * T_r queries q_indptr[r] .. and the K_r keys kv_indptr[r] ..; its queries are the
+ * last T_r of its K_r tokens, and query i sees keys j <= K_r - T_r + i.
+ *   q (num_tokens, num_heads, nope_dim + rope_dim), k (num_keys, num_heads,
+ *   nope_dim), v, out (.., num_heads, v_dim), k_pe (num_keys, rope_dim), the rotated
+ *   key part of all heads; all of dtype SPEC_BF16 or SPEC_FP16, strides in elements,
+ *   multiples of 8.  nope_dim and v_dim: multiples of 8 up to 128, rope_dim: up to
+ *   64.  out = sum_j softmax_j(scale * (q_n.k_j + q_r.k_pe_j)) v_j; a query that sees
+ *   no key gets 0.  Roundings as in spec_attention.  Keys that a query does not see
+ *   have no part in its result.
+ *   max_q_len: a bound of T_r that shapes the launch, not the result.
+ */
+int spec_latent_prefill(const void* q, int64_t q_token, int64_t q_head, const void* k,
+                        int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                        int64_t v_head, const void* k_pe, int64_t k_pe_token, void* out,
+                        int64_t out_token, int64_t out_head, int32_t dtype, int32_t num_heads,
+                        int32_t nope_dim, int32_t rope_dim, int32_t v_dim,
+                        const int32_t* q_indptr, const int32_t* kv_indptr, int32_t bs,
+                        int64_t num_tokens, int64_t num_keys, float scale, int32_t max_q_len,
+                        void* stream);
+
+/*
+ * spec_target_probs -- the rows of target_probs that spec_verify takes, from logits
+ * (num_tokens, vocab) of dtype SPEC_BF16, SPEC_FP16 or SPEC_FP32 with rows ld_logits
+ * apart (any alignment that the type has).  For the row of node i of request r, in
+ * 32 bits and in this order, of every value v with logit x:
+ *   c = how often v stands in the request's text since its prompt and among the
+ *   node and its ancestors; met = c > 0 or v stands in the prompt.
+ *   met: x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *   x -= c * frequency[r];  x -= presence[r] if c > 0
+ *   x += bias_values[b] for b = bias_indptr[r] .. bias_indptr[r + 1] with
+ *   bias_ids[b] = v, added up in their order
+ *   x = -inf if x is NaN or bit v % 32 of allowed[row][v / 32] is not set
+ *   out = softmax(x / temperature[r]); a temperature that is not above 0: 1 at the
+ *   first of the largest, 0 elsewhere.  Where the largest is +inf, its places share
+ *   1 equally; a row that holds nothing but -inf becomes 0.
+ *   The text of request r is history[rows[r]] (rows NULL: r; [num_rows], ld_history
+ *   apart, history_width entries) up to history_lens[row], its prompt up to
+ *   prompt_lens[row] (NULL: none).  tokens, parents: the nodes as in spec_verify
+ *   (tokens NULL: nodes do not count; parents NULL: each follows the one before).
+ *   Tokens outside [0, vocab) count nowhere.  Each of temperature (1), repetition
+ *   (1), presence (0), frequency (0), the biases (num_bias entries; none), history
+ *   (none) and allowed (all) may be NULL.
+ *   Rows of no request are left as they were.  max_q_len: a bound of the requests'
+ *   nodes that shapes the launch, not the result.
+ *   workspace: spec_target_probs_workspace_bytes(), 16-byte aligned, not shared by
+ *   overlapping calls; it may be the one of spec_attention() and spec_verify().
+ */
+#define SPEC_FP32 3
+int64_t spec_target_probs_workspace_bytes(int64_t num_tokens, int64_t vocab);
+int spec_target_probs(const void* logits, int64_t ld_logits, int32_t dtype, int64_t vocab,
+                      const int32_t* q_indptr, int32_t bs, int64_t num_tokens,
+                      int32_t max_q_len, const int32_t* tokens, const int32_t* parents,
+                      const int32_t* history, int64_t ld_history, int32_t history_width,
+                      int32_t num_rows, const int32_t* history_lens, const int32_t* prompt_lens,
+                      const int32_t* rows, const float* temperature, const float* repetition,
+                      const float* presence, const float* frequency, const int32_t* bias_indptr,
+                      const int32_t* bias_ids, const float* bias_values, int64_t num_bias,
+                      const int32_t* allowed, int64_t ld_allowed, float* out, int64_t ld_out,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * spec_set_option -- process-wide settings; returns the previous value, -1 for
  * an unknown name or a negative value.
  *   "verify_spin_limit"  polls after which a workgroup of spec_verify that waits

@@ -29,12 +29,12 @@ def mask_words(seen, words):
 
 
 def attention(q, k, v, seen, scale):
-    """q (T, Hq, D), k and v (S, Hkv, D), seen (T, S): the result (T, Hq, D), the sums of
+    """q (T, Hq, D), k (S, Hkv, D), v (S, Hkv, Dv), seen (T, S): the result (T, Hq, Dv), the sums of
     weight times |v|, and per (token, head) the largest sum of |q k| and |score| of a key in
     sight.  Keys out of sight are left out before anything is computed with them."""
     T, hq, D = q.shape
     g = hq // k.shape[1]
-    o, mag = np.zeros((T, hq, D)), np.zeros((T, hq, D))
+    o, mag = np.zeros((T, hq, v.shape[2])), np.zeros((T, hq, v.shape[2]))
     prod, top = np.zeros((T, hq)), np.zeros((T, hq))
     for t in range(T):
         at = np.nonzero(seen[t])[0]

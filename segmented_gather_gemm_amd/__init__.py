@@ -26,6 +26,13 @@ from .binding import (
     lora_set_option,
     lora_shrink,
 )
+from .latent import (
+    PagedLatentCache,
+    spec_latent_attention,
+    spec_latent_gather,
+    spec_latent_prefill,
+    spec_latent_write,
+)
 from .speculative import (
     PagedKVCache,
     spec_attention,
@@ -34,7 +41,9 @@ from .speculative import (
     spec_kv_fork,
     spec_kv_resize,
     spec_kv_write,
+    spec_rope_write,
     spec_set_option,
+    spec_target_probs,
     spec_tree_mask,
     spec_verify,
 )
@@ -49,5 +58,7 @@ __all__ = [
     "lora_plan_max_segments", "lora_plan_segments", "lora_qkv", "lora_qkv_noalloc",
     "lora_set_option", "lora_shrink", "PagedKVCache", "spec_attention", "spec_kv_compact",
     "spec_kv_copy_pages", "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_set_option",
-    "spec_tree_mask", "spec_verify",
+    "spec_tree_mask", "spec_verify", "PagedLatentCache", "spec_latent_attention",
+    "spec_latent_gather", "spec_latent_prefill", "spec_latent_write", "spec_rope_write",
+    "spec_target_probs",
 ]

@@ -31,11 +31,10 @@
 
 #include "sgg_device.h"
 #include "spec_attention.h"
+#include "spec_pages.h"
 
 namespace sgg {
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
@@ -238,30 +237,6 @@ __device__ __forceinline__ f32x4 attn_mfma(u32x4_t a, u32x4_t b, f32x4 c) {
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
-// Two floats to the 16-bit type, rounded to nearest even.
-template <bool kFp16>
-__device__ __forceinline__ uint32_t pack16(float x, float y) {
-  if constexpr (kFp16) {
-    f16x2_t v = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
-    return __builtin_bit_cast(uint32_t, v);
-  } else {
-    bf16x2_t v = {static_cast<__bf16>(x), static_cast<__bf16>(y)};
-    return __builtin_bit_cast(uint32_t, v);
-  }
-}
-
-// Four 8-bit values to the 16-bit type (exact).
-template <bool kFp16>
-__device__ __forceinline__ void widen4(int x, uint32_t* lo, uint32_t* hi) {
-  if constexpr (kFp16) {
-    *lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, false));
-    *hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, 1.0f, true));
-  } else {
-    *lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
-    *hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true));
-  }
 }
 
 // Maximum over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48).

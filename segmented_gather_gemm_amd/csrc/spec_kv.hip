@@ -9,6 +9,7 @@
 // any order.  The result is the same on every run.
 #include "sgg_device.h"
 #include "spec_kernels.h"
+#include "spec_pages.h"
 
 namespace sgg {
 namespace {
@@ -30,28 +31,6 @@ __device__ __forceinline__ int load_agent(const int32_t* p) {
 __device__ __forceinline__ void store_past(char* p, const uint4& v) {
   typedef uint32_t Words __attribute__((ext_vector_type(4)));
   __builtin_nontemporal_store(__builtin_bit_cast(Words, v), reinterpret_cast<Words*>(p));
-}
-
-// Cache row of request i, or -1.
-__device__ __forceinline__ int row_of(const KvRows& t, int i) {
-  const int r = t.rows ? t.rows[i] : i;
-  return r >= 0 && r < t.num_rows ? r : -1;
-}
-
-// Pages of cache row `row` that may be written: entries past those that a row
-// holds may name pages of other rows.
-__device__ __forceinline__ int slots_of(const KvRows& t, int row) {
-  return t.held ? min(t.held[row], t.max_pages) : t.max_pages;
-}
-
-// Page of position `pos` in cache row `row` of `slots` pages, or -1 where there is none.
-__device__ __forceinline__ int64_t page_at(const KvRows& t, int row, int slots, int64_t pos,
-                                           int shift, int64_t num_pages) {
-  if (pos < 0) return -1;
-  const int64_t slot = pos >> shift;
-  if (slot >= slots) return -1;
-  const int64_t page = t.table[row * t.ld + slot];
-  return page >= 0 && page < num_pages ? page : -1;
 }
 
 // The value that a lane below holds, by register moves (0 where there is none).
@@ -378,17 +357,6 @@ __global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(KvView c, const i
         if (e0 + k * kCopyThreads < total) store_past(d + off[k], v[k]);
     }
   }
-}
-
-__device__ __forceinline__ float to_f32(uint32_t bits, bool fp16) {
-  if (!fp16) return bf16_to_f32(bits);
-  return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
-}
-
-// x / scale clamped to the 8-bit type's range; NaN passes.
-__device__ __forceinline__ float scaled_e4m3(float x, float scale) {
-  const float y = x / scale;
-  return y != y ? y : fminf(fmaxf(y, -448.0f), 448.0f);
 }
 
 // One workgroup per (request, token slab); 8 values of a key or value row a

@@ -20,6 +20,14 @@
 #define SIG_spec_attention_workspace_bytes "iiiiiil"
 #define SIG_spec_attention "pllplliippliipppilpifppilplp"
 #define SIG_spec_verify_workspace_bytes "il"
+#define SIG_spec_rope_write "pllpllipllpllipiiifpppliippppilppp"
+#define SIG_spec_latent_write "pllplliplplipifpppliippppilpp"
+#define SIG_spec_latent_gather "ppliipppilplipp"
+#define SIG_spec_latent_attention_workspace_bytes "iiiiil"
+#define SIG_spec_latent_attention "pllplliippliipppilpifpilplp"
+#define SIG_spec_latent_prefill "pllpllpllplplliiiiippillfip"
+#define SIG_spec_target_probs_workspace_bytes "ll"
+#define SIG_spec_target_probs "plilpilipppliipppppppppplplplplp"
 #define SIG_spec_set_option "pl"
 #define SIG_spec_verify "pppilplpllppplippplp"
 
@@ -115,6 +123,73 @@ static PyObject* py_spec_verify(PyObject* self, PyObject* const* args, Py_ssize_
       L(18), P(19)));
 }
 
+static PyObject* py_spec_rope_write(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_rope_write);
+  RETURN_INT(spec_rope_write(
+      P(0), L(1), L(2), P(3), L(4), L(5), I(6), P(7), L(8), L(9), P(10), L(11), L(12), I(13),
+      (const float*)P(14), I(15), I(16), I(17), F(18), (const int32_t*)P(19), (const
+      SpecKvCache*)P(20), (const int32_t*)P(21), L(22), I(23), I(24), (const int32_t*)P(25),
+      (const int32_t*)P(26), (const int32_t*)P(27), (const int32_t*)P(28), I(29), L(30), (const
+      float*)P(31), (const float*)P(32), P(33)));
+}
+
+static PyObject* py_spec_latent_write(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_latent_write);
+  RETURN_INT(spec_latent_write(
+      P(0), L(1), L(2), P(3), L(4), L(5), I(6), P(7), L(8), P(9), L(10), I(11), (const
+      float*)P(12), I(13), F(14), (const int32_t*)P(15), (const SpecLatentCache*)P(16), (const
+      int32_t*)P(17), L(18), I(19), I(20), (const int32_t*)P(21), (const int32_t*)P(22), (const
+      int32_t*)P(23), (const int32_t*)P(24), I(25), L(26), (const float*)P(27), P(28)));
+}
+
+static PyObject* py_spec_latent_gather(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_latent_gather);
+  RETURN_INT(spec_latent_gather(
+      (const SpecLatentCache*)P(0), (const int32_t*)P(1), L(2), I(3), I(4), (const
+      int32_t*)P(5), (const int32_t*)P(6), (const int32_t*)P(7), I(8), L(9), P(10), L(11),
+      I(12), (const float*)P(13), P(14)));
+}
+
+static PyObject* py_spec_latent_attention_workspace_bytes(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_latent_attention_workspace_bytes);
+  RETURN_INT(spec_latent_attention_workspace_bytes(
+      I(0), I(1), I(2), I(3), I(4), L(5)));
+}
+
+static PyObject* py_spec_latent_attention(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_latent_attention);
+  RETURN_INT(spec_latent_attention(
+      P(0), L(1), L(2), P(3), L(4), L(5), I(6), I(7), (const SpecLatentCache*)P(8), (const
+      int32_t*)P(9), L(10), I(11), I(12), (const int32_t*)P(13), (const int32_t*)P(14), (const
+      int32_t*)P(15), I(16), L(17), (const int64_t*)P(18), I(19), F(20), (const float*)P(21),
+      I(22), L(23), P(24), L(25), P(26)));
+}
+
+static PyObject* py_spec_latent_prefill(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_latent_prefill);
+  RETURN_INT(spec_latent_prefill(
+      P(0), L(1), L(2), P(3), L(4), L(5), P(6), L(7), L(8), P(9), L(10), P(11), L(12), L(13),
+      I(14), I(15), I(16), I(17), I(18), (const int32_t*)P(19), (const int32_t*)P(20), I(21),
+      L(22), L(23), F(24), I(25), P(26)));
+}
+
+static PyObject* py_spec_target_probs_workspace_bytes(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_target_probs_workspace_bytes);
+  RETURN_INT(spec_target_probs_workspace_bytes(
+      L(0), L(1)));
+}
+
+static PyObject* py_spec_target_probs(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+  CONVERT(spec_target_probs);
+  RETURN_INT(spec_target_probs(
+      P(0), L(1), I(2), L(3), (const int32_t*)P(4), I(5), L(6), I(7), (const int32_t*)P(8),
+      (const int32_t*)P(9), (const int32_t*)P(10), L(11), I(12), I(13), (const int32_t*)P(14),
+      (const int32_t*)P(15), (const int32_t*)P(16), (const float*)P(17), (const float*)P(18),
+      (const float*)P(19), (const float*)P(20), (const int32_t*)P(21), (const int32_t*)P(22),
+      (const float*)P(23), L(24), (const int32_t*)P(25), L(26), (float*)P(27), L(28), P(29),
+      L(30), P(31)));
+}
+
 static PyObject* py_spec_set_option(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   CONVERT(spec_set_option);
   RETURN_INT(spec_set_option(
@@ -134,6 +209,14 @@ static PyMethodDef methods[] = {
     ENTRY(spec_attention),
     ENTRY(spec_verify_workspace_bytes),
     ENTRY(spec_verify),
+    ENTRY(spec_rope_write),
+    ENTRY(spec_latent_write),
+    ENTRY(spec_latent_gather),
+    ENTRY(spec_latent_attention_workspace_bytes),
+    ENTRY(spec_latent_attention),
+    ENTRY(spec_latent_prefill),
+    ENTRY(spec_target_probs_workspace_bytes),
+    ENTRY(spec_target_probs),
     ENTRY(spec_set_option),
     {NULL, NULL, 0, NULL},
 };
@@ -161,6 +244,14 @@ PyMODINIT_FUNC PyInit__sggspec(void) {
       {"spec_attention", SIG_spec_attention},
       {"spec_verify_workspace_bytes", SIG_spec_verify_workspace_bytes},
       {"spec_verify", SIG_spec_verify},
+      {"spec_rope_write", SIG_spec_rope_write},
+      {"spec_latent_write", SIG_spec_latent_write},
+      {"spec_latent_gather", SIG_spec_latent_gather},
+      {"spec_latent_attention_workspace_bytes", SIG_spec_latent_attention_workspace_bytes},
+      {"spec_latent_attention", SIG_spec_latent_attention},
+      {"spec_latent_prefill", SIG_spec_latent_prefill},
+      {"spec_target_probs_workspace_bytes", SIG_spec_target_probs_workspace_bytes},
+      {"spec_target_probs", SIG_spec_target_probs},
       {"spec_set_option", SIG_spec_set_option},
   };
   int bad = sigs == NULL;

@@ -202,6 +202,68 @@ PyObject* heads(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// latents(tensor, rope_dim): the SpecLatentCache of (pages, page_size, columns) as bytes,
+// the last rope_dim columns for the key part, and all columns.
+PyObject* latents(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Arg a;
+  if (n != 2) return PyErr_Format(PyExc_TypeError, "latents takes a tensor and rope_dim");
+  if (!tensor_of("cache", args[0], &a)) return nullptr;
+  const long long rope = PyLong_AsLongLong(args[1]);
+  if (rope == -1 && PyErr_Occurred()) return nullptr;
+  const at::Tensor& t = *a.t;
+  SpecLatentCache c{};
+  switch (t.scalar_type()) {
+    case at::kBFloat16: c.dtype = SPEC_BF16; break;
+    case at::kHalf: c.dtype = SPEC_FP16; break;
+    case at::kFloat8_e4m3fn: c.dtype = SPEC_E4M3; break;
+    default:
+      return complain(PyExc_TypeError, "the cache",
+                      "must be bfloat16, float16 or float8_e4m3fn, got ", a, "dtype");
+  }
+  if (index_of(t) < 0) return PyErr_Format(PyExc_ValueError, "the cache must be on a ROCm device");
+  if (t.dim() != 3)
+    return complain(PyExc_ValueError, "the cache", "must be (pages, page_size, columns), got ", a,
+                    "shape");
+  int64_t st[3];
+  if (!strides_of("cache", t, st)) return nullptr;
+  const long long wide = t.size(2);
+  if (t.size(1) > INT32_MAX || wide > INT32_MAX)
+    return complain(PyExc_OverflowError, "the cache", "is too large: ", a, "shape");
+  if (rope <= 0 || rope >= wide)
+    return PyErr_Format(PyExc_ValueError, "a cache of %lld columns does not hold %lld of the key part",
+                        wide, rope);
+  c.data = t.data_ptr();
+  c.page_stride = st[0];
+  c.token_stride = st[1];
+  c.num_pages = t.size(0);
+  c.page_size = static_cast<int32_t>(t.size(1));
+  c.latent_dim = static_cast<int32_t>(wide - rope);
+  c.rope_dim = static_cast<int32_t>(rope);
+  return Py_BuildValue("(y#L)", reinterpret_cast<const char*>(&c),
+                       static_cast<Py_ssize_t>(sizeof(c)), wide);
+  END_HANDLE_TH_ERRORS
+}
+
+// rows(name, tensor): address and row stride of (tokens, columns) of a 16-bit type.
+PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 2) return PyErr_Format(PyExc_TypeError, "rows takes a name and a tensor");
+  const char* name = PyUnicode_AsUTF8(args[0]);
+  Arg a;
+  if (name == nullptr || !tensor_of(name, args[1], &a)) return nullptr;
+  const at::Tensor& t = *a.t;
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kHalf)
+    return complain(PyExc_TypeError, name, "must be bfloat16 or float16, got ", a, "dtype");
+  if (t.dim() != 2)
+    return complain(PyExc_ValueError, name, "must be (tokens, columns), got ", a, "shape");
+  int64_t st[2];
+  if (!strides_of(name, t, st)) return nullptr;
+  return Py_BuildValue("(KL)", reinterpret_cast<unsigned long long>(t.data_ptr()),
+                       static_cast<long long>(st[0]));
+  END_HANDLE_TH_ERRORS
+}
+
 // new_i32(like, size...): an uninitialised int32 tensor on the device of `like`.
 PyObject* new_i32(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -220,7 +282,8 @@ PyObject* new_i32(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define ENTRY(fn) {#fn, reinterpret_cast<PyCFunction>(fn), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(i32),   ENTRY(f32),     ENTRY(table), ENTRY(cache),
-                         ENTRY(heads), ENTRY(new_i32), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(heads), ENTRY(latents), ENTRY(rows),  ENTRY(new_i32),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sggtensor",
                       "Checks of the tensor arguments of the spec_* calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -17,6 +17,7 @@ from ._lib import check, spec_calls, tensor_args
 from .binding import _stream
 
 _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 3}
 
 # the checks of one tensor argument each (csrc/tensorargs.cpp)
 _args = tensor_args()
@@ -28,19 +29,20 @@ _workspaces = {}
 _outgrown = []
 
 
-def _workspace(t, nbytes):
+def _workspace(t, nbytes, zero=True):
     """Scratch of ``nbytes`` for a call on tensor ``t``'s current stream: (address, bytes).
 
     Zero when it is made; every call leaves its counters at zero.  One grow-only buffer per
     stream, so calls on different streams never share one; an outgrown buffer is kept, for a
     kernel under way may still use it.  While a graph is captured the call gets a buffer of its
-    own, cleared in the graph: the graph's memory is not the streams'.
+    own, cleared in the graph (``zero``: the call counts on it): the graph's memory is not the
+    streams'.
     """
     if nbytes <= 0:
         return 0, 0, None
     stream = _stream(t)
     if torch._C._cuda_isCurrentStreamCapturing():
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
+        ws = (torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=t.device)
         return ws.data_ptr(), nbytes, ws
     key = (t.get_device(), stream)
     ws = _workspaces.get(key)
@@ -156,6 +158,67 @@ def spec_kv_write(k, v, k_cache, v_cache, page_table, kv_lens, q_indptr, rows=No
     else:
         check(spec_calls().spec_kv_write_held(
             *new, _i32("page_counts", page_counts, dev, num_rows), *batch))
+
+
+def _positions(positions, dev, n):
+    return 0 if positions is None else _i32("positions", positions, dev, n)
+
+
+def spec_rope_write(q, k, v, inv_freq, k_cache, v_cache, page_table, kv_lens, q_indptr, rows=None,
+                    positions=None, rope_start=0, interleaved=False, factor=1.0, k_scale=None,
+                    v_scale=None, page_counts=None, q_out=None):
+    """Queries and keys rotated by their positions, the keys and values written into one layer's
+    cache on the way: spec_kv_write of the rotated ``k``.  Columns ``rope_start`` to ``rope_start``
+    + 2 len(inv_freq) of every head are rotated by position * ``inv_freq`` (float32), as pairs of
+    neighbours (``interleaved``) or half of the columns apart, times ``factor``.  ``positions``
+    (tokens), as from spec_tree_mask; None: the tokens' places in the cache.  Returns ``q_out``
+    (like q; it may be q itself); ``q`` None: only keys and values, nothing is returned."""
+    dev = k_cache.get_device()
+    c, (L, _, _, H, D) = _cache(k_cache, v_cache)
+    if L != 1:
+        raise ValueError(f"k and v belong to one layer, the cache has {L}: "
+                         f"{tuple(k_cache.shape)}")
+    kp, kt, kh = _heads("k", k)
+    vp, vt, vh = _heads("v", v)
+    n = k.shape[0]
+    if k.shape != (n, H, D) or v.shape != (n, H, D) or v.dtype is not k.dtype:
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} must be "
+                         f"(tokens, {H}, {D}) of one type")
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("k and v must be on the cache's device")
+    queries, q_out = _queries(q, q_out, k, D, "q")
+    t, ld, width, num_rows = _table(page_table, dev)
+    bs, ind, rp = _batch(q_indptr, rows, dev)
+    check(spec_calls().spec_rope_write(
+        *queries, kp, kt, kh, vp, vt, vh, _CODES[k.dtype], _f32("inv_freq", inv_freq, dev),
+        2 * inv_freq.numel(), rope_start, bool(interleaved), factor,
+        _positions(positions, dev, n), c, t, ld, width, num_rows,
+        0 if page_counts is None else _i32("page_counts", page_counts, dev, num_rows),
+        _i32("kv_lens", kv_lens, dev, num_rows), rp, ind, bs, n,
+        0 if k_scale is None else _f32("k_scale", k_scale, dev, H),
+        0 if v_scale is None else _f32("v_scale", v_scale, dev, H), _stream(k_cache)))
+    return q_out
+
+
+def _queries(q, q_out, like, dim, name):
+    """Addresses, strides and heads of queries (tokens, heads, dim) beside the tokens of ``like``
+    and of where they go, and that tensor."""
+    if q is None:
+        if q_out is not None:
+            raise ValueError(f"q_out without {name}")
+        return (0, 0, 0, 0, 0, 0, 0), None
+    qp, qt, qh = _heads(name, q)
+    if q.shape[0] != like.shape[0] or q.shape[2] != dim or q.dtype is not like.dtype \
+            or q.get_device() != like.get_device():
+        raise ValueError(f"{name} {tuple(q.shape)} {q.dtype} must be ({like.shape[0]}, heads, {dim}) "
+                         f"of the new rows' type, on their device")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape or q_out.dtype is not q.dtype \
+            or q_out.get_device() != q.get_device():
+        raise ValueError(f"q_out {tuple(q_out.shape)} {q_out.dtype} does not match {name}")
+    op, ot, oh = _heads("q_out", q_out)
+    return (qp, qt, qh, op, ot, oh, q.shape[1]), q_out
 
 
 def spec_kv_compact(k_cache, v_cache, page_table, kv_lens, path, accept_lens, rows=None,
@@ -285,6 +348,85 @@ def spec_verify(tokens, parents, q_indptr, target_probs, uniforms, final_uniform
     return path, accept, nxt
 
 
+def spec_target_probs(logits, q_indptr, max_q_len, temperature=None, tokens=None, parents=None,
+                      history=None, history_lens=None, prompt_lens=None, rows=None,
+                      repetition=None, presence=None, frequency=None, bias_indptr=None,
+                      bias_ids=None, bias_values=None, allowed=None, out=None, workspace=None):
+    """The target's probabilities (tokens, vocab) float32, as spec_verify takes them, from its
+    ``logits`` (tokens, vocab) in bfloat16, float16 or float32.
+
+    Per request (bs), float32: ``temperature`` (not above 0: all on the largest), ``repetition``,
+    ``presence`` and ``frequency`` penalties for values that the request's text holds or the node's
+    path: ``history`` (cache rows, width) int32 up to ``history_lens`` (cache rows), of which
+    ``prompt_lens`` (cache rows) are its prompt and count for ``repetition`` alone; ``tokens`` and
+    ``parents`` (tokens) are the nodes' (no parents: a chain).  Request r adds ``bias_values`` to
+    the logits of ``bias_ids`` in its range of ``bias_indptr`` (bs + 1).  ``allowed`` (tokens, words)
+    int32: a node's row has a bit for every value that may follow it.  include/sgg_spec.h has the
+    order.  ``max_q_len`` shapes the launch, not the result; ``workspace`` as in
+    spec_latent_attention."""
+    dev = logits.get_device()
+    bs, ind, rp = _batch(q_indptr, rows, dev)
+    if logits.dtype not in _LOGITS or logits.dim() != 2 or dev < 0 \
+            or (logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError(f"logits must be (tokens, vocab) rows of bfloat16, float16 or float32 on a "
+                         f"ROCm device, got {tuple(logits.shape)} {logits.dtype}")
+    n, V = logits.shape
+    if out is None:
+        out = torch.empty((n, V), dtype=torch.float32, device=logits.device)
+    elif out.shape != logits.shape or out.dtype is not torch.float32 \
+            or out.get_device() != dev or (out.stride(1) != 1 and V != 1):
+        raise ValueError(f"out must be float32 {(n, V)} rows, got {tuple(out.shape)} {out.dtype}")
+    hp = ld = width = num_rows = 0
+    if history is not None:
+        if history.dtype is not torch.int32 or history.dim() != 2 \
+                or history.get_device() != dev \
+                or (history.stride(1) != 1 and history.shape[1] != 1):
+            raise ValueError(f"history must be int32 (cache rows, width) rows, got "
+                             f"{tuple(history.shape)} {history.dtype}")
+        num_rows, width = history.shape
+        hp, ld = history.data_ptr(), history.stride(0) if num_rows > 1 else width
+        if history_lens is None:
+            raise ValueError("history needs history_lens")
+    num_bias = 0
+    if bias_indptr is not None:
+        if bias_ids is None or bias_values is None:
+            raise ValueError("bias_indptr needs bias_ids and bias_values")
+        num_bias = bias_ids.numel()
+    ap = words = 0
+    if allowed is not None:
+        if allowed.dtype is not torch.int32 or allowed.dim() != 2 or allowed.shape[0] != n \
+                or allowed.get_device() != dev \
+                or (allowed.stride(1) != 1 and allowed.shape[1] != 1) \
+                or allowed.shape[1] < (V + 31) // 32:
+            raise ValueError(f"allowed must be int32 ({n}, {(V + 31) // 32}) rows, got "
+                             f"{tuple(allowed.shape)} {allowed.dtype}")
+        ap, words = allowed.data_ptr(), allowed.stride(0) if n > 1 else allowed.shape[1]
+
+    def each(name, x):
+        return 0 if x is None else _f32(name, x, dev, bs)
+
+    def lens(name, x):
+        return 0 if x is None or history is None else _i32(name, x, dev, num_rows)
+
+    calls = spec_calls()
+    if workspace is None:
+        wp, wn, _held = _workspace(logits, calls.spec_target_probs_workspace_bytes(n, V), False)
+    else:
+        wp, wn = _given_workspace(workspace, dev)
+    check(calls.spec_target_probs(
+        logits.data_ptr(), logits.stride(0) if n > 1 else V, _LOGITS[logits.dtype], V, ind, bs, n,
+        max_q_len, 0 if tokens is None else _i32("tokens", tokens, dev, n),
+        0 if parents is None else _i32("parents", parents, dev, n), hp, ld, width, num_rows,
+        lens("history_lens", history_lens), lens("prompt_lens", prompt_lens), rp,
+        each("temperature", temperature), each("repetition", repetition),
+        each("presence", presence), each("frequency", frequency),
+        0 if bias_indptr is None else _i32("bias_indptr", bias_indptr, dev, bs + 1),
+        0 if bias_indptr is None else _i32("bias_ids", bias_ids, dev, num_bias),
+        0 if bias_indptr is None else _f32("bias_values", bias_values, dev, num_bias), num_bias,
+        ap, words, out.data_ptr(), out.stride(0) if n > 1 else V, wp, wn, _stream(logits)))
+    return out
+
+
 def spec_set_option(name, value):
     """Process-wide setting ("verify_spin_limit": polls); returns the previous value."""
     old = spec_calls().spec_set_option(name.encode() + b"\0", int(value))
@@ -353,6 +495,14 @@ class PagedKVCache:
         spec_kv_write(k, v, self.k[layer], self.v[layer], self.page_table, self.kv_lens,
                       q_indptr, rows, page_counts=self.page_counts, **self._scales(layer))
 
+    def rope_write(self, layer, q, k, v, inv_freq, q_indptr, rows=None, positions=None,
+                   rope_start=0, interleaved=False, factor=1.0, q_out=None):
+        """``write`` with the rotation of queries and keys on the way; returns the queries."""
+        return spec_rope_write(q, k, v, inv_freq, self.k[layer], self.v[layer], self.page_table,
+                               self.kv_lens, q_indptr, rows, positions, rope_start, interleaved,
+                               factor, page_counts=self.page_counts, q_out=q_out,
+                               **self._scales(layer))
+
     def attention(self, layer, q, q_indptr, max_q_len, max_kv_len, tree_mask=None, rows=None,
                   scale=None, out=None):
         return spec_attention(q, self.k[layer], self.v[layer], self.page_table, self.kv_lens,
@@ -366,5 +516,5 @@ class PagedKVCache:
 
 
 __all__ = ["PagedKVCache", "spec_attention", "spec_kv_compact", "spec_kv_copy_pages",
-           "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_set_option", "spec_tree_mask",
-           "spec_verify"]
+           "spec_kv_fork", "spec_kv_resize", "spec_kv_write", "spec_rope_write", "spec_set_option",
+           "spec_target_probs", "spec_tree_mask", "spec_verify"]
