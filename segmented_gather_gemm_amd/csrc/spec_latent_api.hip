@@ -257,10 +257,10 @@ namespace sgg {
 LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cache_bytes,
                          int32_t max_q_len, int64_t max_kv_len) {
   LatentShape s{};
-  constexpr int64_t kResident = 256;
+  constexpr int64_t kResident = 512;
   const int64_t rows = static_cast<int64_t>(max_q_len) * heads;
   s.padded_dim = latent <= 256 ? 256 : 512;
-  s.mb = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8;
+  s.mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   s.block_rows = 16 * s.mb;
   s.slot_bytes = static_cast<int64_t>(s.block_rows) * (s.padded_dim * 4 + 8);
   s.min_tiles = 2;

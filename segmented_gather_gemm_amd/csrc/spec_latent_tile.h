@@ -43,6 +43,7 @@ struct LatentDims {
   static constexpr int kKS = DL / 32;                 // steps of 32 columns, then 2 of the rope's
   static constexpr int kCols = DL / 16 / kWaves;      // 16-column tiles of a wave's values
   static constexpr int kSlotBytes = kRows * (DL * 4 + 8);
+  static_assert(kMine == 8, "the swizzles repeat with a wave's keys");
   static_assert((NST - 1) * kLoads <= 48, "too many loads under way");
 };
 
@@ -51,6 +52,9 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+// Keeps the compiler from computing what follows from x ahead of a loop.
+__device__ __forceinline__ void hide(int& x) { asm volatile("" : "+v"(x)); }
 
 // Where piece c of key r lies in its row: latents (rows of multiples of 256 bytes),
 // and the rope's 8 pieces.
@@ -82,7 +86,7 @@ struct LatentPlan {
   }
 };
 
-template <bool kFp16, bool kE4M3, int DL, int MB, int NST, int kPerSimd>
+template <bool kFp16, bool kE4M3, int DL, int MB, int NST, int kPerSimd, int kAhead>
 __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) {
   using D = LatentDims<kE4M3, DL, MB, NST>;
   const AttnParams& p = lp.a;
@@ -100,22 +104,13 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
   const bool scores = wave < D::kScoreWaves;
   const int latent = p.head_dim;
 
-  // fragment addresses in a tile
-  int ka[4], kr[2], va[D::kCols];
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    ka[s] = l16 * D::kRow + (((4 * s + g) ^ latent_swizzle(l16)) << 4);
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    kr[s] = D::kKeys * D::kRow + l16 * D::kRopeRow + (((4 * s + g) ^ rope_swizzle(l16)) << 4);
-  {
-    const int vr = 4 * g + (l16 >> 2);
-#pragma unroll
-    for (int j = 0; j < D::kCols; ++j) {
-      const int c = 2 * (wave * D::kCols + j) + (l16 >> 1 & 1);
-      va[j] = vr * D::kRow + ((c ^ latent_swizzle(vr)) << 4) + 8 * (l16 & 1);
-    }
-  }
+  // Fragment addresses in a tile.  A row begins at a multiple of the span that the
+  // swizzle permutes, so the pieces of other steps lie at these with bits flipped.
+  const int ka = l16 * D::kRow + ((g ^ latent_swizzle(l16)) << 4);
+  const int kr = D::kKeys * D::kRow + l16 * D::kRopeRow + ((g ^ rope_swizzle(l16)) << 4);
+  const int vr = 4 * g + (l16 >> 2), v0 = 2 * wave * D::kCols;
+  const int va = vr * D::kRow + (v0 / 16 << 8) +
+                 (((v0 % 16 + (l16 >> 1 & 1)) ^ latent_swizzle(vr)) << 4) + 8 * (l16 & 1);
   const int pieces = latent * (kE4M3 ? 1 : 2) / 16, rope_pieces = lp.rope * (kE4M3 ? 1 : 2) / 16;
   constexpr int kRopePieces = (kE4M3 ? D::kRawRope : D::kRopeRow) / 16;
 
@@ -168,14 +163,16 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
     // in lane order: the swizzle is on the source's side (the 8-bit ring has none).
     auto load_tile = [&](int tile, int stage) {
       char* base = lds + stage * D::kStage;
-      const int k8 = lane / 8;  // the key whose address this lane finds
-      const int key = min(tile * D::kKeys + wave * D::kMine + k8, end - 1);
+      int ll = lane;
+      hide(ll);  // (offsets are made anew rather than held in registers)
+      // the address of key ll / 8 of this wave's
+      const int key = min(tile * D::kKeys + wave * D::kMine + ll / 8, end - 1);
       const uint64_t mine =
           pages[(key >> p.c.page_shift) - slot0] + static_cast<uint64_t>(key & low) * token_bytes;
       const int lo = static_cast<int>(mine), hi = static_cast<int>(mine >> 32);
 #pragma unroll
       for (int i = 0; i < D::kMine / D::kPer; ++i) {
-        const int sub = lane / D::kPieces;  // which of this instruction's latents
+        const int sub = ll / D::kPieces;  // which of this instruction's latents
         uint32_t al = 0, ah = 0;
 #pragma unroll
         for (int j = 0; j < D::kPer; ++j) {
@@ -183,8 +180,8 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
           const uint32_t h = __builtin_amdgcn_readlane(hi, 8 * (i * D::kPer + j));
           if (j == 0 || sub == j) al = l, ah = h;
         }
-        const int r = wave * D::kMine + i * D::kPer + sub;
-        const int piece = (lane % D::kPieces) ^ (kE4M3 ? 0 : latent_swizzle(r));
+        const int piece =
+            (ll % D::kPieces) ^ (kE4M3 ? 0 : latent_swizzle(i * D::kPer + sub));
         const uint64_t at = (static_cast<uint64_t>(ah) << 32 | al) + 16 * piece;
         char* to = base + (wave * D::kMine + i * D::kPer) * (D::kPieces * 16);
         if (piece < pieces)
@@ -192,8 +189,8 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
                                            0);
       }
       // the rope's columns: 8 keys in one instruction
-      const int sub = lane / kRopePieces, r = wave * D::kMine + sub;
-      const int piece = (lane % kRopePieces) ^ (kE4M3 ? 0 : rope_swizzle(r));
+      const int sub = ll / kRopePieces;
+      const int piece = (ll % kRopePieces) ^ (kE4M3 ? 0 : rope_swizzle(sub));
       uint64_t at = mine;
       if constexpr (kE4M3) {
         const uint32_t l = __shfl(lo, 8 * (sub & 7)), h = __shfl(hi, 8 * (sub & 7));
@@ -242,20 +239,24 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
     u32x4_t qf[D::kMQ][D::kKS + 2];
     int tok_of[D::kMQ];
     if (scores) {
+      int gq = g;
+      hide(gq);  // the columns' offsets are not worth registers from one unit to the next
 #pragma unroll
       for (int m = 0; m < D::kMQ; ++m) {
         int tok, qh;
         const bool in = row_of(wave * D::kMQ + m, &tok, &qh);
         tok_of[m] = tok;
-        const char* qp = p.q + (q0 + tok) * p.q_token + qh * p.q_head;
+        // (all loads at once: what there is no row or column for reads its first and becomes 0)
+        const char* qp = p.q + (q0 + (in ? tok : 0)) * p.q_token + (in ? qh : 0) * p.q_head;
 #pragma unroll
         for (int s = 0; s < D::kKS + 2; ++s) {
           const bool rope = s >= D::kKS;
-          const int d0 = 32 * (rope ? s - D::kKS : s) + 8 * g;
-          qf[m][s] = in && d0 < (rope ? lp.rope : latent)
-                         ? *reinterpret_cast<const u32x4_t*>(qp + 2 * (d0 + (rope ? latent : 0)))
-                         : u32x4_t{0, 0, 0, 0};
-          qf[m][s] ^= flip;
+          const int d0 = 32 * (rope ? s - D::kKS : s) + 8 * gq;
+          const bool there = d0 < (rope ? lp.rope : latent);
+          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(
+              qp + (there ? 2 * (d0 + (rope ? latent : 0)) : 0));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[m][s][i] = in && there ? w[i] ^ flip : 0;
         }
       }
     }
@@ -322,6 +323,10 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
         }
         stage = stage + 1 == NST ? 0 : stage + 1;
         const int key0 = tile * D::kKeys;
+        int kx = ka, rx = kr, vx = va;
+        hide(kx);
+        hide(rx);
+        hide(vx);
         const bool open = key0 + D::kKeys <= open_end;  // every row sees the whole tile
         if (scores) {
           // S^T of two 16-key tiles
@@ -330,17 +335,28 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
           for (int m = 0; m < D::kMQ; ++m)
 #pragma unroll
             for (int t = 0; t < 2; ++t) st[m][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int s = 0; s < D::kKS + 2; ++s) {
+          // fragments of kAhead steps are under way while those before are multiplied
+          constexpr int kSteps = D::kKS + 2;
+          u32x4_t kf[kAhead + 1][2];
+          auto fetch = [&](int s) {
             const bool rope = s >= D::kKS;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const char* at = rope ? base + kr[s - D::kKS] + 16 * t * D::kRopeRow
-                                    : base + ka[s % 4] + 256 * (s / 4) + 16 * t * D::kRow;
-              const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(at);
+            for (int t = 0; t < 2; ++t)
+              kf[s % (kAhead + 1)][t] = *reinterpret_cast<const u32x4_t*>(
+                  rope ? base + (rx ^ ((s - D::kKS) << 6)) + 16 * t * D::kRopeRow
+                       : base + (kx ^ (s % 4 << 6)) + 256 * (s / 4) + 16 * t * D::kRow);
+          };
 #pragma unroll
-              for (int m = 0; m < D::kMQ; ++m) st[m][t] = attn_mfma<kFp16>(kf, qf[m][s], st[m][t]);
-            }
+          for (int s = 0; s < kAhead; ++s) fetch(s);
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            if (s + kAhead < kSteps) fetch(s + kAhead);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int m = 0; m < D::kMQ; ++m)
+                st[m][t] = attn_mfma<kFp16>(kf[s % (kAhead + 1)][t], qf[m][s], st[m][t]);
+            __builtin_amdgcn_sched_barrier(0);
           }
           if (!open) {
 #pragma unroll
@@ -402,7 +418,7 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
         }
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j) {
-          const char* at = base + va[j];
+          const char* at = base + (vx ^ (j << 5));
           const i32x2_t x = __builtin_bit_cast(
               i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)at));
           const i32x2_t y = __builtin_bit_cast(
@@ -431,6 +447,9 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
           stats[(wave * D::kMQ + m) * 16 + l16] = make_float2(mx[m] * scale, sum[m][0]);
     }
     lds_barrier();
+    int ge = g, le = lane;
+    hide(ge);
+    hide(le);
     if (chunks == 1) {
       const float vs = kE4M3 && p.k_scale ? *p.k_scale : 1.0f;
 #pragma unroll
@@ -442,7 +461,7 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
         char* op = p.out + (q0 + tok) * p.o_token + qh * p.o_head;
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j) {
-          const int d0 = 16 * (wave * D::kCols + j) + 4 * g;
+          const int d0 = 16 * (wave * D::kCols + j) + 4 * ge;
           if (d0 >= latent) continue;
           uint2 y;
           y.x = pack16<kFp16>(o[m][j][0] * inv, o[m][j][1] * inv);
@@ -459,7 +478,7 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
       for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j)
-          *reinterpret_cast<f32x4*>(slot + ((wave * MB + m) * D::kCols + j) * 1024 + lane * 16) =
+          *reinterpret_cast<f32x4*>(slot + ((wave * MB + m) * D::kCols + j) * 1024 + le * 16) =
               o[m][j];
       if (tid < D::kRows)
         *reinterpret_cast<float2*>(slot + D::kRows * DL * 4 + tid * 8) = stats[tid];
@@ -546,11 +565,11 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentParams lp) {
   }
 }
 
-template <bool kFp16, bool kE4M3, int DL, int MB, int NST, int kPerSimd>
+template <bool kFp16, bool kE4M3, int DL, int MB, int NST, int kAhead>
 hipError_t launch_latent_as(const LatentParams& p, const LatentShape& s, hipStream_t stream) {
   using D = LatentDims<kE4M3, DL, MB, NST>;
   if (s.block_rows != D::kRows || s.slot_bytes != D::kSlotBytes) return hipErrorInvalidValue;
-  latent_kernel<kFp16, kE4M3, DL, MB, NST, kPerSimd>
+  latent_kernel<kFp16, kE4M3, DL, MB, NST, 2, kAhead>
       <<<dim3(static_cast<uint32_t>(s.grid)), dim3(256), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.ranges <= 1) return e;
@@ -561,16 +580,15 @@ hipError_t launch_latent_as(const LatentParams& p, const LatentShape& s, hipStre
 
 template <bool kFp16, bool kE4M3>
 hipError_t launch_latent(const LatentParams& p, const LatentShape& s, hipStream_t stream) {
-#define SGG_LATENT(dl, m) \
-  if (s.padded_dim == dl && s.mb == m) return launch_latent_as<kFp16, kE4M3, dl, m, 4, 1>(p, s, stream)
-  SGG_LATENT(256, 1);
-  SGG_LATENT(256, 2);
-  SGG_LATENT(256, 4);
-  SGG_LATENT(256, 8);
-  SGG_LATENT(512, 1);
-  SGG_LATENT(512, 2);
-  SGG_LATENT(512, 4);
-  SGG_LATENT(512, 8);
+#define SGG_LATENT(dl, m, n, ahead)    \
+  if (s.padded_dim == dl && s.mb == m) \
+    return launch_latent_as<kFp16, kE4M3, dl, m, n, ahead>(p, s, stream)
+  SGG_LATENT(256, 1, 4, 3);
+  SGG_LATENT(256, 2, 4, 3);
+  SGG_LATENT(256, 4, 4, 2);
+  SGG_LATENT(512, 1, 2, 3);
+  SGG_LATENT(512, 2, 2, 3);
+  SGG_LATENT(512, 4, 2, 1);
 #undef SGG_LATENT
   return hipErrorInvalidValue;
 }
