@@ -365,14 +365,14 @@ int spec_latent_prefill(const void* q, int64_t q_token, int64_t q_head, const vo
  * 32 bits and in this order, of every value v with logit x:
  *   c = how often v stands in the request's text since its prompt and among the
  *   node and its ancestors; met = c > 0 or v stands in the prompt.
- *   met: x = x > 0 ? x / repetition[r] : x * repetition[r]
- *   x -= c * frequency[r];  x -= presence[r] if c > 0
- *   x += bias_values[b] for b = bias_indptr[r] .. bias_indptr[r + 1] with
- *   bias_ids[b] = v, added up in their order
+ *   met: x = x > 0 ? x * (1 / repetition[r]) : x * repetition[r]
+ *   x += bias - (c > 0 ? c * frequency[r] + presence[r] : 0), where bias is the sum of
+ *   bias_values[b] for b = bias_indptr[r] .. bias_indptr[r + 1] with bias_ids[b] = v,
+ *   added up in their order
  *   x = -inf if x is NaN or bit v % 32 of allowed[row][v / 32] is not set
  *   out = softmax(x / temperature[r]); a temperature that is not above 0: 1 at the
- *   first of the largest, 0 elsewhere.  Where the largest is +inf, its places share
- *   1 equally; a row that holds nothing but -inf becomes 0.
+ *   first of the largest, 0 elsewhere.  Infinities count as the largest numbers
+ *   (places of +inf share 1 equally); a row that holds nothing but -inf becomes 0.
  *   The text of request r is history[rows[r]] (rows NULL: r; [num_rows], ld_history
  *   apart, history_width entries) up to history_lens[row], its prompt up to
  *   prompt_lens[row] (NULL: none).  tokens, parents: the nodes as in spec_verify

@@ -36,7 +36,7 @@ struct ProbsParams {
   // workspace, [num_tokens][chunks]: maximum and sum of a chunk, index of the maximum
   float2* stats;
   int32_t* first;
-  int32_t chunks;
+  int32_t chunks, nodes;  // nodes of a workgroup; set by launch_probs
 };
 enum { kLogitsBf16 = 0, kLogitsFp16 = 1, kLogitsFp32 = 3 };
 int64_t probs_workspace_bytes(int64_t num_tokens, int64_t vocab);

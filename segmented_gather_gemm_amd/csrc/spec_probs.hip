@@ -7,6 +7,8 @@
 // once, in LDS, for all its nodes; what a node's path adds is a few entries, kept
 // in a list by node.  Two launches: the maximum and the sum of every chunk, then
 // the probabilities, which take the chunks' together.
+#include <cfloat>
+
 #include "spec_pages.h"
 #include "spec_probs.h"
 
@@ -16,143 +18,270 @@ namespace {
 constexpr int kProbsThreads = 256;
 constexpr int kProbsWaves = kProbsThreads / kWave;
 constexpr int kProbsNodes = 16;
-constexpr int kProbsEntries = 32;   // of a node's path in the chunk; more are walked again
-constexpr int kProbsTree = 1024;    // nodes whose parents and tokens are kept in LDS
+constexpr int kProbsEntries = 32;   // values of a node's path in the chunk; more are walked again
+constexpr int kProbsTree = 256;     // nodes whose parents and tokens are kept in LDS
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kProbsChunk == 8 * kProbsThreads, "a thread takes two groups of four values");
 
-// What the text says of a value: occurrences since the prompt, and two flags.
-constexpr uint32_t kInPrompt = 1u << 31, kBiased = 1u << 30, kCount = kBiased - 1;
+// Reduction over the 64 lanes by register moves: rotations within 16 lanes, then the
+// halves exchanged.  Every lane gets the result.
+template <int kRotate>
+__device__ __forceinline__ int rotated(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, 0x120 + kRotate, 0xf, 0xf, false);
+}
+template <class Op>
+__device__ __forceinline__ int over_lanes(int x, Op op) {
+  x = op(x, rotated<8>(x));
+  x = op(x, rotated<4>(x));
+  x = op(x, rotated<2>(x));
+  x = op(x, rotated<1>(x));
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = op(static_cast<int>(a[0]), static_cast<int>(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return op(static_cast<int>(b[0]), static_cast<int>(b[1]));
+}
+__device__ __forceinline__ float lanes_sum(float x) {
+  return __int_as_float(over_lanes(__float_as_int(x), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+__device__ __forceinline__ int lanes_min(int x) {
+  return over_lanes(x, [](int a, int b) { return min(a, b); });
+}
+// The largest of numbers that are no NaN, in a scalar register: compared as whole
+// numbers of the same order, which takes one instruction a step.
+__device__ __forceinline__ float lanes_max(float x) {
+  const int bits = __float_as_int(x);
+  const int top = __builtin_amdgcn_readfirstlane(
+      over_lanes(bits ^ (bits >> 31 & INT32_MAX), [](int a, int b) { return max(a, b); }));
+  return __int_as_float(top ^ (top >> 31 & INT32_MAX));
+}
+// What counts as nothing: NaN, -inf, and what the grammar does not allow.  Infinities are
+// the largest numbers from here on, so that differences are never NaN.
+constexpr float kNothing = -FLT_MAX;
+__device__ __forceinline__ float finite(float x) {  // (of NaN, the smallest of the three)
+  return __builtin_amdgcn_fmed3f(x, kNothing, FLT_MAX);
+}
+
+// What the text says of a value: occurrences since the prompt, and a flag.
+constexpr uint32_t kInPrompt = 1u << 31, kCount = kInPrompt - 1;
 
 struct ProbsShared {
   uint32_t word[kProbsChunk];
-  float bias[kProbsChunk];
+  float shift[kProbsChunk];          // what is added to a value's logit
+  float up[kProbsChunk];             // what it is multiplied with if above 0,
+  float down[kProbsChunk];           // and if not
+  uint8_t any[kProbsChunk / 4];      // whether one of four values has any of these
   int parent[kProbsTree], token[kProbsTree];
-  int entries[kProbsNodes];
-  uint16_t entry[kProbsNodes][kProbsEntries];
+  int entries[kProbsNodes];          // of `entry`, or more than there is room for
+  uint32_t entry[kProbsNodes][kProbsEntries];  // place in the chunk, occurrences << 16
   float2 stats[kProbsNodes][kProbsWaves];
   int first[kProbsNodes][kProbsWaves];
 };
 
-// The request's nodes, their parents and tokens.
-struct Nodes {
-  const ProbsParams& p;
-  const ProbsShared& s;
-  int q0;
-  __device__ __forceinline__ int parent(int i) const {
-    if (!p.parents) return i - 1;
-    const int x = i < kProbsTree ? s.parent[i] : p.parents[q0 + i];
-    return x >= 0 && x < i ? x : -1;
+// exp((x - top) / temperature), k = log2(e) / temperature.
+__device__ __forceinline__ float weight(float x, float top, float k) {
+  return __builtin_amdgcn_exp2f((x - top) * k);
+}
+
+// Four neighbouring logits as they lie in memory.  Rows need no more alignment than
+// their type has; values past the vocabulary are read as its last.
+template <int kType>
+struct Four {
+  typedef float F __attribute__((ext_vector_type(4), aligned(4)));
+  typedef uint32_t U __attribute__((ext_vector_type(2), aligned(2)));
+  static constexpr bool kWide = kType == kLogitsFp32;
+  uint32_t w[kWide ? 4 : 2];
+
+  __device__ __forceinline__ void load(const char* row, int v, int vocab) {
+    if (v + 4 <= vocab) {
+      if constexpr (kWide) {
+        const F f = *reinterpret_cast<const F*>(row + 4u * static_cast<uint32_t>(v));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(f[i]);
+      } else {
+        const U u = *reinterpret_cast<const U*>(row + 2u * static_cast<uint32_t>(v));
+        w[0] = u[0], w[1] = u[1];
+      }
+    } else {
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = min(v + i, vocab - 1);
+        if constexpr (kWide) x[i] = reinterpret_cast<const uint32_t*>(row)[at];
+        else x[i] = reinterpret_cast<const uint16_t*>(row)[at];
+      }
+      if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = x[i];
+      } else {
+        w[0] = x[0] | x[1] << 16, w[1] = x[2] | x[3] << 16;
+      }
+    }
   }
-  __device__ __forceinline__ int token(int i) const {
-    return i < kProbsTree ? s.token[i] : p.tokens[q0 + i];
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (kWide) return __uint_as_float(w[i]);
+    else return to_f32(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu, kType == kLogitsFp16);
   }
 };
-
-// Four neighbouring logits from value v on as floats; NaN and what lies past the
-// vocabulary are -inf.  Rows need no more alignment than their type.
-template <int kType>
-__device__ __forceinline__ void load4(const char* row, int64_t v, int64_t vocab, float* x) {
-  if (v + 4 <= vocab) {
-    if constexpr (kType == kLogitsFp32) {
-      typedef float F __attribute__((ext_vector_type(4), aligned(4)));
-      const F f = *reinterpret_cast<const F*>(row + 4 * v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = f[i];
-    } else {
-      typedef uint32_t U __attribute__((ext_vector_type(2), aligned(2)));
-      const U u = *reinterpret_cast<const U*>(row + 2 * v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = to_f32(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu, kType == kLogitsFp16);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = -INFINITY;
-      if (v + i >= vocab) continue;
-      if constexpr (kType == kLogitsFp32) x[i] = reinterpret_cast<const float*>(row)[v + i];
-      else x[i] = to_f32(reinterpret_cast<const uint16_t*>(row)[v + i], kType == kLogitsFp16);
-    }
-  }
-}
 
 template <int kType, bool kFinal>
 __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
   __shared__ ProbsShared s;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int chunk = blockIdx.x, r = blockIdx.y;
+  // Loads that do not wait for one another first: a small batch is a chain of them.
   const int q0 = p.q_indptr[r], q1 = p.q_indptr[r + 1];
-  if (q0 < 0 || q1 > p.num_tokens || q1 <= q0) return;
-  const int T = q1 - q0;
-  if (static_cast<int>(blockIdx.z) * kProbsNodes >= T) return;
   const int row = p.rows ? p.rows[r] : r;
-  const int64_t c0 = static_cast<int64_t>(chunk) * kProbsChunk;
-  const int here = static_cast<int>(min(p.vocab - c0, static_cast<int64_t>(kProbsChunk)));
-
-  // what the text and the biases say of the chunk's values
-  for (int e = tid; e < kProbsChunk; e += kProbsThreads) {
-    s.word[e] = 0;
-    s.bias[e] = 0.0f;
-  }
-  const bool path = p.tokens != nullptr;
-  if (path) {
-    for (int i = tid; i < min(T, kProbsTree); i += kProbsThreads) {
-      s.token[i] = p.tokens[q0 + i];
-      if (p.parents) s.parent[i] = p.parents[q0 + i];
-    }
-  }
-  __syncthreads();
-  if (p.history && row >= 0 && row < p.num_rows) {
-    const int len = min(max(p.history_lens[row], 0), p.width);
-    const int prompt = p.prompt_lens ? min(p.prompt_lens[row], len) : 0;
-    const int32_t* text = p.history + row * p.ld_history;
-    for (int i = tid; i < len; i += kProbsThreads) {
-      const int64_t at = text[i] - c0;
-      if (at < 0 || at >= here) continue;
-      if (i < prompt) atomicOr(&s.word[at], kInPrompt);
-      else atomicAdd(&s.word[at], 1u);
-    }
-  }
-  if (p.bias_indptr && wave == 0) {
-    // added in their order, so that an id named twice gives the same sum on every run
-    const int64_t b0 = max(p.bias_indptr[r], 0);
-    const int64_t b1 = min(static_cast<int64_t>(p.bias_indptr[r + 1]), p.num_bias);
-    for (int64_t b = b0; b < b1; b += kWave) {
-      const bool in = b + lane < b1;
-      const int64_t at = in ? p.bias_ids[b + lane] - c0 : -1;
-      const float value = in ? p.bias_values[b + lane] : 0.0f;
-      uint64_t left = __ballot(at >= 0 && at < here);
-      while (left) {
-        const int l = __ffsll(static_cast<unsigned long long>(left)) - 1;
-        left &= left - 1;
-        if (lane == l) {
-          s.bias[at] += value;
-          atomicOr(&s.word[at], kBiased);
-        }
-      }
-    }
-  }
-  const Nodes nodes{p, s, q0};
+  const int bias0 = p.bias_indptr ? p.bias_indptr[r] : 0;
+  const int bias1 = p.bias_indptr ? p.bias_indptr[r + 1] : 0;
   const float heat = p.temperature ? p.temperature[r] : 1.0f;
   const float rep = p.repetition ? p.repetition[r] : 1.0f;
   const float pres = p.presence ? p.presence[r] : 0.0f;
   const float freq = p.frequency ? p.frequency[r] : 0.0f;
-  const bool greedy = !(heat > 0.0f);
-  // (an infinite temperature must not make NaN of what is -inf)
-  const float k = fmaxf(kLog2e / heat, 0x1p-126f);
+  if (q0 < 0 || q1 > p.num_tokens || q1 <= q0) return;
+  const int T = q1 - q0;
+  if (static_cast<int>(blockIdx.z) * p.nodes >= T) return;
+  const bool told = p.history && row >= 0 && row < p.num_rows;
+  const int len = told ? min(max(p.history_lens[row], 0), p.width) : 0;
+  const int prompt = told && p.prompt_lens ? min(p.prompt_lens[row], len) : 0;
+  const int32_t* text = p.history + (told ? row * p.ld_history : 0);
+  const int vocab = static_cast<int>(p.vocab), c0 = chunk * kProbsChunk;
+  const int here = min(vocab - c0, kProbsChunk);
 
-  for (int i0 = blockIdx.z * kProbsNodes; i0 < T; i0 += gridDim.z * kProbsNodes) {
-    const int count = min(kProbsNodes, T - i0);
+  // Nodes' logits and their rows of the grammar's mask; those of the next two nodes are
+  // under way while one is computed.
+  Four<kType> raw[3][2];
+  uint32_t mask[3][2] = {};
+  auto fetch = [&](int d, int i) {
+    const int64_t n = q0 + i;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int v = c0 + 4 * (tid + g * kProbsThreads);
+      raw[d][g].load(p.logits + n * p.ld_logits, v, vocab);
+      if (p.allowed)
+        mask[d][g] = (p.allowed + n * p.ld_allowed)[static_cast<uint32_t>(min(v, vocab - 1)) >> 5];
+    }
+  };
+  {
+    const int i = blockIdx.z * p.nodes;
+    fetch(0, i);
+    fetch(1, min(i + 1, T - 1));
+  }
+  const bool path = p.tokens != nullptr;
+  int first_token = 0, first_parent = 0;
+  if (path && tid < T) {
+    first_token = p.tokens[q0 + tid];
+    if (p.parents) first_parent = p.parents[q0 + tid];
+  }
+  // where in the chunk a value lies, -1: not in it
+  auto place = [&](int v) {
+    const uint32_t at = static_cast<uint32_t>(v) - static_cast<uint32_t>(c0);
+    return v >= 0 && at < static_cast<uint32_t>(here) ? static_cast<int>(at) : -1;
+  };
+  const int64_t b0 = max(bias0, 0), b1 = min(static_cast<int64_t>(bias1), p.num_bias);
+  auto bias_at = [&](int64_t b) { return b < b1 ? place(p.bias_ids[b]) : -1; };
+  int bias_spot = -1;
+  float bias_value = 0.0f;
+  if (wave == 0 && b0 + lane < b1) {
+    bias_spot = bias_at(b0 + lane);
+    bias_value = p.bias_values[b0 + lane];
+  }
+
+  // what the text and the biases say of the chunk's values
+  for (int e = tid; e < kProbsChunk; e += kProbsThreads) {
+    s.word[e] = 0;
+    s.shift[e] = 0.0f;
+  }
+  if (path) {
+    for (int i = tid; i < min(T, kProbsTree); i += kProbsThreads) {
+      s.token[i] = i == tid ? first_token : p.tokens[q0 + i];
+      if (p.parents) s.parent[i] = i == tid ? first_parent : p.parents[q0 + i];
+    }
+  }
+  __syncthreads();
+  // (a batch of loads at a time, all under way at once)
+  constexpr int kBatch = 8;
+  for (int i0 = tid; i0 < len; i0 += kBatch * kProbsThreads) {
+    int at[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) at[b] = text[min(i0 + b * kProbsThreads, len - 1)];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kProbsThreads;
+      const int x = place(at[b]);
+      if (i >= len || x < 0) continue;
+      if (i < prompt) atomicOr(&s.word[x], kInPrompt);
+      else atomicAdd(&s.word[x], 1u);
+    }
+  }
+  if (wave == 0) {
+    // added in their order, so that an id named twice gives the same sum on every run
+    for (int64_t b = b0; b < b1; b += kWave) {
+      uint64_t left = __ballot(bias_spot >= 0);
+      while (left) {
+        const int l = __ffsll(static_cast<unsigned long long>(left)) - 1;
+        left &= left - 1;
+        if (lane == l) s.shift[bias_spot] += bias_value;
+      }
+      bias_spot = bias_at(b + kWave + lane);
+      if (bias_spot >= 0) bias_value = p.bias_values[b + kWave + lane];
+    }
+  }
+  __syncthreads();
+  // A value's logit x becomes x * (x > 0 ? up : down) + shift: what a node's path does not
+  // change is made once.
+  const float rep_inv = 1.0f / rep;
+  for (int e = tid; e < kProbsChunk / 4; e += kProbsThreads) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = s.word[4 * e + i], given = w & kCount;
+      float shift = s.shift[4 * e + i];
+      if (given) shift -= static_cast<float>(given) * freq + pres;
+      s.shift[4 * e + i] = shift;
+      s.up[4 * e + i] = w ? rep_inv : 1.0f;
+      s.down[4 * e + i] = w ? rep : 1.0f;
+      any |= w != 0 || shift != 0.0f;
+    }
+    s.any[e] = any;
+  }
+  // (each memory by its own address space, which keeps the loads apart)
+  typedef const __attribute__((address_space(3))) int* LdsInts;
+  typedef const __attribute__((address_space(1))) int* GlobalInts;
+  auto node_of = [&](const int* near, const int32_t* far, int i) {
+    if (i < kProbsTree) return ((LdsInts)near)[i];
+    return ((GlobalInts)far)[q0 + i];
+  };
+  auto parent_of = [&](int i) {
+    if (!p.parents) return i - 1;
+    const int x = node_of(s.parent, p.parents, i);
+    return x >= 0 && x < i ? x : -1;
+  };
+  auto token_of = [&](int i) { return node_of(s.token, p.tokens, i); };
+  const bool greedy = !(heat > 0.0f);
+  // (what is nothing stays so at any temperature, and a tiny one does not make NaN of 0)
+  const float k = fminf(fmaxf(kLog2e / heat, 0x1p-100f), 0x1p127f);
+
+  for (int i0 = blockIdx.z * p.nodes; i0 < T; i0 += gridDim.z * p.nodes) {
+    const int count = min(p.nodes, T - i0);
     __syncthreads();  // the words are there; the last nodes' lists have been read
     if (tid < count) {
       int n = 0;
       if (path) {
-        for (int i = i0 + tid; i >= 0; i = nodes.parent(i)) {
-          const int64_t at = nodes.token(i) - c0;
-          if (at < 0 || at >= here) continue;
-          if (n < kProbsEntries) s.entry[tid][n] = static_cast<uint16_t>(at);
-          ++n;
+        for (int i = i0 + tid; i >= 0; i = parent_of(i)) {
+          const int at = place(token_of(i));
+          if (at < 0) continue;
+          int e = 0;
+          while (e < min(n, kProbsEntries) && (s.entry[tid][e] & 0xffffu) != static_cast<uint32_t>(at))
+            ++e;
+          if (e < n && e < kProbsEntries) {
+            if (s.entry[tid][e] >= 0xffff0000u) n = kProbsEntries + 1;  // (walked again)
+            s.entry[tid][e] += 1u << 16;
+          } else {
+            if (n < kProbsEntries) s.entry[tid][n] = static_cast<uint32_t>(at) | 1u << 16;
+            n = min(n, kProbsEntries) + 1;
+          }
         }
       }
       s.entries[tid] = n;
@@ -161,7 +290,7 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
       // maximum and sum of each node's row from its chunks'
       for (int j = wave; j < count; j += kProbsWaves) {
         const int64_t at = static_cast<int64_t>(q0 + i0 + j) * p.chunks;
-        float top = -INFINITY;
+        float top = kNothing;
         int first = INT32_MAX;
         for (int c = lane; c < p.chunks; c += kWave) {
           const float m = p.stats[at + c].x;
@@ -180,7 +309,7 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
         double sum = 0.0;
         for (int c = lane; c < p.chunks; c += kWave) {
           const float2 x = p.stats[at + c];
-          sum += x.x == top ? x.y : x.y * __builtin_amdgcn_exp2f((x.x - top) * k);
+          sum += x.y * weight(x.x, top, k);
         }
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2) sum += __shfl_xor(sum, d);
@@ -191,106 +320,134 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
       }
     }
     __syncthreads();
+    if (i0 > static_cast<int>(blockIdx.z) * p.nodes) {
+      fetch(0, i0);
+      fetch(1, min(i0 + 1, T - 1));
+    }
 #pragma unroll 1
     for (int j = 0; j < count; ++j) {
       const int64_t n = q0 + i0 + j;
-      const char* logits = p.logits + n * p.ld_logits;
-      const int entries = s.entries[j];
-      float x[2][4];
+      fetch(2, min(i0 + j + 2, T - 1));
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = raw[0][i / 4][i % 4];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int at = 4 * (tid + g * kProbsThreads);
-        const int64_t v = c0 + at;
-        load4<kType>(logits, v, p.vocab, x[g]);
-        uint32_t bits = 15u;
-        if (p.allowed && at < here)
-          bits = p.allowed[n * p.ld_allowed + (v >> 5)] >> (v & 31);
-        const uint4 w4 = *reinterpret_cast<const uint4*>(&s.word[at]);
-        uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        if (entries <= kProbsEntries) {
-          for (int e = 0; e < entries; ++e) {
-            const int d = s.entry[j][e] - at;
+        if (s.any[at / 4]) {
+          const f32x4 up = *reinterpret_cast<const f32x4*>(&s.up[at]);
+          const f32x4 down = *reinterpret_cast<const f32x4*>(&s.down[at]);
+          const f32x4 shift = *reinterpret_cast<const f32x4*>(&s.shift[at]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] += d == i;
-          }
-        } else {
-          for (int i = i0 + j; i >= 0; i = nodes.parent(i)) {
-            const int64_t d = nodes.token(i) - v;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) w[u] += d == u;
-          }
-        }
-        if (w[0] | w[1] | w[2] | w[3]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t given = w[i] & kCount;
-            float y = x[g][i];
-            if (w[i] & ~kBiased) y = y > 0.0f ? y / rep : y * rep;
-            y = __fsub_rn(y, __fmul_rn(static_cast<float>(given), freq));
-            if (given) y = __fsub_rn(y, pres);
-            if (w[i] & kBiased) y = __fadd_rn(y, s.bias[at + i]);
-            x[g][i] = y;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[g][i] = fmaxf(x[g][i], -INFINITY);  // NaN gives way
-          if (!(bits >> i & 1) || at + i >= here) x[g][i] = -INFINITY;
+          for (int i = 0; i < 4; ++i)
+            x[4 * g + i] = fmaf(x[4 * g + i], x[4 * g + i] > 0.0f ? up[i] : down[i], shift[i]);
         }
       }
+      const int entries = __builtin_amdgcn_readfirstlane(s.entries[j]);
+      if (__builtin_expect(entries > 0, 0)) {
+        // values that the node's path holds, from their logits once more
+        auto redo = [&](int at, uint32_t more) {
+          const int u = at - 4 * tid;
+          const int mine = u >= 0 && u < 4 ? u
+                           : u >= 4 * kProbsThreads && u < 4 * kProbsThreads + 4
+                               ? u - 4 * kProbsThreads + 4
+                               : -1;
+          if (mine < 0) return;
+          float extra = static_cast<float>(more) * freq;
+          if (!(s.word[at] & kCount)) extra += pres;
+          const float shift = s.shift[at] - extra;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float y = raw[0][i / 4][i % 4];
+            if (mine == i) x[i] = fmaf(y, y > 0.0f ? rep_inv : rep, shift);
+          }
+        };
+        if (entries <= kProbsEntries) {
+          for (int e = 0; e < entries; ++e) redo(s.entry[j][e] & 0xffffu, s.entry[j][e] >> 16);
+        } else {
+          // (a value's last place on the way up counts all of them)
+          for (int i = i0 + j; i >= 0; i = parent_of(i)) {
+            const int at = place(token_of(i));
+            if (at < 0) continue;
+            uint32_t more = 0;
+            for (int k2 = i0 + j; k2 >= 0; k2 = parent_of(k2)) more += place(token_of(k2)) == at;
+            redo(at, more);
+          }
+        }
+      }
+      if (p.allowed) {  // (all bits set: a NaN)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t off = ~mask[0][i / 4] >> (4 * tid & 31);
+          x[i] = __int_as_float(__float_as_int(x[i]) |
+                                (static_cast<int32_t>(off << (31 - i % 4)) >> 31));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = finite(x[i]);
+      if (here < kProbsChunk) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (4 * (tid + i / 4 * kProbsThreads) + i % 4 >= here) x[i] = kNothing;
+      }
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          raw[d][g] = raw[d + 1][g];
+          mask[d][g] = mask[d + 1][g];
+        }
       if constexpr (!kFinal) {
-        float top = x[0][0];
+        float top = x[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i / 4][i % 4]);
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
+        top = lanes_max(top);
         float sum = 0.0f;
         int first = INT32_MAX;
-        if (top != -INFINITY) {
-          if (greedy) {
+        if (top == kNothing) {
+        } else if (greedy) {
 #pragma unroll
-            for (int i = 7; i >= 0; --i)
-              if (x[i / 4][i % 4] == top)
-                first = static_cast<int>(c0) + 4 * (tid + i / 4 * kProbsThreads) + i % 4;
+          for (int i = 7; i >= 0; --i)
+            if (x[i] == top) first = c0 + 4 * (tid + i / 4 * kProbsThreads) + i % 4;
+          first = lanes_min(first);
+        } else {
 #pragma unroll
-            for (int d = 1; d < kWave; d *= 2) first = min(first, __shfl_xor(first, d));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float y = x[i / 4][i % 4];
-              sum += y == top ? 1.0f : __builtin_amdgcn_exp2f((y - top) * k);
-            }
-#pragma unroll
-            for (int d = 1; d < kWave; d *= 2) sum += __shfl_xor(sum, d);
-          }
+          for (int i = 0; i < 8; ++i) sum += weight(x[i], top, k);
+          sum = lanes_sum(sum);
         }
         if (lane == 0) {
           s.stats[j][wave] = make_float2(top, sum);
           s.first[j][wave] = first;
         }
       } else {
-        const float top = s.stats[j][0].x, inv = s.stats[j][0].y;
+        const float top =
+            __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(s.stats[j][0].x)));
+        const float inv = s.stats[j][0].y;
         const int first = s.first[j][0];
         float* out = p.out + n * p.ld_out;
+        float y[8];
+        if (top == kNothing) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+        } else if (greedy) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = c0 + 4 * (tid + i / 4 * kProbsThreads) + i % 4 == first ? 1.0f : 0.0f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = weight(x[i], top, k) * inv;
+        }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const int at = 4 * (tid + g * kProbsThreads);
-          const int64_t v = c0 + at;
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float z = x[g][i];
-            y[i] = greedy ? (v + i == first ? 1.0f : 0.0f)
-                          : (z == top ? 1.0f : __builtin_amdgcn_exp2f((z - top) * k)) * inv;
-            if (top == -INFINITY) y[i] = 0.0f;
-          }
+          const int at = 4 * (tid + g * kProbsThreads), v = c0 + at;
           if (at + 4 <= here) {
             typedef float F __attribute__((ext_vector_type(4), aligned(4)));
-            *reinterpret_cast<F*>(out + v) = F{y[0], y[1], y[2], y[3]};
+            *reinterpret_cast<F*>(out + static_cast<uint32_t>(v)) =
+                F{y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]};
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (at + i < here) out[v + i] = y[i];
+              if (at + i < here) out[v + i] = y[4 * g + i];
           }
         }
       }
@@ -298,7 +455,7 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
     if constexpr (!kFinal) {
       __syncthreads();
       if (tid < count) {
-        float top = -INFINITY, sum = 0.0f;
+        float top = kNothing, sum = 0.0f;
         int first = INT32_MAX;
 #pragma unroll
         for (int w = 0; w < kProbsWaves; ++w) {
@@ -310,7 +467,7 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
 #pragma unroll
         for (int w = 0; w < kProbsWaves; ++w) {
           const float2 x = s.stats[tid][w];
-          sum += x.x == top ? x.y : x.y * __builtin_amdgcn_exp2f((x.x - top) * k);
+          sum += x.y * weight(x.x, top, k);
         }
         const int64_t at = static_cast<int64_t>(q0 + i0 + tid) * p.chunks + chunk;
         p.stats[at] = make_float2(top, sum);
@@ -332,7 +489,12 @@ hipError_t launch_probs(ProbsParams p, int dtype, void* workspace, hipStream_t s
   p.chunks = static_cast<int32_t>(chunks_of(p.vocab));
   p.stats = static_cast<float2*>(workspace);
   p.first = reinterpret_cast<int32_t*>(p.stats + static_cast<int64_t>(p.num_tokens) * p.chunks);
-  int groups = (p.max_q_len + kProbsNodes - 1) / kProbsNodes;
+  // Nodes of a workgroup share its counts of the text; a small batch has a workgroup for
+  // each node rather (one user's 5 nodes of 32000 values: us with 16 a workgroup).
+  p.nodes = kProbsNodes;
+  const int64_t all = static_cast<int64_t>(p.chunks) * p.num_tokens;
+  while (p.nodes > 1 && all / p.nodes < 1024) p.nodes /= 2;
+  int groups = (p.max_q_len + p.nodes - 1) / p.nodes;
   groups = groups < 1 ? 1 : groups > 64 ? 64 : groups;
   const dim3 grid(p.chunks, p.bs, groups), block(kProbsThreads);
   for (int pass = 0; pass < 2; ++pass) {

@@ -2,7 +2,7 @@
 
 Tolerance, relative to the probability p of a value whose x (before the softmax) lies z below the
 row's largest, in units of the temperature T, with X the largest magnitude on the way to any x of
-the row: x takes at most 5 roundings of 2^-24 X, twice in a difference, 2^-20 X / T; the exponent's
+the row: x takes at most 7 roundings of 2^-24 X, twice in a difference, 2^-20 X / T; the exponent's
 own roundings and the hardware's exponential 2^-21 + 2^-22 z; the same again for the sum, where z
 counts with its probability and is below 32: 2^-18 + 2^-19 X / T + 2^-21 z in all.
 """
