@@ -320,7 +320,8 @@ int spec_latent_gather(const SpecLatentCache* cache, const int32_t* page_table, 
  *   (NULL: 1).  Rows that a token does not see have no part in its result; one that
  *   sees a row with an infinity or NaN has no particular result.
  *   workspace: spec_latent_attention_workspace_bytes(), 16-byte aligned, not shared
- *   by overlapping calls; it may be the one of spec_attention() and spec_verify().
+ *   by overlapping calls; it may be the one of spec_attention() and spec_verify()
+ *   (what those keep at zero is left alone).
  *   The same inputs give the same bits on every run.
  */
 int64_t spec_latent_attention_workspace_bytes(int32_t bs, int32_t num_heads, int32_t latent_dim,

@@ -10,21 +10,26 @@ namespace sgg {
 // number of query heads, and the output has head_dim = latent columns.
 struct LatentParams {
   AttnParams a;
+  int4* split;  // [ranges]: first token, tokens, row block and pieces of a unit
   int32_t rope;
 };
 
-// Row blocks of 16 * mb query rows, tiles of 32 keys, latents padded to padded_dim.
+// Row blocks, tiles of 32 keys, latents padded to padded_dim.
 struct LatentShape {
-  int32_t mb, block_rows, padded_dim;
+  int32_t block_rows, padded_dim;
   int32_t min_tiles, ranges;  // ranges 0: each workgroup takes one unit
+  bool fine;                  // units in many pieces: small items for the join
   int64_t grid, slot_bytes;
 };
 constexpr int kLatentKeys = 32;
 LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cache_bytes,
                          int32_t max_q_len, int64_t max_kv_len);
-// Bytes of workspace: two slots a range.
+// Bytes of workspace: LatentParams::split, then two slots a range.
+inline int64_t latent_splits(const LatentShape& s) {
+  return (s.ranges * int64_t{sizeof(int4)} + 255) / 256 * 256;
+}
 inline int64_t latent_workspace(const LatentShape& s) {
-  return s.ranges > 1 ? 2 * s.ranges * s.slot_bytes : 0;
+  return s.ranges > 1 ? latent_splits(s) + 2 * s.ranges * s.slot_bytes : 0;
 }
 
 // One for each type of queries and cache (spec_latent_*.hip).

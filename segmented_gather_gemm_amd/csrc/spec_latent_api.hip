@@ -257,25 +257,25 @@ namespace sgg {
 LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cache_bytes,
                          int32_t max_q_len, int64_t max_kv_len) {
   LatentShape s{};
-  constexpr int64_t kResident = 512;
   const int64_t rows = static_cast<int64_t>(max_q_len) * heads;
   s.padded_dim = latent <= 256 ? 256 : 512;
-  s.mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  s.block_rows = 16 * s.mb;
+  s.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int64_t resident = s.block_rows == 128 ? 256 : 512;  // workgroups on the GPU at once
   s.slot_bytes = static_cast<int64_t>(s.block_rows) * (s.padded_dim * 4 + 8);
   s.min_tiles = 2;
   const int64_t blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
   const int64_t units = bs * blocks;
-  if (blocks > 1 && units >= 2 * kResident) {
+  if (blocks > 1 && units >= 2 * resident) {
     s.ranges = 0;
     s.grid = units;
   } else {
     const int64_t tiles = (max_kv_len + kLatentKeys - 1) / kLatentKeys;
     const int64_t most = units * ((tiles + s.min_tiles - 1) / s.min_tiles);
-    const int64_t n = most < kResident ? most : kResident;
+    const int64_t n = most < resident ? most : resident;
     s.ranges = static_cast<int32_t>(n < 1 ? 1 : n);
     // (the kernel may take the batch by units)
     s.grid = units > s.ranges ? units : s.ranges;
+    s.fine = s.ranges >= 8 * units;
   }
   return s;
 }
@@ -341,7 +341,10 @@ extern "C" int spec_latent_attention(const void* q, int64_t q_token, int64_t q_h
   p.q_indptr = q_indptr;
   p.mask = reinterpret_cast<const uint64_t*>(tree_mask);
   p.k_scale = cache_scale;
-  p.part = workspace ? partials_of(workspace) : nullptr;
+  if (s.ranges > 1) {
+    lp.split = reinterpret_cast<int4*>(partials_of(workspace));
+    p.part = partials_of(workspace) + sgg::latent_splits(s);
+  }
   p.num_tokens = num_tokens;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.bs = bs;

@@ -22,11 +22,12 @@
 
 namespace sgg {
 
-template <bool kE4M3, int DL, int MB, int NST>
+template <bool kE4M3, int DL, int MB, int NG, int NST>
 struct LatentDims {
-  static constexpr int kWaves = 4;
+  static constexpr int kWaves = 4 * NG;               // NG groups of four, each with rows of its own
   static constexpr int kThreads = kWaves * kWave;
-  static constexpr int kRows = 16 * MB;
+  static constexpr int kFrags = MB * NG;              // row fragments
+  static constexpr int kRows = 16 * kFrags;
   static constexpr int kKeys = kLatentKeys;
   static constexpr int kMine = kKeys / kWaves;        // keys that a wave loads
   static constexpr int kRopeRow = 128;                // bytes of 64 columns, 16-bit
@@ -37,13 +38,13 @@ struct LatentDims {
   static constexpr int kPieces = (kE4M3 ? kRawRow : kRow) / 16;  // of a latent
   static constexpr int kPer = kWave / kPieces;        // latents of a load instruction
   static constexpr int kLoads = kMine / kPer + 1;     // a wave and tile
-  static constexpr int kRing = NST * kStage + (kE4M3 ? kTile : 0);
-  static constexpr int kScoreWaves = MB < kWaves ? MB : kWaves;
-  static constexpr int kMQ = MB / kScoreWaves;        // row fragments of a wave's scores
+  // Two groups fill the CU: scores and values of neighbouring tiles in one turn.
+  static constexpr bool kTwo = NG == 2;
+  static constexpr int kRing = NST * kStage + (kE4M3 ? (kTwo ? 2 : 1) * kTile : 0);
   static constexpr int kKS = DL / 32;                 // steps of 32 columns, then 2 of the rope's
-  static constexpr int kCols = DL / 16 / kWaves;      // 16-column tiles of a wave's values
+  static constexpr int kCols = DL / 16 / 4;           // 16-column tiles of a wave's values
   static constexpr int kSlotBytes = kRows * (DL * 4 + 8);
-  static_assert(kMine == 8, "the swizzles repeat with a wave's keys");
+  static_assert(MB <= 4, "a wave takes the scores of one row fragment");
   static_assert((NST - 1) * kLoads <= 48, "too many loads under way");
 };
 
@@ -61,7 +62,7 @@ __device__ __forceinline__ void hide(int& x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ int latent_swizzle(int r) { return 2 * (r & 7); }
 __device__ __forceinline__ int rope_swizzle(int r) { return r & 6; }
 
-// A range of positions of the batch (see AttnWork), the same for the kernel and the join.
+// The ranges of positions of a batch (see AttnWork).
 template <int NW, int R, int K>
 struct LatentPlan {
   AttnWork<NW, R, K> work;
@@ -86,29 +87,34 @@ struct LatentPlan {
   }
 };
 
-template <bool kFp16, bool kE4M3, int DL, int MB, int NST, int kPerSimd, int kAhead>
-__global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) {
-  using D = LatentDims<kE4M3, DL, MB, NST>;
+template <bool kFp16, bool kE4M3, int DL, int MB, int NG, int NST, int kAhead, int kQL>
+__global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
+  using D = LatentDims<kE4M3, DL, MB, NG, NST>;
   const AttnParams& p = lp.a;
   constexpr int kWindow = 256;  // pages whose addresses are held in LDS
+  constexpr int kAheadV = 2;    // value fragments under way
   __shared__ __align__(1024) char lds[D::kRing];
-  __shared__ u32x4_t weights[MB][kWave];
+  constexpr int kBufs = D::kTwo ? 2 : 1;
+  __shared__ u32x4_t weights[kBufs][D::kFrags][kWave];
+  __shared__ u32x4_t queries[kQL > 0 ? D::kFrags : 1][kQL > 0 ? kQL : 1][kWave];
   __shared__ uint64_t pages[kWindow];
-  __shared__ AttnFind<4> find;
-  __shared__ float alpha[D::kRows];
+  __shared__ AttnFind<D::kWaves> find;
+  __shared__ float alpha[kBufs][D::kRows];
   __shared__ float2 stats[D::kRows];
-  __shared__ __align__(16) int moved[MB < 4 ? 4 : MB];
+  __shared__ __align__(16) int moved[kBufs][NG][4];
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   const int l16 = lane % 16, g = lane / 16;
-  const bool scores = wave < D::kScoreWaves;
+  const int group = wave / 4, w4 = wave % 4;
+  const bool scores = w4 < MB;               // whether this wave takes scores,
+  const int mine = group * MB + w4;          // those of this row fragment
   const int latent = p.head_dim;
 
   // Fragment addresses in a tile.  A row begins at a multiple of the span that the
   // swizzle permutes, so the pieces of other steps lie at these with bits flipped.
   const int ka = l16 * D::kRow + ((g ^ latent_swizzle(l16)) << 4);
   const int kr = D::kKeys * D::kRow + l16 * D::kRopeRow + ((g ^ rope_swizzle(l16)) << 4);
-  const int vr = 4 * g + (l16 >> 2), v0 = 2 * wave * D::kCols;
+  const int vr = 4 * g + (l16 >> 2), v0 = 2 * w4 * D::kCols;
   const int va = vr * D::kRow + (v0 / 16 << 8) +
                  (((v0 % 16 + (l16 >> 1 & 1)) ^ latent_swizzle(vr)) << 4) + 8 * (l16 & 1);
   const int pieces = latent * (kE4M3 ? 1 : 2) / 16, rope_pieces = lp.rope * (kE4M3 ? 1 : 2) / 16;
@@ -119,7 +125,7 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
   const float scale = signed_scale == 0.0f ? 0x1p-126f : fabsf(signed_scale);
   const uint32_t flip = signed_scale < 0.0f ? 0x80008000u : 0u;
 
-  LatentPlan<4, D::kRows, D::kKeys> plan(p, &find);
+  LatentPlan<D::kWaves, D::kRows, D::kKeys> plan(p, &find);
   const uint32_t range = blockIdx.x;
   const uint32_t per_range = plan.per_range;
   const int total = plan.total;
@@ -127,6 +133,9 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
   int pos = range < used ? static_cast<int>(range * per_range) : total;
   const int stop =
       plan.work.by_unit ? total : pos + min(total - pos, static_cast<int>(per_range));
+  // What the join finds of this range: the unit that begins in it and goes on past it.
+  if (tid == 0 && p.ranges > 1 && range < static_cast<uint32_t>(p.ranges))
+    lp.split[range] = make_int4(0, 0, 0, 0);
   while (pos < stop) {
     const AttnUnit u = attn_locate(plan.work, &find, plan.share, pos);
     const int64_t q0 = u.q.first;
@@ -146,7 +155,8 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
       if (tile1 - tile0 < tiles) {
         const uint32_t range0 = uniform(static_cast<uint32_t>(u.start) / per_range);
         chunk = static_cast<int>(range - range0);
-        chunks = 2;
+        chunks = uniform(static_cast<uint32_t>(u.start + tiles - 1) / per_range) - range0 + 1;
+        if (tid == 0 && chunk == 0) lp.split[range] = make_int4(u.q.first, T, u.mb, chunks);
       }
     }
 
@@ -166,10 +176,11 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
       int ll = lane;
       hide(ll);  // (offsets are made anew rather than held in registers)
       // the address of key ll / 8 of this wave's
-      const int key = min(tile * D::kKeys + wave * D::kMine + ll / 8, end - 1);
-      const uint64_t mine =
+      const int key =
+          min(tile * D::kKeys + wave * D::kMine + min(ll / 8, D::kMine - 1), end - 1);
+      const uint64_t at8 =
           pages[(key >> p.c.page_shift) - slot0] + static_cast<uint64_t>(key & low) * token_bytes;
-      const int lo = static_cast<int>(mine), hi = static_cast<int>(mine >> 32);
+      const int lo = static_cast<int>(at8), hi = static_cast<int>(at8 >> 32);
 #pragma unroll
       for (int i = 0; i < D::kMine / D::kPer; ++i) {
         const int sub = ll / D::kPieces;  // which of this instruction's latents
@@ -180,18 +191,19 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
           const uint32_t h = __builtin_amdgcn_readlane(hi, 8 * (i * D::kPer + j));
           if (j == 0 || sub == j) al = l, ah = h;
         }
-        const int piece =
-            (ll % D::kPieces) ^ (kE4M3 ? 0 : latent_swizzle(i * D::kPer + sub));
+        const int r = wave * D::kMine + i * D::kPer + sub;
+        const int piece = (ll % D::kPieces) ^ (kE4M3 ? 0 : latent_swizzle(r));
         const uint64_t at = (static_cast<uint64_t>(ah) << 32 | al) + 16 * piece;
         char* to = base + (wave * D::kMine + i * D::kPer) * (D::kPieces * 16);
         if (piece < pieces)
           __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)at, (SGG_LDS void*)to, 16, 0,
                                            0);
       }
-      // the rope's columns: 8 keys in one instruction
+      // the rope's columns: all of this wave's keys in one instruction
       const int sub = ll / kRopePieces;
-      const int piece = (ll % kRopePieces) ^ (kE4M3 ? 0 : rope_swizzle(sub));
-      uint64_t at = mine;
+      const int piece =
+          (ll % kRopePieces) ^ (kE4M3 ? 0 : rope_swizzle(wave * D::kMine + sub));
+      uint64_t at = at8;
       if constexpr (kE4M3) {
         const uint32_t l = __shfl(lo, 8 * (sub & 7)), h = __shfl(hi, 8 * (sub & 7));
         at = static_cast<uint64_t>(h) << 32 | l;
@@ -208,9 +220,8 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
       else wait_vm<NST >= 4 ? 2 * D::kLoads : 0>();
     };
     // the 8-bit tile into the 16-bit one: 16 values a thread and turn
-    auto widen_tile = [&](int stage) {
+    auto widen_tile = [&](int stage, char* to) {
       const char* from = lds + stage * D::kStage;
-      char* to = lds + NST * D::kStage;
       constexpr int kAll = D::kKeys * (DL + 64) / 16;
       for (int e = tid; e < kAll; e += D::kThreads) {
         const uint4 w = *reinterpret_cast<const uint4*>(from + 16 * e);
@@ -236,28 +247,28 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
       *qh = static_cast<int>(row) - *tok * p.group;
       return *tok < T;
     };
-    u32x4_t qf[D::kMQ][D::kKS + 2];
-    int tok_of[D::kMQ];
+    constexpr int kSteps = D::kKS + 2, kQR = kSteps - kQL;
+    u32x4_t qf[kQR];  // of the first steps; the rest lie in LDS
+    int my_tok = 0;
     if (scores) {
       int gq = g;
       hide(gq);  // the columns' offsets are not worth registers from one unit to the next
+      int qh;
+      const bool in = row_of(mine, &my_tok, &qh);
+      // (all loads at once: what there is no row or column for reads its first and becomes 0)
+      const char* qp = p.q + (q0 + (in ? my_tok : 0)) * p.q_token + (in ? qh : 0) * p.q_head;
 #pragma unroll
-      for (int m = 0; m < D::kMQ; ++m) {
-        int tok, qh;
-        const bool in = row_of(wave * D::kMQ + m, &tok, &qh);
-        tok_of[m] = tok;
-        // (all loads at once: what there is no row or column for reads its first and becomes 0)
-        const char* qp = p.q + (q0 + (in ? tok : 0)) * p.q_token + (in ? qh : 0) * p.q_head;
+      for (int s = 0; s < D::kKS + 2; ++s) {
+        const bool rope = s >= D::kKS;
+        const int d0 = 32 * (rope ? s - D::kKS : s) + 8 * gq;
+        const bool there = d0 < (rope ? lp.rope : latent);
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(
+            qp + (there ? 2 * (d0 + (rope ? latent : 0)) : 0));
+        u32x4_t x;
 #pragma unroll
-        for (int s = 0; s < D::kKS + 2; ++s) {
-          const bool rope = s >= D::kKS;
-          const int d0 = 32 * (rope ? s - D::kKS : s) + 8 * gq;
-          const bool there = d0 < (rope ? lp.rope : latent);
-          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(
-              qp + (there ? 2 * (d0 + (rope ? latent : 0)) : 0));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qf[m][s][i] = in && there ? w[i] ^ flip : 0;
-        }
+        for (int i = 0; i < 4; ++i) x[i] = in && there ? w[i] ^ flip : 0;
+        if (s < kQR) qf[s < kQR ? s : 0] = x;
+        else queries[mine][s < kQR ? 0 : s - kQR][lane] = x;
       }
     }
     // which of the keys j0 .. j0 + 3 past the context token tok sees, as bits (j0 < 0: in it)
@@ -279,17 +290,138 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
     };
 
     f32x4 o[MB][D::kCols];
-    float mx[D::kMQ];
-    f32x4 sum[D::kMQ];  // every element of a lane: the sum of its row
+    float mx = -INFINITY;
+    f32x4 sum = {0, 0, 0, 0};  // every element of a lane: the sum of its row
 #pragma unroll
     for (int m = 0; m < MB; ++m)
 #pragma unroll
       for (int j = 0; j < D::kCols; ++j) o[m][j] = f32x4{0, 0, 0, 0};
+    auto open = [&](int tile) { return (tile + 1) * D::kKeys <= open_end; };  // to every row
+
+    // The weights of a tile, into buffer buf.
+    auto take_scores = [&](int tile, const char* base, int buf) {
+      const int key0 = tile * D::kKeys;
+      int kx = ka, rx = kr;
+      hide(kx);
+      hide(rx);
+      if (scores) {
+        // S^T of two 16-key tiles; fragments of kAhead steps are under way while those
+        // before are multiplied
+        f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        u32x4_t kf[kAhead + 1][2], ql[kAhead + 1];
+        auto fetch = [&](int s) {
+          const bool rope = s >= D::kKS;
 #pragma unroll
-    for (int m = 0; m < D::kMQ; ++m) {
-      mx[m] = -INFINITY;
-      sum[m] = f32x4{0, 0, 0, 0};
-    }
+          for (int t = 0; t < 2; ++t)
+            kf[s % (kAhead + 1)][t] = *reinterpret_cast<const u32x4_t*>(
+                rope ? base + (rx ^ ((s - D::kKS) << 6)) + 16 * t * D::kRopeRow
+                     : base + (kx ^ (s % 4 << 6)) + 256 * (s / 4) + 16 * t * D::kRow);
+          if (s >= kQR) ql[s % (kAhead + 1)] = queries[mine][s - kQR][lane];
+        };
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) fetch(s);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          if (s + kAhead < kSteps) fetch(s + kAhead);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            st[t] = attn_mfma<kFp16>(kf[s % (kAhead + 1)][t],
+                                     s < kQR ? qf[s < kQR ? s : 0] : ql[s % (kAhead + 1)], st[t]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!open(tile)) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t seen = seen4(my_tok, key0 + 16 * t + 4 * g - kv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(seen >> i & 1)) st[t][i] = -INFINITY;
+          }
+        }
+        float top = max3(st[0][0], st[0][1], st[0][2]);
+        top = max3(top, st[0][3], st[1][0]);
+        top = max3(top, st[1][1], st[1][2]);
+        top = max3(top, st[1][3], mx);
+        // The reference of the exponentials moves up once a score is 2^kPSlack past it.
+        const bool move = __ballot((top - mx) * scale > kPSlack) != 0;
+        if (move) {
+          top = row_max(top);
+          const float f = mx == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx - top) * scale);
+          sum[0] *= f;
+          if (g == 0) alpha[buf][mine * 16 + l16] = f;
+          mx = top;
+        }
+        if (lane == 0) moved[buf][group][w4] = move;
+        const float ref = (mx == -INFINITY ? 0.0f : mx * scale) - kPShift<kFp16>;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st[t][i] = __builtin_amdgcn_exp2f(fmaf(st[t][i], scale, -ref));
+        const u32x4_t pf = {pack16<kFp16>(st[0][0], st[0][1]), pack16<kFp16>(st[0][2], st[0][3]),
+                            pack16<kFp16>(st[1][0], st[1][1]), pack16<kFp16>(st[1][2], st[1][3])};
+        // the row's sum, of the weights as they are rounded: a product with ones
+        sum = attn_mfma<kFp16>(kOnes<kFp16>, pf, sum);
+        weights[buf][mine][lane] = pf;
+      }
+    };
+    // A latent hidden from a row has weight 0 there, but 0 times an infinity or NaN is NaN: in
+    // a tile that not every row sees in full they become 0 once it has its scores.  (A row that
+    // sees such a latent has it in its score.)
+    auto make_finite = [&](char* base) {
+      for (int e = tid; e < D::kKeys * D::kRow / 16; e += D::kThreads) {
+        u32x4_t* at = reinterpret_cast<u32x4_t*>(base) + e;
+        u32x4_t x = *at;
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = finite_pair<kFp16>(x[i], &finite);
+        if (!finite) *at = x;
+      }
+      lds_barrier();
+    };
+    // O^T += V^T P^T
+    auto take_values = [&](const char* base, int buf) {
+      int vx = va;
+      hide(vx);
+      u32x4_t vf[kAheadV + 1];
+      auto value = [&](int j) {
+        const char* at = base + (vx ^ (j << 5));
+        const i32x2_t x = __builtin_bit_cast(
+            i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)at));
+        const i32x2_t y = __builtin_bit_cast(
+            i32x2_t,
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)(at + 16 * D::kRow)));
+        vf[j % (kAheadV + 1)] =
+            u32x4_t{static_cast<unsigned>(x[0]), static_cast<unsigned>(x[1]),
+                    static_cast<unsigned>(y[0]), static_cast<unsigned>(y[1])};
+      };
+      u32x4_t pf[MB];
+      const int4 any = *reinterpret_cast<const int4*>(moved[buf][group]);
+      const int rows_moved[4] = {any.x, any.y, any.z, any.w};
+#pragma unroll
+      for (int m = 0; m < MB; ++m) pf[m] = weights[buf][group * MB + m][lane];
+#pragma unroll
+      for (int j = 0; j < kAheadV; ++j) value(j);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        if (uniform(rows_moved[m])) {
+          const float f = alpha[buf][(group * MB + m) * 16 + l16];
+#pragma unroll
+          for (int j = 0; j < D::kCols; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[m][j][i] *= f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D::kCols; ++j) {
+        if (j + kAheadV < D::kCols) value(j + kAheadV);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+          o[m][j] = attn_mfma<kFp16>(vf[j % (kAheadV + 1)], pf[m], o[m][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
     // windows of pages: one, unless the chunk has more pages than the window
     for (int w0 = tile0; w0 < tile1;) {
       slot0 = (w0 * D::kKeys) >> p.c.page_shift;
@@ -304,148 +436,58 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
         pages[e] = reinterpret_cast<uint64_t>(p.c.k) + at * p.c.ks[1];
       }
       __syncthreads();
-      // the first NST - 1 turns only fill the ring
-      int stage = 0, fill = 0;
+      if constexpr (!D::kTwo) {
+        // the first NST - 1 turns only fill the ring
+        int stage = 0, fill = 0;
 #pragma unroll 1
-      for (int tile = w0 - (NST - 1); tile < w1; ++tile) {
-        const int ahead = tile + NST - 1;
-        if (tile >= w0) {
-          wait_tiles(min(w1 - 1 - tile, NST - 2));
-          lds_barrier();  // the tile is there; the last one has been read
-        }
-        if (ahead < w1) load_tile(ahead, fill);
-        fill = fill + 1 == NST ? 0 : fill + 1;
-        if (tile < w0) continue;
-        const char* base = lds + (kE4M3 ? NST : stage) * D::kStage;
-        if constexpr (kE4M3) {
-          widen_tile(stage);
+        for (int tile = w0 - (NST - 1); tile < w1; ++tile) {
+          const int ahead = tile + NST - 1;
+          if (tile >= w0) {
+            wait_tiles(min(w1 - 1 - tile, NST - 2));
+            lds_barrier();  // the tile is there; the last one has been read
+          }
+          if (ahead < w1) load_tile(ahead, fill);
+          fill = fill + 1 == NST ? 0 : fill + 1;
+          if (tile < w0) continue;
+          char* base = lds + (kE4M3 ? NST : stage) * D::kStage;
+          if constexpr (kE4M3) {
+            widen_tile(stage, base);
+            lds_barrier();
+          }
+          stage = stage + 1 == NST ? 0 : stage + 1;
+          take_scores(tile, base, 0);
           lds_barrier();
+          if (!open(tile)) make_finite(base);
+          take_values(base, 0);
         }
-        stage = stage + 1 == NST ? 0 : stage + 1;
-        const int key0 = tile * D::kKeys;
-        int kx = ka, rx = kr, vx = va;
-        hide(kx);
-        hide(rx);
-        hide(vx);
-        const bool open = key0 + D::kKeys <= open_end;  // every row sees the whole tile
-        if (scores) {
-          // S^T of two 16-key tiles
-          f32x4 st[D::kMQ][2];
-#pragma unroll
-          for (int m = 0; m < D::kMQ; ++m)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) st[m][t] = f32x4{0, 0, 0, 0};
-          // fragments of kAhead steps are under way while those before are multiplied
-          constexpr int kSteps = D::kKS + 2;
-          u32x4_t kf[kAhead + 1][2];
-          auto fetch = [&](int s) {
-            const bool rope = s >= D::kKS;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              kf[s % (kAhead + 1)][t] = *reinterpret_cast<const u32x4_t*>(
-                  rope ? base + (rx ^ ((s - D::kKS) << 6)) + 16 * t * D::kRopeRow
-                       : base + (kx ^ (s % 4 << 6)) + 256 * (s / 4) + 16 * t * D::kRow);
-          };
-#pragma unroll
-          for (int s = 0; s < kAhead; ++s) fetch(s);
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            if (s + kAhead < kSteps) fetch(s + kAhead);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int m = 0; m < D::kMQ; ++m)
-                st[m][t] = attn_mfma<kFp16>(kf[s % (kAhead + 1)][t], qf[m][s], st[m][t]);
-            __builtin_amdgcn_sched_barrier(0);
+      } else {
+        // A turn takes a tile's values and the next one's scores: one barrier for both, and
+        // a SIMD's two waves need not be at the same of the two.
+        load_tile(w0, 0);
+        int at = 0;  // the stage of the tile whose scores are next
+#pragma unroll 1
+        for (int tile = w0 - 1; tile < w1; ++tile) {
+          wait_vm<0>();
+          lds_barrier();  // the next tile is there, as are this one's weights
+          const int after = at + 1 == NST ? 0 : at + 1, buf = (tile - w0) & 1;
+          if (tile + 2 < w1) load_tile(tile + 2, after);
+          char* next = lds + at * D::kStage;
+          char* base = lds + (at == 0 ? NST - 1 : at - 1) * D::kStage;
+          if constexpr (kE4M3) {
+            next = lds + NST * D::kStage + (buf ^ 1) * D::kTile;
+            base = lds + NST * D::kStage + buf * D::kTile;
+            if (tile + 1 < w1) widen_tile(at, next);
+            lds_barrier();
           }
-          if (!open) {
-#pragma unroll
-            for (int m = 0; m < D::kMQ; ++m)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const uint32_t seen = seen4(tok_of[m], key0 + 16 * t + 4 * g - kv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (!(seen >> i & 1)) st[m][t][i] = -INFINITY;
-              }
-          }
-#pragma unroll
-          for (int m = 0; m < D::kMQ; ++m) {
-            const int mi = wave * D::kMQ + m;
-            float top = max3(st[m][0][0], st[m][0][1], st[m][0][2]);
-            top = max3(top, st[m][0][3], st[m][1][0]);
-            top = max3(top, st[m][1][1], st[m][1][2]);
-            top = max3(top, st[m][1][3], mx[m]);
-            // The reference of the exponentials moves up once a score is 2^kPSlack past it.
-            const bool move = __ballot((top - mx[m]) * scale > kPSlack) != 0;
-            if (move) {
-              top = row_max(top);
-              const float f =
-                  mx[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mx[m] - top) * scale);
-              sum[m][0] *= f;
-              if (g == 0) alpha[mi * 16 + l16] = f;
-              mx[m] = top;
-            }
-            if (lane == 0) moved[mi] = move;
-            const float ref = (mx[m] == -INFINITY ? 0.0f : mx[m] * scale) - kPShift<kFp16>;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                st[m][t][i] = __builtin_amdgcn_exp2f(fmaf(st[m][t][i], scale, -ref));
-            const u32x4_t pf = {pack16<kFp16>(st[m][0][0], st[m][0][1]),
-                                pack16<kFp16>(st[m][0][2], st[m][0][3]),
-                                pack16<kFp16>(st[m][1][0], st[m][1][1]),
-                                pack16<kFp16>(st[m][1][2], st[m][1][3])};
-            // the row's sum, of the weights as they are rounded: a product with ones
-            sum[m] = attn_mfma<kFp16>(kOnes<kFp16>, pf, sum[m]);
-            weights[mi][lane] = pf;
-          }
-        }
-        lds_barrier();
-        // O^T += V^T P^T
-        u32x4_t pf[MB];
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          pf[m] = weights[m][lane];
-          if (uniform(moved[m])) {
-            const float f = alpha[m * 16 + l16];
-#pragma unroll
-            for (int j = 0; j < D::kCols; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[m][j][i] *= f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < D::kCols; ++j) {
-          const char* at = base + (vx ^ (j << 5));
-          const i32x2_t x = __builtin_bit_cast(
-              i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SGG_LDS s16x4_t*)at));
-          const i32x2_t y = __builtin_bit_cast(
-              i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                           (SGG_LDS s16x4_t*)(at + 16 * D::kRow)));
-          u32x4_t vf = {static_cast<unsigned>(x[0]), static_cast<unsigned>(x[1]),
-                        static_cast<unsigned>(y[0]), static_cast<unsigned>(y[1])};
-          // A latent hidden from a row has weight 0 there, but 0 times an infinity or NaN
-          // is NaN: in a tile that not every row sees in full they go through as 0.  (A row
-          // that sees such a latent has it in its score.)
-          if (!open) {
-            bool finite = true;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vf[i] = finite_pair<kFp16>(vf[i], &finite);
-          }
-#pragma unroll
-          for (int m = 0; m < MB; ++m) o[m][j] = attn_mfma<kFp16>(vf, pf[m], o[m][j]);
+          at = after;
+          if (tile >= w0 && !open(tile)) make_finite(base);
+          if (tile + 1 < w1) take_scores(tile + 1, next, buf ^ 1);
+          if (tile >= w0) take_values(base, buf);
         }
       }
       w0 = w1;
     }
-    if (scores) {
-#pragma unroll
-      for (int m = 0; m < D::kMQ; ++m)
-        if (g == 0)
-          stats[(wave * D::kMQ + m) * 16 + l16] = make_float2(mx[m] * scale, sum[m][0]);
-    }
+    if (scores && g == 0) stats[mine * 16 + l16] = make_float2(mx * scale, sum[0]);
     lds_barrier();
     int ge = g, le = lane;
     hide(ge);
@@ -455,13 +497,13 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         int tok, qh;
-        if (!row_of(m, &tok, &qh)) continue;
-        const float all = stats[m * 16 + l16].y;
+        if (!row_of(group * MB + m, &tok, &qh)) continue;
+        const float all = stats[(group * MB + m) * 16 + l16].y;
         const float inv = all > 0.0f ? vs / all : all != all ? all : 0.0f;
         char* op = p.out + (q0 + tok) * p.o_token + qh * p.o_head;
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j) {
-          const int d0 = 16 * (wave * D::kCols + j) + 4 * ge;
+          const int d0 = 16 * (w4 * D::kCols + j) + 4 * ge;
           if (d0 >= latent) continue;
           uint2 y;
           y.x = pack16<kFp16>(o[m][j][0] * inv, o[m][j][1] * inv);
@@ -478,8 +520,8 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
       for (int m = 0; m < MB; ++m)
 #pragma unroll
         for (int j = 0; j < D::kCols; ++j)
-          *reinterpret_cast<f32x4*>(slot + ((wave * MB + m) * D::kCols + j) * 1024 + le * 16) =
-              o[m][j];
+          *reinterpret_cast<f32x4*>(
+              slot + (((group * MB + m) * 4 + w4) * D::kCols + j) * 1024 + le * 16) = o[m][j];
       if (tid < D::kRows)
         *reinterpret_cast<float2*>(slot + D::kRows * DL * 4 + tid * 8) = stats[tid];
     }
@@ -487,108 +529,149 @@ __global__ __launch_bounds__(256, kPerSimd) void latent_kernel(LatentParams lp) 
   }
 }
 
-// The pieces of a unit that several ranges share, put together: workgroup (k, m, w)
-// takes the unit that begins in range k and goes on past it, row fragment m, and the
-// columns of wave w.  Its waves take pieces in turn.
-template <bool kFp16, bool kE4M3, int DL, int MB>
+// The pieces of a unit that several ranges share, put together: workgroup (k, y) takes
+// the unit that begins in range k and goes on past it, row fragment y / 4 and the columns
+// of wave y % 4; with kFine a quarter of those.  Its waves take columns of a few pieces,
+// or pieces in turn.
+template <bool kFp16, bool kE4M3, int DL, int MB, int NG, bool kFine>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentParams lp) {
-  using D = LatentDims<kE4M3, DL, MB, 2>;
+  using D = LatentDims<kE4M3, DL, MB, NG, 2>;
+  constexpr int kJoiners = 4;                             // waves
+  constexpr int kCols = kFine ? D::kCols / 4 : D::kCols;  // 16-column tiles of a workgroup
+  constexpr int kEach = kFine ? kCols : kCols / kJoiners; // of a wave that takes columns
   const AttnParams& p = lp.a;
-  __shared__ AttnFind<4> find;
-  __shared__ f32x4 part[D::kWaves][D::kCols][kWave];
-  __shared__ float sums[D::kWaves][16];
+  __shared__ f32x4 part[kJoiners][kCols][kWave];
+  __shared__ float sums[kJoiners][16];
+  const int4 split = lp.split[blockIdx.x];
+  const int first = split.x, tokens = split.y, mb = split.z, chunks = split.w;
+  if (chunks < 2) return;
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   const int l16 = lane % 16, g = lane / 16;
-  const int m = blockIdx.y, w = blockIdx.z;
-  LatentPlan<4, D::kRows, D::kKeys> plan(p, &find);
-  const int64_t border = (static_cast<int64_t>(blockIdx.x) + 1) * plan.per_range;
-  if (plan.work.by_unit || border >= plan.total) return;
-  const AttnUnit u = attn_locate(plan.work, &find, plan.share, static_cast<int>(border));
-  const int range0 = uniform(static_cast<uint32_t>(u.start) / plan.per_range);
-  if (u.start >= border || range0 != static_cast<int>(blockIdx.x)) return;
-  const int tiles = (u.keys + D::kKeys - 1) / D::kKeys;
-  const int chunks =
-      uniform(static_cast<uint32_t>(u.start + tiles - 1) / plan.per_range) - range0 + 1;
+  const int item = kFine ? blockIdx.y / 4 : blockIdx.y, j0 = kFine ? blockIdx.y % 4 * kCols : 0;
+  const int m = item / 4, w = item % 4;
   auto slot_of = [&](int c) {
-    return p.part + (2 * static_cast<int64_t>(range0 + c) + (c == 0 ? 1 : 0)) *
+    return p.part + (2 * (static_cast<int64_t>(blockIdx.x) + c) + (c == 0 ? 1 : 0)) *
                         static_cast<int64_t>(D::kSlotBytes);
   };
   auto stats_of = [&](int c) {
     return *reinterpret_cast<const float2*>(slot_of(c) + D::kRows * DL * 4 + (m * 16 + l16) * 8);
   };
+  auto sums_of = [&](int c, int j) {
+    return *reinterpret_cast<const f32x4*>(
+        slot_of(c) + ((m * 4 + w) * D::kCols + j0 + j) * 1024 + lane * 16);
+  };
+  auto share = [&](float2 s, float top) {
+    return s.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s.x - top);
+  };
+  const uint32_t row = mb * D::kRows + m * 16 + l16;
+  const int tok = static_cast<int>(row / static_cast<uint32_t>(p.group));
+  const int qh = static_cast<int>(row) - tok * p.group;
+  const float vs = kE4M3 && p.k_scale ? *p.k_scale : 1.0f;
+  auto put = [&](int j, f32x4 y, float all) {
+    const int d0 = 16 * (w * D::kCols + j0 + j) + 4 * g;
+    if (tok >= tokens || d0 >= p.head_dim) return;
+    const float inv = all > 0.0f ? vs / all : all != all ? all : 0.0f;
+    uint2 z;
+    z.x = pack16<kFp16>(y[0] * inv, y[1] * inv);
+    z.y = pack16<kFp16>(y[2] * inv, y[3] * inv);
+    *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(first) + tok) * p.o_token +
+                              qh * p.o_head + 2 * d0) = z;
+  };
+  constexpr int kFew = 4;
+  if (!kFine && chunks <= kFew) {
+    float2 s[kFew];
+    f32x4 y[kFew][kEach];
+#pragma unroll
+    for (int c = 0; c < kFew; ++c) {
+      const int at = min(c, chunks - 1);
+      s[c] = stats_of(at);
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) y[c][j] = sums_of(at, wave * kEach + j);
+    }
+    float top = s[0].x, all = 0.0f;
+#pragma unroll
+    for (int c = 1; c < kFew; ++c) top = fmaxf(top, s[c].x);
+    f32x4 o[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) o[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < kFew; ++c) {
+      const float f = share(s[c], top);
+      if (c >= chunks) continue;
+      all += s[c].y * f;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] += y[c][j][i] * f;
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) put(wave * kEach + j, o[j], all);
+    return;
+  }
   float top = -INFINITY;
   for (int c = g; c < chunks; c += 4) top = fmaxf(top, stats_of(c).x);
   top = row_max(top);
-  f32x4 o[D::kCols];
+  f32x4 o[kCols];
   float all = 0.0f;
 #pragma unroll
-  for (int j = 0; j < D::kCols; ++j) o[j] = f32x4{0, 0, 0, 0};
-#pragma unroll 2
-  for (int c = wave; c < chunks; c += D::kWaves) {
+  for (int j = 0; j < kCols; ++j) o[j] = f32x4{0, 0, 0, 0};
+#pragma unroll kFine ? 8 : 2
+  for (int c = wave; c < chunks; c += kJoiners) {
     const float2 s = stats_of(c);
-    const float f = s.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s.x - top);
+    const float f = share(s, top);
     all += s.y * f;
-    const char* at = slot_of(c) + (w * MB + m) * D::kCols * 1024 + lane * 16;
 #pragma unroll
-    for (int j = 0; j < D::kCols; ++j) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(at + j * 1024);
+    for (int j = 0; j < kCols; ++j) {
+      const f32x4 y = sums_of(c, j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[j][i] += y[i] * f;
     }
   }
 #pragma unroll
-  for (int j = 0; j < D::kCols; ++j) part[wave][j][lane] = o[j];
+  for (int j = 0; j < kCols; ++j) part[wave][j][lane] = o[j];
   if (g == 0) sums[wave][l16] = all;
   __syncthreads();
-  const uint32_t row = u.mb * D::kRows + m * 16 + l16;
-  const int tok = static_cast<int>(row / static_cast<uint32_t>(p.group));
-  const int qh = static_cast<int>(row) - tok * p.group;
-  if (tok >= u.q.tokens) return;
   all = 0.0f;
 #pragma unroll
-  for (int k = 0; k < D::kWaves; ++k) all += sums[k][l16];
-  const float vs = kE4M3 && p.k_scale ? *p.k_scale : 1.0f;
-  const float inv = all > 0.0f ? vs / all : all != all ? all : 0.0f;
-  char* op = p.out + (static_cast<int64_t>(u.q.first) + tok) * p.o_token + qh * p.o_head;
-  for (int j = wave; j < D::kCols; j += D::kWaves) {
+  for (int k = 0; k < kJoiners; ++k) all += sums[k][l16];
+  for (int j = wave; j < kCols; j += kJoiners) {
     f32x4 y = part[0][j][lane];
 #pragma unroll
-    for (int k = 1; k < D::kWaves; ++k)
+    for (int k = 1; k < kJoiners; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] += part[k][j][lane][i];
-    const int d0 = 16 * (w * D::kCols + j) + 4 * g;
-    if (d0 >= p.head_dim) continue;
-    uint2 z;
-    z.x = pack16<kFp16>(y[0] * inv, y[1] * inv);
-    z.y = pack16<kFp16>(y[2] * inv, y[3] * inv);
-    *reinterpret_cast<uint2*>(op + 2 * d0) = z;
+    put(j, y, all);
   }
 }
 
-template <bool kFp16, bool kE4M3, int DL, int MB, int NST, int kAhead>
+template <bool kFp16, bool kE4M3, int DL, int MB, int NG, int NST, int kAhead, int kQL>
 hipError_t launch_latent_as(const LatentParams& p, const LatentShape& s, hipStream_t stream) {
-  using D = LatentDims<kE4M3, DL, MB, NST>;
+  using D = LatentDims<kE4M3, DL, MB, NG, NST>;
   if (s.block_rows != D::kRows || s.slot_bytes != D::kSlotBytes) return hipErrorInvalidValue;
-  latent_kernel<kFp16, kE4M3, DL, MB, NST, 2, kAhead>
-      <<<dim3(static_cast<uint32_t>(s.grid)), dim3(256), 0, stream>>>(p);
+  latent_kernel<kFp16, kE4M3, DL, MB, NG, NST, kAhead, kQL>
+      <<<dim3(static_cast<uint32_t>(s.grid)), dim3(D::kThreads), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.ranges <= 1) return e;
-  latent_join_kernel<kFp16, kE4M3, DL, MB>
-      <<<dim3(s.ranges - 1, MB, D::kWaves), dim3(256), 0, stream>>>(p);
+  const dim3 items(s.ranges - 1, D::kFrags * 4 * (s.fine ? 4 : 1)), block(256);
+  if (s.fine) latent_join_kernel<kFp16, kE4M3, DL, MB, NG, true><<<items, block, 0, stream>>>(p);
+  else latent_join_kernel<kFp16, kE4M3, DL, MB, NG, false><<<items, block, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <bool kFp16, bool kE4M3>
 hipError_t launch_latent(const LatentParams& p, const LatentShape& s, hipStream_t stream) {
-#define SGG_LATENT(dl, m, n, ahead)    \
-  if (s.padded_dim == dl && s.mb == m) \
-    return launch_latent_as<kFp16, kE4M3, dl, m, n, ahead>(p, s, stream)
-  SGG_LATENT(256, 1, 4, 3);
-  SGG_LATENT(256, 2, 4, 3);
-  SGG_LATENT(256, 4, 4, 2);
-  SGG_LATENT(512, 1, 2, 3);
-  SGG_LATENT(512, 2, 2, 3);
-  SGG_LATENT(512, 4, 2, 1);
+#define SGG_LATENT(dl, m, groups, n, ahead, in_lds)              \
+  if (s.padded_dim == dl && s.block_rows == 16 * (m) * (groups)) \
+    return launch_latent_as<kFp16, kE4M3, dl, m, groups, n, ahead, in_lds>(p, s, stream)
+  constexpr int two = kE4M3 ? 2 : 3;  // stages of a ring beside two tiles in use
+  SGG_LATENT(256, 1, 1, 4, 3, 0);
+  SGG_LATENT(256, 2, 1, 4, 3, 0);
+  SGG_LATENT(256, 4, 1, 4, 3, 0);
+  SGG_LATENT(256, 4, 2, two, 3, 0);
+  SGG_LATENT(512, 1, 1, 2, 3, 0);
+  SGG_LATENT(512, 2, 1, 2, 3, 0);
+  SGG_LATENT(512, 4, 1, 2, 1, 0);
+  SGG_LATENT(512, 4, 2, two, 1, 0);
 #undef SGG_LATENT
   return hipErrorInvalidValue;
 }
