@@ -18,7 +18,8 @@ struct LatentParams {
 struct LatentShape {
   int32_t block_rows, padded_dim;
   int32_t min_tiles, ranges;  // ranges 0: each workgroup takes one unit
-  bool fine;                  // units in many pieces: small items for the join
+  bool fine;                  // few units in many pieces: small items for the join
+  int32_t units;              // as many as there are, or more, unless a bound is exceeded
   int64_t grid, slot_bytes;
 };
 constexpr int kLatentKeys = 32;

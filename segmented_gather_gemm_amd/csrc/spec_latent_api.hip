@@ -276,6 +276,7 @@ LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cach
     // (the kernel may take the batch by units)
     s.grid = units > s.ranges ? units : s.ranges;
     s.fine = s.ranges >= 8 * units;
+    s.units = static_cast<int32_t>(units);  // (below ranges where it counts)
   }
   return s;
 }

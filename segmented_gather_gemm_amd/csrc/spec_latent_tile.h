@@ -531,7 +531,7 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
 
 // The pieces of a unit that several ranges share, put together: workgroup (k, y) takes
 // the unit that begins in range k and goes on past it, row fragment y / 4 and the columns
-// of wave y % 4; with kFine a quarter of those.  Its waves take columns of a few pieces,
+// of wave y % 4; with kFine the k-th such unit, and a quarter of those columns.  Its waves take columns of a few pieces,
 // or pieces in turn.
 template <bool kFp16, bool kE4M3, int DL, int MB, int NG, bool kFine>
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentParams lp) {
@@ -541,106 +541,149 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentParams lp) {
   constexpr int kEach = kFine ? kCols : kCols / kJoiners; // of a wave that takes columns
   const AttnParams& p = lp.a;
   __shared__ f32x4 part[kJoiners][kCols][kWave];
-  __shared__ float sums[kJoiners][16];
-  const int4 split = lp.split[blockIdx.x];
-  const int first = split.x, tokens = split.y, mb = split.z, chunks = split.w;
-  if (chunks < 2) return;
+  __shared__ float2 sums[kJoiners][16];
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   const int l16 = lane % 16, g = lane / 16;
-  const int item = kFine ? blockIdx.y / 4 : blockIdx.y, j0 = kFine ? blockIdx.y % 4 * kCols : 0;
-  const int m = item / 4, w = item % 4;
-  auto slot_of = [&](int c) {
-    return p.part + (2 * (static_cast<int64_t>(blockIdx.x) + c) + (c == 0 ? 1 : 0)) *
-                        static_cast<int64_t>(D::kSlotBytes);
-  };
-  auto stats_of = [&](int c) {
-    return *reinterpret_cast<const float2*>(slot_of(c) + D::kRows * DL * 4 + (m * 16 + l16) * 8);
-  };
-  auto sums_of = [&](int c, int j) {
-    return *reinterpret_cast<const f32x4*>(
-        slot_of(c) + ((m * 4 + w) * D::kCols + j0 + j) * 1024 + lane * 16);
-  };
-  auto share = [&](float2 s, float top) {
-    return s.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s.x - top);
-  };
-  const uint32_t row = mb * D::kRows + m * 16 + l16;
-  const int tok = static_cast<int>(row / static_cast<uint32_t>(p.group));
-  const int qh = static_cast<int>(row) - tok * p.group;
-  const float vs = kE4M3 && p.k_scale ? *p.k_scale : 1.0f;
-  auto put = [&](int j, f32x4 y, float all) {
-    const int d0 = 16 * (w * D::kCols + j0 + j) + 4 * g;
-    if (tok >= tokens || d0 >= p.head_dim) return;
-    const float inv = all > 0.0f ? vs / all : all != all ? all : 0.0f;
-    uint2 z;
-    z.x = pack16<kFp16>(y[0] * inv, y[1] * inv);
-    z.y = pack16<kFp16>(y[2] * inv, y[3] * inv);
-    *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(first) + tok) * p.o_token +
-                              qh * p.o_head + 2 * d0) = z;
-  };
-  constexpr int kFew = 4;
-  if (!kFine && chunks <= kFew) {
-    float2 s[kFew];
-    f32x4 y[kFew][kEach];
+  auto join = [&](int k) {
+    const int4 split = lp.split[k];
+    const int first = split.x, tokens = split.y, mb = split.z, chunks = split.w;
+    if (chunks < 2) return;
+    const int item = kFine ? blockIdx.y / 4 : blockIdx.y, j0 = kFine ? blockIdx.y % 4 * kCols : 0;
+    const int m = item / 4, w = item % 4;
+    auto slot_of = [&](int c) {
+      return p.part + (2 * (static_cast<int64_t>(k) + c) + (c == 0 ? 1 : 0)) *
+                          static_cast<int64_t>(D::kSlotBytes);
+    };
+    auto stats_of = [&](int c) {
+      return *reinterpret_cast<const float2*>(slot_of(c) + D::kRows * DL * 4 + (m * 16 + l16) * 8);
+    };
+    auto sums_of = [&](int c, int j) {
+      return *reinterpret_cast<const f32x4*>(
+          slot_of(c) + ((m * 4 + w) * D::kCols + j0 + j) * 1024 + lane * 16);
+    };
+    auto share = [&](float2 s, float top) {
+      return s.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s.x - top);
+    };
+    const uint32_t row = mb * D::kRows + m * 16 + l16;
+    const int tok = static_cast<int>(row / static_cast<uint32_t>(p.group));
+    const int qh = static_cast<int>(row) - tok * p.group;
+    const float vs = kE4M3 && p.k_scale ? *p.k_scale : 1.0f;
+    auto put = [&](int j, f32x4 y, float all) {
+      const int d0 = 16 * (w * D::kCols + j0 + j) + 4 * g;
+      if (tok >= tokens || d0 >= p.head_dim) return;
+      const float inv = all > 0.0f ? vs / all : all != all ? all : 0.0f;
+      uint2 z;
+      z.x = pack16<kFp16>(y[0] * inv, y[1] * inv);
+      z.y = pack16<kFp16>(y[2] * inv, y[3] * inv);
+      *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(first) + tok) * p.o_token +
+                                qh * p.o_head + 2 * d0) = z;
+    };
+    constexpr int kFew = 4;
+    if (!kFine && chunks <= kFew) {
+      float2 s[kFew];
+      f32x4 y[kFew][kEach];
 #pragma unroll
-    for (int c = 0; c < kFew; ++c) {
-      const int at = min(c, chunks - 1);
-      s[c] = stats_of(at);
+      for (int c = 0; c < kFew; ++c) {
+        const int at = min(c, chunks - 1);
+        s[c] = stats_of(at);
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) y[c][j] = sums_of(at, wave * kEach + j);
+        for (int j = 0; j < kEach; ++j) y[c][j] = sums_of(at, wave * kEach + j);
+      }
+      float top = s[0].x, all = 0.0f;
+#pragma unroll
+      for (int c = 1; c < kFew; ++c) top = fmaxf(top, s[c].x);
+      f32x4 o[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) o[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kFew; ++c) {
+        const float f = share(s[c], top);
+        if (c >= chunks) continue;
+        all += s[c].y * f;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] += y[c][j][i] * f;
+      }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) put(wave * kEach + j, o[j], all);
+      return;
     }
-    float top = s[0].x, all = 0.0f;
+    // each wave by the largest of its own pieces
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int c = wave + kJoiners * g; c < chunks; c += kJoiners * 4)
+      top = fmaxf(top, stats_of(c).x);
+    top = row_max(top);
+    f32x4 o[kCols];
+    float all = 0.0f;
 #pragma unroll
-    for (int c = 1; c < kFew; ++c) top = fmaxf(top, s[c].x);
-    f32x4 o[kEach];
+    for (int j = 0; j < kCols; ++j) o[j] = f32x4{0, 0, 0, 0};
+    constexpr int kBatch = kFine ? 8 : 2;  // pieces whose sums are under way
+    for (int c0 = wave; c0 < chunks; c0 += kJoiners * kBatch) {
+      float2 s[kBatch];
+      f32x4 y[kBatch][kCols];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) o[j] = f32x4{0, 0, 0, 0};
+      for (int b = 0; b < kBatch; ++b) {
+        const int c = min(c0 + kJoiners * b, chunks - 1);
+        s[b] = stats_of(c);
 #pragma unroll
-    for (int c = 0; c < kFew; ++c) {
-      const float f = share(s[c], top);
-      if (c >= chunks) continue;
-      all += s[c].y * f;
+        for (int j = 0; j < kCols; ++j) y[b][j] = sums_of(c, j);
+      }
 #pragma unroll
-      for (int j = 0; j < kEach; ++j)
+      for (int b = 0; b < kBatch; ++b) {
+        if (c0 + kJoiners * b >= chunks) continue;
+        const float f = share(s[b], top);
+        all += s[b].y * f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][i] += y[c][j][i] * f;
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] += y[b][j][i] * f;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) put(wave * kEach + j, o[j], all);
-    return;
-  }
-  float top = -INFINITY;
-  for (int c = g; c < chunks; c += 4) top = fmaxf(top, stats_of(c).x);
-  top = row_max(top);
-  f32x4 o[kCols];
-  float all = 0.0f;
+    for (int j = 0; j < kCols; ++j) part[wave][j][lane] = o[j];
+    if (g == 0) sums[wave][l16] = make_float2(top, all);
+    __syncthreads();
+    float f[kJoiners];
+    top = -INFINITY;
+    all = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) o[j] = f32x4{0, 0, 0, 0};
-#pragma unroll kFine ? 8 : 2
-  for (int c = wave; c < chunks; c += kJoiners) {
-    const float2 s = stats_of(c);
-    const float f = share(s, top);
-    all += s.y * f;
+    for (int q = 0; q < kJoiners; ++q) top = fmaxf(top, sums[q][l16].x);
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const f32x4 y = sums_of(c, j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] += y[i] * f;
+    for (int q = 0; q < kJoiners; ++q) {
+      f[q] = share(sums[q][l16], top);
+      all += sums[q][l16].y * f[q];
     }
-  }
+    for (int j = wave; j < kCols; j += kJoiners) {
+      f32x4 y = {0, 0, 0, 0};
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) part[wave][j][lane] = o[j];
-  if (g == 0) sums[wave][l16] = all;
-  __syncthreads();
-  all = 0.0f;
+      for (int q = 0; q < kJoiners; ++q)
 #pragma unroll
-  for (int k = 0; k < kJoiners; ++k) all += sums[k][l16];
-  for (int j = wave; j < kCols; j += kJoiners) {
-    f32x4 y = part[0][j][lane];
-#pragma unroll
-    for (int k = 1; k < kJoiners; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += part[k][j][lane][i];
-    put(j, y, all);
+        for (int i = 0; i < 4; ++i) y[i] += part[q][j][lane][i] * f[q];
+      put(j, y, all);
+    }
+  };
+  if constexpr (!kFine) {
+    join(blockIdx.x);
+  } else {
+    // the nth ranges that have such a unit (there may be more of them than workgroups)
+    for (int nth = blockIdx.x;; nth += gridDim.x) {
+      int seen = 0, k = -1;
+      for (int r0 = 0; r0 < p.ranges && k < 0; r0 += kWave) {
+        const bool is = r0 + lane < p.ranges && lp.split[min(r0 + lane, p.ranges - 1)].w > 1;
+        uint64_t left = __ballot(is);
+        const int n = __popcll(left);
+        if (seen + n > nth) {
+          for (int i = seen; i < nth; ++i) left &= left - 1;
+          k = r0 + __ffsll(static_cast<unsigned long long>(left)) - 1;
+        }
+        seen += n;
+      }
+      if (k < 0) return;
+      join(k);
+      __syncthreads();  // part and sums have been read
+    }
   }
 }
 
@@ -652,7 +695,7 @@ hipError_t launch_latent_as(const LatentParams& p, const LatentShape& s, hipStre
       <<<dim3(static_cast<uint32_t>(s.grid)), dim3(D::kThreads), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.ranges <= 1) return e;
-  const dim3 items(s.ranges - 1, D::kFrags * 4 * (s.fine ? 4 : 1)), block(256);
+  const dim3 items(s.fine ? s.units : s.ranges - 1, D::kFrags * 4 * (s.fine ? 4 : 1)), block(256);
   if (s.fine) latent_join_kernel<kFp16, kE4M3, DL, MB, NG, true><<<items, block, 0, stream>>>(p);
   else latent_join_kernel<kFp16, kE4M3, DL, MB, NG, false><<<items, block, 0, stream>>>(p);
   return hipGetLastError();
