@@ -262,7 +262,7 @@ LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cach
   s.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const int64_t resident = s.block_rows == 128 ? 256 : 512;  // workgroups on the GPU at once
   s.slot_bytes = static_cast<int64_t>(s.block_rows) * (s.padded_dim * 4 + 8);
-  s.min_tiles = 2;
+  s.min_tiles = s.block_rows <= 32 ? 1 : s.block_rows / 32;
   const int64_t blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
   const int64_t units = bs * blocks;
   if (blocks > 1 && units >= 2 * resident) {
