@@ -7,6 +7,13 @@
 // once, in LDS, for all its nodes; what a node's path adds is a few entries, kept
 // in a list by node.  Two launches: the maximum and the sum of every chunk, then
 // the probabilities, which take the chunks' together.
+//
+// 64 requests of 16 nodes, 128256 bf16 values each, 4000 tokens of text: 109 us for the
+// first launch, whose vector units are busy for 70 % of the time (some 15 instructions
+// a value), and 167 us for the second, which reads 263 MB and writes 525 MB at
+// 4.7 TB/s, what a large copy reaches.  What the text says of a thread's 8 values stays
+// in registers for all nodes (from LDS: 118 us), which four workgroups a CU just allow;
+// with three the second launch takes 198 us.
 #include <cfloat>
 
 #include "spec_pages.h"
@@ -19,42 +26,19 @@ constexpr int kProbsThreads = 256;
 constexpr int kProbsWaves = kProbsThreads / kWave;
 constexpr int kProbsNodes = 16;
 constexpr int kProbsEntries = 32;   // values of a node's path in the chunk; more are walked again
+constexpr int kProbsParts = kProbsThreads / 4;  // of a node's row: what four lanes hold
 constexpr int kProbsTree = 256;     // nodes whose parents and tokens are kept in LDS
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kProbsChunk == 8 * kProbsThreads, "a thread takes two groups of four values");
 
-// Reduction over the 64 lanes by register moves: rotations within 16 lanes, then the
-// halves exchanged.  Every lane gets the result.
+// A register of the lane kRotate further on, within 16 lanes.
 template <int kRotate>
 __device__ __forceinline__ int rotated(int x) {
   return __builtin_amdgcn_update_dpp(x, x, 0x120 + kRotate, 0xf, 0xf, false);
 }
-template <class Op>
-__device__ __forceinline__ int over_lanes(int x, Op op) {
-  x = op(x, rotated<8>(x));
-  x = op(x, rotated<4>(x));
-  x = op(x, rotated<2>(x));
-  x = op(x, rotated<1>(x));
-  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-  x = op(static_cast<int>(a[0]), static_cast<int>(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  return op(static_cast<int>(b[0]), static_cast<int>(b[1]));
-}
-__device__ __forceinline__ float lanes_sum(float x) {
-  return __int_as_float(over_lanes(__float_as_int(x), [](int a, int b) {
-    return __float_as_int(__int_as_float(a) + __int_as_float(b));
-  }));
-}
-__device__ __forceinline__ int lanes_min(int x) {
-  return over_lanes(x, [](int a, int b) { return min(a, b); });
-}
-// The largest of numbers that are no NaN, in a scalar register: compared as whole
-// numbers of the same order, which takes one instruction a step.
-__device__ __forceinline__ float lanes_max(float x) {
-  const int bits = __float_as_int(x);
-  const int top = __builtin_amdgcn_readfirstlane(
-      over_lanes(bits ^ (bits >> 31 & INT32_MAX), [](int a, int b) { return max(a, b); }));
-  return __int_as_float(top ^ (top >> 31 & INT32_MAX));
+template <int kRotate>
+__device__ __forceinline__ float turned(float x) {
+  return __int_as_float(rotated<kRotate>(__float_as_int(x)));
 }
 // What counts as nothing: NaN, -inf, and what the grammar does not allow.  Infinities are
 // the largest numbers from here on, so that differences are never NaN.
@@ -69,14 +53,11 @@ constexpr uint32_t kInPrompt = 1u << 31, kCount = kInPrompt - 1;
 struct ProbsShared {
   uint32_t word[kProbsChunk];
   float shift[kProbsChunk];          // what is added to a value's logit
-  float up[kProbsChunk];             // what it is multiplied with if above 0,
-  float down[kProbsChunk];           // and if not
-  uint8_t any[kProbsChunk / 4];      // whether one of four values has any of these
   int parent[kProbsTree], token[kProbsTree];
   int entries[kProbsNodes];          // of `entry`, or more than there is room for
   uint32_t entry[kProbsNodes][kProbsEntries];  // place in the chunk, occurrences << 16
-  float2 stats[kProbsNodes][kProbsWaves];
-  int first[kProbsNodes][kProbsWaves];
+  float2 stats[kProbsNodes][kProbsParts];
+  int first[kProbsNodes][kProbsParts];
 };
 
 // exp((x - top) / temperature), k = log2(e) / temperature.
@@ -126,7 +107,7 @@ struct Four {
 };
 
 template <int kType, bool kFinal>
-__global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
+__global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) {
   __shared__ ProbsShared s;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int chunk = blockIdx.x, r = blockIdx.y;
@@ -232,19 +213,16 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
   // A value's logit x becomes x * (x > 0 ? up : down) + shift: what a node's path does not
   // change is made once.
   const float rep_inv = 1.0f / rep;
-  for (int e = tid; e < kProbsChunk / 4; e += kProbsThreads) {
-    bool any = false;
+  float up[8], down[8], shift[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = s.word[4 * e + i], given = w & kCount;
-      float shift = s.shift[4 * e + i];
-      if (given) shift -= static_cast<float>(given) * freq + pres;
-      s.shift[4 * e + i] = shift;
-      s.up[4 * e + i] = w ? rep_inv : 1.0f;
-      s.down[4 * e + i] = w ? rep : 1.0f;
-      any |= w != 0 || shift != 0.0f;
-    }
-    s.any[e] = any;
+  for (int i = 0; i < 8; ++i) {
+    const int at = 4 * (tid + i / 4 * kProbsThreads) + i % 4;
+    const uint32_t w = s.word[at], given = w & kCount;
+    shift[i] = s.shift[at];
+    if (given) shift[i] -= static_cast<float>(given) * freq + pres;
+    s.shift[at] = shift[i];
+    up[i] = w ? rep_inv : 1.0f;
+    down[i] = w ? rep : 1.0f;
   }
   // (each memory by its own address space, which keeps the loads apart)
   typedef const __attribute__((address_space(3))) int* LdsInts;
@@ -332,17 +310,7 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = raw[0][i / 4][i % 4];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int at = 4 * (tid + g * kProbsThreads);
-        if (s.any[at / 4]) {
-          const f32x4 up = *reinterpret_cast<const f32x4*>(&s.up[at]);
-          const f32x4 down = *reinterpret_cast<const f32x4*>(&s.down[at]);
-          const f32x4 shift = *reinterpret_cast<const f32x4*>(&s.shift[at]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[4 * g + i] = fmaf(x[4 * g + i], x[4 * g + i] > 0.0f ? up[i] : down[i], shift[i]);
-        }
-      }
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], x[i] > 0.0f ? up[i] : down[i], shift[i]);
       const int entries = __builtin_amdgcn_readfirstlane(s.entries[j]);
       if (__builtin_expect(entries > 0, 0)) {
         // values that the node's path holds, from their logits once more
@@ -398,26 +366,30 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
           mask[d][g] = mask[d + 1][g];
         }
       if constexpr (!kFinal) {
+        // Four lanes' values together now, the rest of the way for all nodes at once.
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
-        top = lanes_max(top);
+        top = fmaxf(top, turned<8>(top));
+        top = fmaxf(top, turned<4>(top));
         float sum = 0.0f;
         int first = INT32_MAX;
-        if (top == kNothing) {
-        } else if (greedy) {
+        if (greedy) {
 #pragma unroll
           for (int i = 7; i >= 0; --i)
             if (x[i] == top) first = c0 + 4 * (tid + i / 4 * kProbsThreads) + i % 4;
-          first = lanes_min(first);
+          first = min(first, rotated<8>(first));
+          first = min(first, rotated<4>(first));
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum += weight(x[i], top, k);
-          sum = lanes_sum(sum);
+          sum += turned<8>(sum);
+          sum += turned<4>(sum);
         }
-        if (lane == 0) {
-          s.stats[j][wave] = make_float2(top, sum);
-          s.first[j][wave] = first;
+        if (lane % 16 < 4) {
+          const int part = 4 * (tid / 16) + lane % 4;
+          s.stats[j][part] = make_float2(top, top == kNothing ? 0.0f : sum);
+          s.first[j][part] = first;
         }
       } else {
         const float top =
@@ -454,22 +426,36 @@ __global__ __launch_bounds__(kProbsThreads) void probs_kernel(ProbsParams p) {
     }
     if constexpr (!kFinal) {
       __syncthreads();
-      if (tid < count) {
-        float top = kNothing, sum = 0.0f;
-        int first = INT32_MAX;
+      static_assert(kProbsNodes * 16 == kProbsThreads && kProbsParts == 64, "16 lanes a node");
+      const int j = tid / 16;
+      float top = kNothing, sum = 0.0f;
+      int first = INT32_MAX;
+      if (j < count) {
 #pragma unroll
-        for (int w = 0; w < kProbsWaves; ++w) {
-          const float m = s.stats[tid][w].x;
-          const int f = s.first[tid][w];
-          if (m > top || (m == top && f < first)) first = f;
-          top = fmaxf(top, m);
-        }
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, s.stats[j][4 * (lane % 16) + e].x);
+      }
+      top = fmaxf(top, turned<8>(top));
+      top = fmaxf(top, turned<4>(top));
+      top = fmaxf(top, turned<2>(top));
+      top = fmaxf(top, turned<1>(top));
+      if (j < count) {
 #pragma unroll
-        for (int w = 0; w < kProbsWaves; ++w) {
-          const float2 x = s.stats[tid][w];
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = s.stats[j][4 * (lane % 16) + e];
+          if (x.x == top) first = min(first, s.first[j][4 * (lane % 16) + e]);
           sum += x.y * weight(x.x, top, k);
         }
-        const int64_t at = static_cast<int64_t>(q0 + i0 + tid) * p.chunks + chunk;
+      }
+      sum += turned<8>(sum);
+      sum += turned<4>(sum);
+      sum += turned<2>(sum);
+      sum += turned<1>(sum);
+      first = min(first, rotated<8>(first));
+      first = min(first, rotated<4>(first));
+      first = min(first, rotated<2>(first));
+      first = min(first, rotated<1>(first));
+      if (j < count && lane % 16 == 0) {
+        const int64_t at = static_cast<int64_t>(q0 + i0 + j) * p.chunks + chunk;
         p.stats[at] = make_float2(top, sum);
         p.first[at] = first;
       }
@@ -490,7 +476,8 @@ hipError_t launch_probs(ProbsParams p, int dtype, void* workspace, hipStream_t s
   p.stats = static_cast<float2*>(workspace);
   p.first = reinterpret_cast<int32_t*>(p.stats + static_cast<int64_t>(p.num_tokens) * p.chunks);
   // Nodes of a workgroup share its counts of the text; a small batch has a workgroup for
-  // each node rather (one user's 5 nodes of 32000 values: us with 16 a workgroup).
+  // each node rather (one user's 5 nodes of 32000 values:
+  // 17 us, and 37 with 16 a workgroup).
   p.nodes = kProbsNodes;
   const int64_t all = static_cast<int64_t>(p.chunks) * p.num_tokens;
   while (p.nodes > 1 && all / p.nodes < 1024) p.nodes /= 2;
