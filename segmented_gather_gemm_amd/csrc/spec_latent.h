@@ -23,8 +23,8 @@ struct LatentShape {
   int64_t grid, slot_bytes;
 };
 constexpr int kLatentKeys = 32;
-LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cache_bytes,
-                         int32_t max_q_len, int64_t max_kv_len);
+LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t max_q_len,
+                         int64_t max_kv_len);
 // Bytes of workspace: LatentParams::split, then two slots a range.
 inline int64_t latent_splits(const LatentShape& s) {
   return (s.ranges * int64_t{sizeof(int4)} + 255) / 256 * 256;

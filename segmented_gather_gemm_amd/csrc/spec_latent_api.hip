@@ -252,10 +252,22 @@ extern "C" int spec_latent_gather(const SpecLatentCache* cache, const int32_t* p
 
 namespace sgg {
 
-// Row blocks of the smallest size that holds one request's rows, up to 128.  Workgroups
-// are one to a CU: the ring of keys takes its LDS.
-LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t cache_bytes,
-                         int32_t max_q_len, int64_t max_kv_len) {
+// Row blocks of the smallest size that holds one request's rows, up to 128: rows that
+// nobody has cost matrix work, and a block fewer saves a read of all latents.  (128
+// requests of 16 rows and some 4500 latents: 149 us, 198 in blocks of 64.  The 128 rows
+// of each of two requests with 100003: 111 us, 117 in two blocks of 64.  32 requests of
+// 768 rows: 236 us, 244.)  Two workgroups of up to 64 rows share a CU's LDS and
+// registers, one of 128 takes it whole.
+//
+// The tiles of all units, a request's row blocks, are one line that is cut into as many
+// ranges as workgroups are on the GPU at once; a small block's ranges may be single tiles
+// (one request's 500 latents: 14.1 us, 14.9 at two tiles and more), larger blocks' at
+// least so long that their partial sums are no more than the latents read.  Units so many
+// that they fill the GPU by themselves take a workgroup each and nothing is joined.
+// Where units are few and pieces many the join takes smaller items (two requests of 256
+// pieces: 111 us, 120; one of 16: 14.6, 16.0).
+LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t max_q_len,
+                         int64_t max_kv_len) {
   LatentShape s{};
   const int64_t rows = static_cast<int64_t>(max_q_len) * heads;
   s.padded_dim = latent <= 256 ? 256 : 512;
@@ -287,8 +299,8 @@ extern "C" int64_t spec_latent_attention_workspace_bytes(int32_t bs, int32_t num
                                                          int32_t latent_dim, int32_t cache_dtype,
                                                          int32_t max_q_len, int64_t max_kv_len) {
   if (check_latent_heads(bs, num_heads, latent_dim, max_q_len, max_kv_len) != SGG_OK) return -1;
-  const sgg::LatentShape s = sgg::latent_shape(
-      bs, num_heads, latent_dim, cache_dtype == SPEC_E4M3 ? 1 : 2, max_q_len, max_kv_len);
+  const sgg::LatentShape s =
+      sgg::latent_shape(bs, num_heads, latent_dim, max_q_len, max_kv_len);
   sgg::ok();
   return with_zero_region(sgg::latent_workspace(s));
 }
@@ -324,8 +336,8 @@ extern "C" int spec_latent_attention(const void* q, int64_t q_token, int64_t q_h
   SGG_CHECK(kv_lens && q_indptr, SGG_ERR_INVALID, "kv_lens or q_indptr is NULL");
   SGG_CHECK(num_tokens * num_heads < (1 << 30), SGG_ERR_UNSUPPORTED,
             "%" PRId64 " tokens of %d heads are 2^30 rows or more", num_tokens, num_heads);
-  const sgg::LatentShape s = sgg::latent_shape(bs, num_heads, cache->latent_dim, e4m3 ? 1 : 2,
-                                               max_q_len, max_kv_len);
+  const sgg::LatentShape s = sgg::latent_shape(bs, num_heads, cache->latent_dim, max_q_len,
+                                               max_kv_len);
   SGG_CHECK(s.grid <= INT32_MAX, SGG_ERR_UNSUPPORTED,
             "%d requests of %d tokens are above the grid", bs, max_q_len);
   SGG_TRY(check_workspace(workspace, workspace_bytes,
@@ -394,6 +406,9 @@ extern "C" int spec_latent_prefill(const void* q, int64_t q_token, int64_t q_hea
     SGG_TRY(check_rows16(k, k_token, k_head, "k"));
     SGG_TRY(check_rows16(v, v_token, v_head, "v"));
     SGG_TRY(check_rows16(k_pe, k_pe_token, 0, "k_pe"));
+    // (a tile's 32 keys lie within 32 bits)
+    SGG_CHECK(k_token < (1 << 26) && v_token < (1 << 26) && k_pe_token < (1 << 26),
+              SGG_ERR_UNSUPPORTED, "strides of a key of 2^26 elements or more");
   }
   SGG_CHECK(q_indptr && kv_indptr, SGG_ERR_INVALID, "q_indptr or kv_indptr is NULL");
   SGG_CHECK((static_cast<int64_t>(bs) * num_heads + sgg::kXcds) * (max_q_len / 64 + 1) <=

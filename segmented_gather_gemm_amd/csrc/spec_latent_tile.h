@@ -3,8 +3,8 @@
 //
 // All heads share a token's latent, so one token is as many query rows as it has
 // heads, and a latent is read once for a block of up to 128 rows.  The sums of a
-// row are 512 columns wide: a wave cannot hold many rows, so the four waves of a
-// workgroup divide a tile of 32 keys twice, the scores by rows and the products
+// row are 512 columns wide: a wave cannot hold many rows, so four waves that share
+// up to 64 rows divide a tile of 32 keys twice, the scores by rows and the products
 // with the values by columns.  The weights pass from one division to the other
 // through LDS as the matrix instructions leave and take them: S^T = K Q^T gives a
 // lane the scores of one row for 8 keys, and their exponentials are, as they
@@ -15,6 +15,17 @@
 // Keys come straight into LDS through a ring of stages; an 8-bit cache's are
 // widened (exactly) from the ring into one tile of the 16-bit type, once for all
 // waves, and the cache's scale goes to the scores and to the result.
+//
+// Blocks of 128 rows have two such groups of waves over the same tile, and take the
+// values of one tile and the scores of the next in one turn: half the barriers, and
+// a SIMD's two waves need not be at the same of the two.
+//
+// What bounds it, with bf16: 16 rows (128 requests of some 4500 latents: 147 us) the
+// read, at 4.5 TB/s; 768 rows a request (32 of some 2600: 219 us, 630 TFLOP/s) nothing
+// alone: matrix instructions take half of the time, the reads of fragments from LDS
+// and the exponentials share the rest, and 4.9 TB/s come through the second-level
+// caches, whose hits alone would save 40 us.  Deeper rings and more fragments under
+// way change nothing.
 #pragma once
 
 #include "spec_attention_tile.h"
@@ -87,7 +98,7 @@ struct LatentPlan {
   }
 };
 
-template <bool kFp16, bool kE4M3, int DL, int MB, int NG, int NST, int kAhead, int kQL>
+template <bool kFp16, bool kE4M3, int DL, int MB, int NG, int NST, int kAhead>
 __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
   using D = LatentDims<kE4M3, DL, MB, NG, NST>;
   const AttnParams& p = lp.a;
@@ -96,7 +107,6 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
   __shared__ __align__(1024) char lds[D::kRing];
   constexpr int kBufs = D::kTwo ? 2 : 1;
   __shared__ u32x4_t weights[kBufs][D::kFrags][kWave];
-  __shared__ u32x4_t queries[kQL > 0 ? D::kFrags : 1][kQL > 0 ? kQL : 1][kWave];
   __shared__ uint64_t pages[kWindow];
   __shared__ AttnFind<D::kWaves> find;
   __shared__ float alpha[kBufs][D::kRows];
@@ -247,8 +257,8 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
       *qh = static_cast<int>(row) - *tok * p.group;
       return *tok < T;
     };
-    constexpr int kSteps = D::kKS + 2, kQR = kSteps - kQL;
-    u32x4_t qf[kQR];  // of the first steps; the rest lie in LDS
+    constexpr int kSteps = D::kKS + 2;
+    u32x4_t qf[kSteps];
     int my_tok = 0;
     if (scores) {
       int gq = g;
@@ -264,11 +274,8 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
         const bool there = d0 < (rope ? lp.rope : latent);
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(
             qp + (there ? 2 * (d0 + (rope ? latent : 0)) : 0));
-        u32x4_t x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = in && there ? w[i] ^ flip : 0;
-        if (s < kQR) qf[s < kQR ? s : 0] = x;
-        else queries[mine][s < kQR ? 0 : s - kQR][lane] = x;
+        for (int i = 0; i < 4; ++i) qf[s][i] = in && there ? w[i] ^ flip : 0;
       }
     }
     // which of the keys j0 .. j0 + 3 past the context token tok sees, as bits (j0 < 0: in it)
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
         // S^T of two 16-key tiles; fragments of kAhead steps are under way while those
         // before are multiplied
         f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        u32x4_t kf[kAhead + 1][2], ql[kAhead + 1];
+        u32x4_t kf[kAhead + 1][2];
         auto fetch = [&](int s) {
           const bool rope = s >= D::kKS;
 #pragma unroll
@@ -316,7 +323,6 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
             kf[s % (kAhead + 1)][t] = *reinterpret_cast<const u32x4_t*>(
                 rope ? base + (rx ^ ((s - D::kKS) << 6)) + 16 * t * D::kRopeRow
                      : base + (kx ^ (s % 4 << 6)) + 256 * (s / 4) + 16 * t * D::kRow);
-          if (s >= kQR) ql[s % (kAhead + 1)] = queries[mine][s - kQR][lane];
         };
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) fetch(s);
@@ -325,8 +331,7 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
           if (s + kAhead < kSteps) fetch(s + kAhead);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            st[t] = attn_mfma<kFp16>(kf[s % (kAhead + 1)][t],
-                                     s < kQR ? qf[s < kQR ? s : 0] : ql[s % (kAhead + 1)], st[t]);
+            st[t] = attn_mfma<kFp16>(kf[s % (kAhead + 1)][t], qf[s], st[t]);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (!open(tile)) {
@@ -687,11 +692,11 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentParams lp) {
   }
 }
 
-template <bool kFp16, bool kE4M3, int DL, int MB, int NG, int NST, int kAhead, int kQL>
+template <bool kFp16, bool kE4M3, int DL, int MB, int NG, int NST, int kAhead>
 hipError_t launch_latent_as(const LatentParams& p, const LatentShape& s, hipStream_t stream) {
   using D = LatentDims<kE4M3, DL, MB, NG, NST>;
   if (s.block_rows != D::kRows || s.slot_bytes != D::kSlotBytes) return hipErrorInvalidValue;
-  latent_kernel<kFp16, kE4M3, DL, MB, NG, NST, kAhead, kQL>
+  latent_kernel<kFp16, kE4M3, DL, MB, NG, NST, kAhead>
       <<<dim3(static_cast<uint32_t>(s.grid)), dim3(D::kThreads), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.ranges <= 1) return e;
@@ -703,18 +708,18 @@ hipError_t launch_latent_as(const LatentParams& p, const LatentShape& s, hipStre
 
 template <bool kFp16, bool kE4M3>
 hipError_t launch_latent(const LatentParams& p, const LatentShape& s, hipStream_t stream) {
-#define SGG_LATENT(dl, m, groups, n, ahead, in_lds)              \
+#define SGG_LATENT(dl, m, groups, n, ahead)                      \
   if (s.padded_dim == dl && s.block_rows == 16 * (m) * (groups)) \
-    return launch_latent_as<kFp16, kE4M3, dl, m, groups, n, ahead, in_lds>(p, s, stream)
+    return launch_latent_as<kFp16, kE4M3, dl, m, groups, n, ahead>(p, s, stream)
   constexpr int two = kE4M3 ? 2 : 3;  // stages of a ring beside two tiles in use
-  SGG_LATENT(256, 1, 1, 4, 3, 0);
-  SGG_LATENT(256, 2, 1, 4, 3, 0);
-  SGG_LATENT(256, 4, 1, 4, 3, 0);
-  SGG_LATENT(256, 4, 2, two, 3, 0);
-  SGG_LATENT(512, 1, 1, 2, 3, 0);
-  SGG_LATENT(512, 2, 1, 2, 3, 0);
-  SGG_LATENT(512, 4, 1, 2, 1, 0);
-  SGG_LATENT(512, 4, 2, two, 1, 0);
+  SGG_LATENT(256, 1, 1, 4, 3);
+  SGG_LATENT(256, 2, 1, 4, 3);
+  SGG_LATENT(256, 4, 1, 4, 3);
+  SGG_LATENT(256, 4, 2, two, 3);
+  SGG_LATENT(512, 1, 1, 2, 3);
+  SGG_LATENT(512, 2, 1, 2, 3);
+  SGG_LATENT(512, 4, 1, 2, 1);
+  SGG_LATENT(512, 4, 2, two, 1);
 #undef SGG_LATENT
   return hipErrorInvalidValue;
 }

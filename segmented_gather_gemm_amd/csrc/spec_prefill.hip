@@ -7,6 +7,14 @@
 // into LDS through a ring of stages.  Scores, weights and values as in the
 // attention over pages: S^T = K Q^T over dn + dr columns, whose exponentials are,
 // as they stand, the second operand of O^T = V^T P^T.
+//
+// What bounds it: 4 requests of 1024 tokens behind up to 3000 others, 32 heads of
+// 128 + 64 and 128 columns, 750 TFLOP/s.  Matrix instructions take 41 % of the time,
+// the vector unit's others 31 %, LDS reads 20 %; a wave does these in turn, and the
+// two waves of a SIMD, all that its registers hold, overlap them in part.  Tiles of 64
+// keys (half the barriers) and 64 rows a wave (half the reads) want more registers
+// than there are and are slower.  The softmax has the higher priority: what waits for
+// it is the next matrix work (305 us without).
 #include "spec_attention_tile.h"
 #include "spec_prefill.h"
 
@@ -64,8 +72,9 @@ __global__ __launch_bounds__(kPrefillThreads, 2) void prefill_kernel(PrefillPara
               (((2 * d + (l16 >> 1 & 1)) ^ key_swizzle<kPieces>(vr)) << 4) + 8 * (l16 & 1);
   }
   const int k_pieces = p.dn / 8, v_pieces = p.dv / 8, r_pieces = p.dr / 8;
-  // the padding of short rows is never loaded and stays zero
-  if (k_pieces < kPieces || v_pieces < kPieces || r_pieces < 8) {
+  // the padding of short keys is never loaded and stays zero; that of values feeds
+  // columns that nobody stores, and repeats their last piece
+  if (k_pieces < kPieces || r_pieces < 8) {
     for (int e = tid; e < kPrefillStages * kStage / 16; e += kPrefillThreads)
       reinterpret_cast<uint4*>(lds)[e] = make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -86,26 +95,39 @@ __global__ __launch_bounds__(kPrefillThreads, 2) void prefill_kernel(PrefillPara
     bool finite = true;  // no infinity or NaN among the values of tiles not seen in full
     __syncthreads();     // the last block is done with LDS
     if (tid == 0) patch = 0;
+    // offsets within a tile of 32 keys; its last one repeats the last key
+    uint32_t ko[kMine / kPer], vo[kMine / kPer], ro;
+    auto offsets = [&](int last) {
+#pragma unroll
+      for (int i = 0; i < kMine / kPer; ++i) {
+        const int row = wave * kMine + i * kPer + lane / kPieces;
+        const int piece = (lane % kPieces) ^ key_swizzle<kPieces>(row);
+        ko[i] = min(row, last) * static_cast<uint32_t>(p.kt) + 16 * piece;
+        vo[i] = min(row, last) * static_cast<uint32_t>(p.vt) + 16 * min(piece, v_pieces - 1);
+      }
+      const int row = wave * kMine + lane / 8;
+      ro = min(row, last) * static_cast<uint32_t>(p.krt) +
+           16 * ((lane % 8) ^ key_swizzle<8>(row));
+    };
+    offsets(kPrefillKeys - 1);
     auto load_tile = [&](int tile, int stage) {
+      const int64_t key0 = tile * kPrefillKeys;
+      if (key0 + kPrefillKeys > end) offsets(end - 1 - static_cast<int>(key0));
+      const char *kt = kb + key0 * p.kt, *vt = vb + key0 * p.vt, *rt = rb + key0 * p.krt;
       char* base = lds + stage * kStage;
 #pragma unroll
       for (int i = 0; i < kMine / kPer; ++i) {
         const int row = wave * kMine + i * kPer + lane / kPieces;
-        const int64_t key = min(tile * kPrefillKeys + row, end - 1);
         const int piece = (lane % kPieces) ^ key_swizzle<kPieces>(row);
         char* to = base + (wave * kMine + i * kPer) * kRow;
         if (piece < k_pieces)
-          __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)(kb + key * p.kt + 16 * piece),
+          __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)(kt + ko[i]),
                                            (SGG_LDS void*)to, 16, 0, 0);
-        if (piece < v_pieces)
-          __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)(vb + key * p.vt + 16 * piece),
-                                           (SGG_LDS void*)(to + kKey), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)(vt + vo[i]),
+                                         (SGG_LDS void*)(to + kKey), 16, 0, 0);
       }
-      const int row = wave * kMine + lane / 8;
-      const int64_t key = min(tile * kPrefillKeys + row, end - 1);
-      const int piece = (lane % 8) ^ key_swizzle<8>(row);
-      if (piece < r_pieces)
-        __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)(rb + key * p.krt + 16 * piece),
+      if (((lane % 8) ^ key_swizzle<8>(wave * kMine + lane / 8)) < r_pieces)
+        __builtin_amdgcn_global_load_lds((const SGG_GLOBAL void*)(rt + ro),
                                          (SGG_LDS void*)(base + 2 * kKey + wave * kMine * kRopeRow),
                                          16, 0, 0);
     };
@@ -139,20 +161,14 @@ __global__ __launch_bounds__(kPrefillThreads, 2) void prefill_kernel(PrefillPara
 #pragma unroll
       for (int d = 0; d < kDT; ++d) o[m][d] = f32x4{0, 0, 0, 0};
     }
-    int stage = 0, fill = 0;
-#pragma unroll 1
-    for (int tile = -(kPrefillStages - 1); tile < tiles; ++tile) {
-      const int ahead = tile + kPrefillStages - 1;
-      if (tile >= 0) {
-        wait_tiles(min(tiles - 1 - tile, kPrefillStages - 2));
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-      }
-      if (ahead < tiles) load_tile(ahead, fill);  // into the stage that the last turn has read
-      fill = fill + 1 == kPrefillStages ? 0 : fill + 1;
-      if (tile < 0) continue;
+    auto turn = [&](int tile, int stage) __attribute__((always_inline)) {
+      wait_tiles(min(tiles - 1 - tile, kPrefillStages - 2));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      // into the stage that the last turn has read
+      if (tile + kPrefillStages - 1 < tiles)
+        load_tile(tile + kPrefillStages - 1, stage == 0 ? kPrefillStages - 1 : stage - 1);
       const char* base = lds + stage * kStage;
-      stage = stage + 1 == kPrefillStages ? 0 : stage + 1;
       const int key0 = tile * kPrefillKeys;
       f32x4 st[MF][2];
 #pragma unroll
@@ -238,6 +254,13 @@ __global__ __launch_bounds__(kPrefillThreads, 2) void prefill_kernel(PrefillPara
           for (int m = 0; m < MF; ++m) o[m][d0 + d] = attn_mfma<kFp16>(vf[d], pf[m], o[m][d0 + d]);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage has been read
+    };
+    for (int t = 0; t < kPrefillStages - 1 && t < tiles; ++t) load_tile(t, t);
+    int stage = 0;
+#pragma unroll 1
+    for (int tile = 0; tile < tiles; ++tile) {
+      turn(tile, stage);
+      stage = stage + 1 == kPrefillStages ? 0 : stage + 1;
     }
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
@@ -281,7 +304,8 @@ __global__ __launch_bounds__(kPrefillThreads, 2) void prefill_kernel(PrefillPara
 hipError_t launch_prefill(PrefillParams p, bool fp16, int32_t max_q_len, hipStream_t stream) {
   const int64_t pairs = static_cast<int64_t>(p.bs) * p.heads;
   const int64_t rounds = (pairs + kXcds - 1) / kXcds;
-  // 128 rows a workgroup once that fills the GPU
+  // 128 rows a workgroup once that fills the GPU (4 requests' 1024 tokens of 32 heads:
+  // 285 us, 395 with 64; 100 tokens of 16 heads: 10 us, 15 with 128)
   const int mf = rounds * kXcds * ((max_q_len + 127) / 128) >= 512 ? 2 : 1;
   p.blocks = (max_q_len + 64 * mf - 1) / (64 * mf);
   if (p.blocks < 1) p.blocks = 1;
