@@ -165,6 +165,11 @@ def test_prefill_refused(kw, code, text):
     refused(prefill(**kw), code, text)
 
 
+@pytest.mark.parametrize("kw", [dict(kt=1 << 26), dict(vt=1 << 26), dict(kpt=1 << 26)])
+def test_prefill_refuses_keys_far_apart(kw):
+    refused(prefill(**kw), -2, "2^26")
+
+
 def probs(x=F, ldx=1000, dtype=FP32, V=1000, ind=F, bs=4, n=9, mq=4, tokens=F, parents=F, hist=F,
           ldh=50, width=50, rows_n=6, hl=F, pl=F, rows=F, temp=F, rep=F, pres=F, freq=F, bp=F, bi=F,
           bv=F, nb=7, allowed=F, lda=32, out=F, ldo=1000, ws=F, wsn=1 << 30):
