@@ -257,12 +257,15 @@ namespace sgg {
 // requests of 16 rows and some 4500 latents: 149 us, 198 in blocks of 64.  The 128 rows
 // of each of two requests with 100003: 111 us, 117 in two blocks of 64.  32 requests of
 // 768 rows: 236 us, 244.)  Two workgroups of up to 64 rows share a CU's LDS and
-// registers, one of 128 takes it whole.
+// registers, one of 128 takes it whole.  A batch that is too small to give every CU a
+// range takes smaller blocks: more workgroups, and less of each in one after another (one
+// request of 128 rows and 500 latents: 16.8 us, 24.8 in one block; 16 of 64 and 600:
+// 29.5, 36.9; one of 128 and 8000, the dearest: 39.7, 36.3).
 //
 // The tiles of all units, a request's row blocks, are one line that is cut into as many
 // ranges as workgroups are on the GPU at once; a small block's ranges may be single tiles
 // (one request's 500 latents: 14.1 us, 14.9 at two tiles and more), larger blocks' at
-// least so long that their partial sums are no more than the latents read.  Units so many
+// least rows / 32 tiles, for a piece costs the write and the read of 2 KB a row.  Units so many
 // that they fill the GPU by themselves take a workgroup each and nothing is joined.
 // Where units are few and pieces many the join takes smaller items (two requests of 256
 // pieces: 111 us, 120; one of 16: 14.6, 16.0).
@@ -271,18 +274,22 @@ LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t max_
   LatentShape s{};
   const int64_t rows = static_cast<int64_t>(max_q_len) * heads;
   s.padded_dim = latent <= 256 ? 256 : 512;
-  s.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int64_t tiles = (max_kv_len + kLatentKeys - 1) / kLatentKeys;
+  int64_t blocks, units, most;
+  for (s.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;;
+       s.block_rows /= 2) {
+    s.min_tiles = s.block_rows <= 32 ? 1 : s.block_rows / 32;
+    blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
+    units = bs * blocks;
+    most = units * ((tiles + s.min_tiles - 1) / s.min_tiles);
+    if (s.block_rows == 16 || most >= 256) break;
+  }
   const int64_t resident = s.block_rows == 128 ? 256 : 512;  // workgroups on the GPU at once
   s.slot_bytes = static_cast<int64_t>(s.block_rows) * (s.padded_dim * 4 + 8);
-  s.min_tiles = s.block_rows <= 32 ? 1 : s.block_rows / 32;
-  const int64_t blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
-  const int64_t units = bs * blocks;
   if (blocks > 1 && units >= 2 * resident) {
     s.ranges = 0;
     s.grid = units;
   } else {
-    const int64_t tiles = (max_kv_len + kLatentKeys - 1) / kLatentKeys;
-    const int64_t most = units * ((tiles + s.min_tiles - 1) / s.min_tiles);
     const int64_t n = most < resident ? most : resident;
     s.ranges = static_cast<int32_t>(n < 1 ? 1 : n);
     // (the kernel may take the batch by units)

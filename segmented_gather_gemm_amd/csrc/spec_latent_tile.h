@@ -73,7 +73,9 @@ __device__ __forceinline__ void hide(int& x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ int latent_swizzle(int r) { return 2 * (r & 7); }
 __device__ __forceinline__ int rope_swizzle(int r) { return r & 6; }
 
-// The ranges of positions of a batch (see AttnWork).
+// The ranges of positions of a batch (see AttnWork).  Units too short to be worth two
+// ranges are taken one by one: ranges of min_tiles would hold several of them (123
+// requests of 192 rows and a tile: 78 us in ranges).
 template <int NW, int R, int K>
 struct LatentPlan {
   AttnWork<NW, R, K> work;
@@ -85,6 +87,7 @@ struct LatentPlan {
     AttnTotal sizes = attn_scan(work, find, &share);
     if (!work.by_unit &&
         (sizes.all > INT32_MAX ||
+         sizes.longest <= 2 * p.min_tiles ||
          (sizes.units >= p.ranges && sizes.longest <= 2 * (sizes.all / p.ranges)))) {
       work.by_unit = true;
       __syncthreads();

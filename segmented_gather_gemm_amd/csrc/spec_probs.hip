@@ -170,9 +170,12 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
   }
 
   // what the text and the biases say of the chunk's values
+  static_assert(sizeof(s.stats) >= kProbsChunk * sizeof(int), "a lane's number for each value");
+  int* const turn = reinterpret_cast<int*>(s.stats);  // (free until the nodes')
   for (int e = tid; e < kProbsChunk; e += kProbsThreads) {
     s.word[e] = 0;
     s.shift[e] = 0.0f;
+    if (b0 < b1) turn[e] = kWave;
   }
   if (path) {
     for (int i = tid; i < min(T, kProbsTree); i += kProbsThreads) {
@@ -197,13 +200,19 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
     }
   }
   if (wave == 0) {
-    // added in their order, so that an id named twice gives the same sum on every run
+    // added in their order, so that an id named twice gives the same sum on every run: of
+    // the lanes that have the same value the first goes, then the next (one after another,
+    // whatever their values, takes 30 us for 300 in one chunk)
     for (int64_t b = b0; b < b1; b += kWave) {
-      uint64_t left = __ballot(bias_spot >= 0);
-      while (left) {
-        const int l = __ffsll(static_cast<unsigned long long>(left)) - 1;
-        left &= left - 1;
-        if (lane == l) s.shift[bias_spot] += bias_value;
+      while (__ballot(bias_spot >= 0)) {
+        if (bias_spot >= 0) atomicMin(&turn[bias_spot], lane);
+        __builtin_amdgcn_wave_barrier();
+        if (bias_spot >= 0 && *static_cast<volatile int*>(&turn[bias_spot]) == lane) {
+          s.shift[bias_spot] += bias_value;
+          turn[bias_spot] = kWave;
+          bias_spot = -1;
+        }
+        __builtin_amdgcn_wave_barrier();
       }
       bias_spot = bias_at(b + kWave + lane);
       if (bias_spot >= 0) bias_value = p.bias_values[b + kWave + lane];

@@ -219,3 +219,27 @@ def test_probabilities_go_into_the_verification():
     u, f = torch.full((8,), 0.5, device=DEV), torch.full((2,), 0.5, device=DEV)
     path, accept, nxt = _sgg().spec_verify(tok, _i32(np.concatenate(s.trees)), _i32(s.ptr), p, u, f, 4)
     assert accept.tolist() == [4, 3] and nxt.tolist() == [int(p[3].argmax()), int(p[6].argmax())]
+
+
+def test_biases_of_one_value_are_added_in_their_order():
+    """Sums whose float32 value depends on the order, several to a batch of 64 and across batches.
+
+    The sums are exact copies, so what is left is the softmax: below 2^-18 of each as in check."""
+    rng = np.random.default_rng(8)
+    ids = rng.integers(0, 5, 333)
+    values = rng.choice([1.0, -1.0, 2.0 ** 24, -2.0 ** 24, 0.25], 333).astype(np.float32)
+    want, back = np.zeros(5, np.float32), np.zeros(5, np.float32)
+    for i in range(333):
+        want[ids[i]] += values[i]
+        back[ids[332 - i]] += values[332 - i]
+    assert (want != back).any()
+    # down to a few units, so that every sum shows
+    ids = np.concatenate([ids, np.arange(5)])
+    values = np.concatenate([values, rng.integers(-2, 3, 5) - want]).astype(np.float32)
+    want += values[333:]
+    assert np.abs(want).max() <= 4
+    got = _sgg().spec_target_probs(torch.zeros((1, 5), device=DEV), _i32([0, 1]), 1,
+                                   bias_indptr=_i32([0, 338]), bias_ids=_i32(ids),
+                                   bias_values=_f32(values))
+    e = np.exp(want.astype(np.float64))
+    assert (np.abs(f64(got[0]) - e / e.sum()) <= 2.0 ** -18 * e / e.sum()).all()
