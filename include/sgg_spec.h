@@ -8,7 +8,10 @@
  * spec_tree_mask), verify the drafts against the target's probabilities
  * (spec_verify), move the accepted tokens' rows together (spec_kv_compact) and
  * give the other pages back (spec_kv_resize).  spec_kv_fork lets one sequence
- * go on as several.
+ * go on as several.  spec_rope_write rotates queries and keys on the way into the
+ * pages, spec_target_probs makes the target's probabilities of its logits, and
+ * spec_latent_write, _gather, _attention and _prefill serve models whose tokens keep
+ * one latent for all heads.
  *
  * Status codes, lora_last_error(), ownership and streams are those of
  * sgg_lora.h: 0 on success, arguments checked on the host before anything is
