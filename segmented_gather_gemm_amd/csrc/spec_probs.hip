@@ -25,8 +25,8 @@ namespace {
 constexpr int kProbsThreads = 256;
 constexpr int kProbsWaves = kProbsThreads / kWave;
 constexpr int kProbsNodes = 16;
-constexpr int kProbsEntries = 32;   // values of a node's path in the chunk; more are walked again
-constexpr int kProbsParts = kProbsThreads / 4;  // of a node's row: what four lanes hold
+constexpr int kProbsEntries = 32;   // values of a node's path in the chunk; more are counted
+constexpr int kProbsParts = kProbsThreads / 8;  // of a node's row: what eight lanes hold
 constexpr int kProbsTree = 256;     // nodes whose parents and tokens are kept in LDS
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kProbsChunk == 8 * kProbsThreads, "a thread takes two groups of four values");
@@ -53,6 +53,7 @@ constexpr uint32_t kInPrompt = 1u << 31, kCount = kInPrompt - 1;
 struct ProbsShared {
   uint32_t word[kProbsChunk];
   float shift[kProbsChunk];          // what is added to a value's logit
+  uint32_t path[kProbsChunk];        // occurrences on a long path; zero between its uses
   int parent[kProbsTree], token[kProbsTree];
   int entries[kProbsNodes];          // of `entry`, or more than there is room for
   uint32_t entry[kProbsNodes][kProbsEntries];  // place in the chunk, occurrences << 16
@@ -170,12 +171,10 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
   }
 
   // what the text and the biases say of the chunk's values
-  static_assert(sizeof(s.stats) >= kProbsChunk * sizeof(int), "a lane's number for each value");
-  int* const turn = reinterpret_cast<int*>(s.stats);  // (free until the nodes')
   for (int e = tid; e < kProbsChunk; e += kProbsThreads) {
     s.word[e] = 0;
     s.shift[e] = 0.0f;
-    if (b0 < b1) turn[e] = kWave;
+    s.path[e] = 0;
   }
   if (path) {
     for (int i = tid; i < min(T, kProbsTree); i += kProbsThreads) {
@@ -205,11 +204,12 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
     // whatever their values, takes 30 us for 300 in one chunk)
     for (int64_t b = b0; b < b1; b += kWave) {
       while (__ballot(bias_spot >= 0)) {
-        if (bias_spot >= 0) atomicMin(&turn[bias_spot], lane);
+        const uint32_t turn = kWave - lane;
+        if (bias_spot >= 0) atomicMax(&s.path[bias_spot], turn);
         __builtin_amdgcn_wave_barrier();
-        if (bias_spot >= 0 && *static_cast<volatile int*>(&turn[bias_spot]) == lane) {
+        if (bias_spot >= 0 && *static_cast<volatile uint32_t*>(&s.path[bias_spot]) == turn) {
           s.shift[bias_spot] += bias_value;
-          turn[bias_spot] = kWave;
+          s.path[bias_spot] = 0;
           bias_spot = -1;
         }
         __builtin_amdgcn_wave_barrier();
@@ -256,14 +256,14 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
     if (tid < count) {
       int n = 0;
       if (path) {
-        for (int i = i0 + tid; i >= 0; i = parent_of(i)) {
+        for (int i = i0 + tid; i >= 0 && n <= kProbsEntries; i = parent_of(i)) {
           const int at = place(token_of(i));
           if (at < 0) continue;
           int e = 0;
           while (e < min(n, kProbsEntries) && (s.entry[tid][e] & 0xffffu) != static_cast<uint32_t>(at))
             ++e;
           if (e < n && e < kProbsEntries) {
-            if (s.entry[tid][e] >= 0xffff0000u) n = kProbsEntries + 1;  // (walked again)
+            if (s.entry[tid][e] >= 0xffff0000u) n = kProbsEntries + 1;  // (counted)
             s.entry[tid][e] += 1u << 16;
           } else {
             if (n < kProbsEntries) s.entry[tid][n] = static_cast<uint32_t>(at) | 1u << 16;
@@ -342,13 +342,24 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
         if (entries <= kProbsEntries) {
           for (int e = 0; e < entries; ++e) redo(s.entry[j][e] & 0xffffu, s.entry[j][e] >> 16);
         } else {
-          // (a value's last place on the way up counts all of them)
-          for (int i = i0 + j; i >= 0; i = parent_of(i)) {
-            const int at = place(token_of(i));
-            if (at < 0) continue;
-            uint32_t more = 0;
-            for (int k2 = i0 + j; k2 >= 0; k2 = parent_of(k2)) more += place(token_of(k2)) == at;
-            redo(at, more);
+          __syncthreads();  // the last long path's counts have been cleared
+          if (!p.parents) {
+            for (int i = tid; i <= i0 + j; i += kProbsThreads) {
+              const int at = place(token_of(i));
+              if (at >= 0) atomicAdd(&s.path[at], 1u);
+            }
+          } else if (tid == 0) {
+            for (int i = i0 + j; i >= 0; i = parent_of(i)) {
+              const int at = place(token_of(i));
+              if (at >= 0) ++s.path[at];
+            }
+          }
+          __syncthreads();
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int at = 4 * (tid + i / 4 * kProbsThreads) + i % 4;
+            if (const uint32_t more = s.path[at]) redo(at, more);
+            s.path[at] = 0;
           }
         }
       }
@@ -375,12 +386,13 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
           mask[d][g] = mask[d + 1][g];
         }
       if constexpr (!kFinal) {
-        // Four lanes' values together now, the rest of the way for all nodes at once.
+        // Eight lanes' values together now, the rest of the way for all nodes at once.
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = fmaxf(top, x[i]);
         top = fmaxf(top, turned<8>(top));
         top = fmaxf(top, turned<4>(top));
+        top = fmaxf(top, turned<2>(top));
         float sum = 0.0f;
         int first = INT32_MAX;
         if (greedy) {
@@ -389,14 +401,16 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
             if (x[i] == top) first = c0 + 4 * (tid + i / 4 * kProbsThreads) + i % 4;
           first = min(first, rotated<8>(first));
           first = min(first, rotated<4>(first));
+          first = min(first, rotated<2>(first));
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum += weight(x[i], top, k);
           sum += turned<8>(sum);
           sum += turned<4>(sum);
+          sum += turned<2>(sum);
         }
-        if (lane % 16 < 4) {
-          const int part = 4 * (tid / 16) + lane % 4;
+        if (lane % 16 < 2) {
+          const int part = 2 * (tid / 16) + lane % 2;
           s.stats[j][part] = make_float2(top, top == kNothing ? 0.0f : sum);
           s.first[j][part] = first;
         }
@@ -435,13 +449,13 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
     }
     if constexpr (!kFinal) {
       __syncthreads();
-      static_assert(kProbsNodes * 16 == kProbsThreads && kProbsParts == 64, "16 lanes a node");
+      static_assert(kProbsNodes * 16 == kProbsThreads && kProbsParts == 32, "16 lanes a node");
       const int j = tid / 16;
       float top = kNothing, sum = 0.0f;
       int first = INT32_MAX;
       if (j < count) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, s.stats[j][4 * (lane % 16) + e].x);
+        for (int e = 0; e < 2; ++e) top = fmaxf(top, s.stats[j][2 * (lane % 16) + e].x);
       }
       top = fmaxf(top, turned<8>(top));
       top = fmaxf(top, turned<4>(top));
@@ -449,9 +463,9 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
       top = fmaxf(top, turned<1>(top));
       if (j < count) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = s.stats[j][4 * (lane % 16) + e];
-          if (x.x == top) first = min(first, s.first[j][4 * (lane % 16) + e]);
+        for (int e = 0; e < 2; ++e) {
+          const float2 x = s.stats[j][2 * (lane % 16) + e];
+          if (x.x == top) first = min(first, s.first[j][2 * (lane % 16) + e]);
           sum += x.y * weight(x.x, top, k);
         }
       }

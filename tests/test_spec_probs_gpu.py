@@ -243,3 +243,15 @@ def test_biases_of_one_value_are_added_in_their_order():
                                    bias_values=_f32(values))
     e = np.exp(want.astype(np.float64))
     assert (np.abs(f64(got[0]) - e / e.sum()) <= 2.0 ** -18 * e / e.sum()).all()
+
+
+@pytest.mark.parametrize("V", [700, 5000])
+def test_long_paths_of_many_values(V):
+    """Paths of more values than a list holds, of trees and of chains with and without parents."""
+    s = Batch([300, 3, 90], V, seed=9, chain=False, history=30)
+    s.tokens = s.rng.integers(-2, V + 2, 393)
+    s.check(s.call())
+    s.trees = [list(range(-1, k - 1)) for k in s.ql]
+    got = s.call()
+    s.check(got)
+    assert torch.equal(s.call(parents=None), got)
