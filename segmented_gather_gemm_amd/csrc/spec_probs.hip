@@ -25,7 +25,7 @@ namespace {
 constexpr int kProbsThreads = 256;
 constexpr int kProbsWaves = kProbsThreads / kWave;
 constexpr int kProbsNodes = 16;
-constexpr int kProbsEntries = 32;   // values of a node's path in the chunk; more are counted
+constexpr int kProbsEntries = 32;   // tokens of a node's path in the chunk; more are counted
 constexpr int kProbsParts = kProbsThreads / 8;  // of a node's row: what eight lanes hold
 constexpr int kProbsTree = 256;     // nodes whose parents and tokens are kept in LDS
 constexpr float kLog2e = 1.4426950408889634f;
@@ -56,7 +56,7 @@ struct ProbsShared {
   uint32_t path[kProbsChunk];        // occurrences on a long path; zero between its uses
   int parent[kProbsTree], token[kProbsTree];
   int entries[kProbsNodes];          // of `entry`, or more than there is room for
-  uint32_t entry[kProbsNodes][kProbsEntries];  // place in the chunk, occurrences << 16
+  int entry[kProbsNodes][kProbsEntries];       // places in the chunk of the node's path
   float2 stats[kProbsNodes][kProbsParts];
   int first[kProbsNodes][kProbsParts];
 };
@@ -162,13 +162,22 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
     return v >= 0 && at < static_cast<uint32_t>(here) ? static_cast<int>(at) : -1;
   };
   const int64_t b0 = max(bias0, 0), b1 = min(static_cast<int64_t>(bias1), p.num_bias);
-  auto bias_at = [&](int64_t b) { return b < b1 ? place(p.bias_ids[b]) : -1; };
-  int bias_spot = -1;
-  float bias_value = 0.0f;
-  if (wave == 0 && b0 + lane < b1) {
-    bias_spot = bias_at(b0 + lane);
-    bias_value = p.bias_values[b0 + lane];
-  }
+  constexpr int kBiases = 4;  // batches of 64 biases whose loads are under way at once
+  int bias_spot[kBiases];
+  float bias_value[kBiases];
+  auto fetch_biases = [&](int64_t b) {
+#pragma unroll
+    for (int i = 0; i < kBiases; ++i) {
+      const int64_t at = b + i * kWave + lane;
+      bias_spot[i] = -1;
+      bias_value[i] = 0.0f;
+      if (at < b1) {
+        bias_spot[i] = p.bias_ids[at];
+        bias_value[i] = p.bias_values[at];
+      }
+    }
+  };
+  if (wave == 0) fetch_biases(b0);
 
   // what the text and the biases say of the chunk's values
   for (int e = tid; e < kProbsChunk; e += kProbsThreads) {
@@ -202,20 +211,23 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
     // added in their order, so that an id named twice gives the same sum on every run: of
     // the lanes that have the same value the first goes, then the next (one after another,
     // whatever their values, takes 30 us for 300 in one chunk)
-    for (int64_t b = b0; b < b1; b += kWave) {
-      while (__ballot(bias_spot >= 0)) {
-        const uint32_t turn = kWave - lane;
-        if (bias_spot >= 0) atomicMax(&s.path[bias_spot], turn);
-        __builtin_amdgcn_wave_barrier();
-        if (bias_spot >= 0 && *static_cast<volatile uint32_t*>(&s.path[bias_spot]) == turn) {
-          s.shift[bias_spot] += bias_value;
-          s.path[bias_spot] = 0;
-          bias_spot = -1;
+    for (int64_t b = b0; b < b1; b += kBiases * kWave) {
+#pragma unroll
+      for (int i = 0; i < kBiases; ++i) {
+        int at = place(bias_spot[i]);
+        while (__ballot(at >= 0)) {
+          const uint32_t turn = kWave - lane;
+          if (at >= 0) atomicMax(&s.path[at], turn);
+          __builtin_amdgcn_wave_barrier();
+          if (at >= 0 && *static_cast<volatile uint32_t*>(&s.path[at]) == turn) {
+            s.shift[at] += bias_value[i];
+            s.path[at] = 0;
+            at = -1;
+          }
+          __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
       }
-      bias_spot = bias_at(b + kWave + lane);
-      if (bias_spot >= 0) bias_value = p.bias_values[b + kWave + lane];
+      if (b + kBiases * kWave < b1) fetch_biases(b + kBiases * kWave);
     }
   }
   __syncthreads();
@@ -259,16 +271,8 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
         for (int i = i0 + tid; i >= 0 && n <= kProbsEntries; i = parent_of(i)) {
           const int at = place(token_of(i));
           if (at < 0) continue;
-          int e = 0;
-          while (e < min(n, kProbsEntries) && (s.entry[tid][e] & 0xffffu) != static_cast<uint32_t>(at))
-            ++e;
-          if (e < n && e < kProbsEntries) {
-            if (s.entry[tid][e] >= 0xffff0000u) n = kProbsEntries + 1;  // (counted)
-            s.entry[tid][e] += 1u << 16;
-          } else {
-            if (n < kProbsEntries) s.entry[tid][n] = static_cast<uint32_t>(at) | 1u << 16;
-            n = min(n, kProbsEntries) + 1;
-          }
+          if (n < kProbsEntries) s.entry[tid][n] = at;
+          ++n;
         }
       }
       s.entries[tid] = n;
@@ -323,13 +327,8 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
       const int entries = __builtin_amdgcn_readfirstlane(s.entries[j]);
       if (__builtin_expect(entries > 0, 0)) {
         // values that the node's path holds, from their logits once more
-        auto redo = [&](int at, uint32_t more) {
-          const int u = at - 4 * tid;
-          const int mine = u >= 0 && u < 4 ? u
-                           : u >= 4 * kProbsThreads && u < 4 * kProbsThreads + 4
-                               ? u - 4 * kProbsThreads + 4
-                               : -1;
-          if (mine < 0) return;
+        auto redo = [&](int mine, uint32_t more) {
+          const int at = 4 * (tid + mine / 4 * kProbsThreads) + mine % 4;
           float extra = static_cast<float>(more) * freq;
           if (!(s.word[at] & kCount)) extra += pres;
           const float shift = s.shift[at] - extra;
@@ -340,7 +339,15 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
           }
         };
         if (entries <= kProbsEntries) {
-          for (int e = 0; e < entries; ++e) redo(s.entry[j][e] & 0xffffu, s.entry[j][e] >> 16);
+          uint64_t times = 0;  // 8 bits for each of the thread's values
+          for (int e = 0; e < entries; ++e) {
+            const int at = s.entry[j][e];
+            if (at / 4 % kProbsThreads == tid)
+              times += 1ull << 8 * (at % 4 + at / (4 * kProbsThreads) * 4);
+          }
+#pragma unroll 1
+          for (int i = 0; times != 0; ++i, times >>= 8)
+            if (const uint32_t more = times & 255) redo(i, more);
         } else {
           __syncthreads();  // the last long path's counts have been cleared
           if (!p.parents) {
@@ -358,7 +365,7 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const int at = 4 * (tid + i / 4 * kProbsThreads) + i % 4;
-            if (const uint32_t more = s.path[at]) redo(at, more);
+            if (const uint32_t more = s.path[at]) redo(i, more);
             s.path[at] = 0;
           }
         }
