@@ -282,7 +282,7 @@ LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t max_
     blocks = rows > 0 ? (rows + s.block_rows - 1) / s.block_rows : 1;
     units = bs * blocks;
     most = units * ((tiles + s.min_tiles - 1) / s.min_tiles);
-    if (s.block_rows == 16 || most >= 256) break;
+    if (s.block_rows == 16 || tiles == 0 || most >= 256) break;
   }
   const int64_t resident = s.block_rows == 128 ? 256 : 512;  // workgroups on the GPU at once
   s.slot_bytes = static_cast<int64_t>(s.block_rows) * (s.padded_dim * 4 + 8);
