@@ -125,6 +125,18 @@ def test_latent_attention(case):
     assert torch.equal(s.call(), got)
 
 
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_blocks_of_a_long_launch(case):
+    """The same requests in a launch for long ones, which takes the row blocks that hold them."""
+    kv, ql, H, latent, rope, ps, dtype, cache, drafts = case
+    rng = np.random.default_rng(H)
+    s = Latents(kv, ql, H, latent, rope, ps, dtype, cache,
+                [tree(n, rng) for n in ql] if drafts else None, seed=latent + H + 1)
+    got = s.call(max_kv_len=1 << 20)
+    s.check(got)
+    assert torch.equal(s.call(max_kv_len=1 << 20), got)
+
+
 @pytest.mark.parametrize("kv,ql,H,cache", [
     ([5000], [1], 16, None), ([9000, 40], [2, 1], 16, "e4m3"), ([4097], [4], 32, None),
     ([3333, 2000], [1, 2], 64, None), ([2500], [3], 128, "e4m3")])
