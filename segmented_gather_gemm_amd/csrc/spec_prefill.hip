@@ -305,7 +305,7 @@ hipError_t launch_prefill(PrefillParams p, bool fp16, int32_t max_q_len, hipStre
   const int64_t pairs = static_cast<int64_t>(p.bs) * p.heads;
   const int64_t rounds = (pairs + kXcds - 1) / kXcds;
   // 128 rows a workgroup once that fills the GPU (4 requests' 1024 tokens of 32 heads:
-  // 290 us in that run, 395 with 64; 100 tokens of 16 heads: 10 us, 15 with 128)
+  // 290 us, 395 with 64; 100 tokens of 16 heads: 10 us, 15 with 128)
   const int mf = rounds * kXcds * ((max_q_len + 127) / 128) >= 512 ? 2 : 1;
   p.blocks = (max_q_len + 64 * mf - 1) / (64 * mf);
   if (p.blocks < 1) p.blocks = 1;
