@@ -26,18 +26,23 @@ int check_types(int32_t dtype, int32_t cache_dtype, const char* what) {
   return SGG_OK;
 }
 
+int check_latent_dim(int32_t latent, int32_t dtype) {
+  SGG_CHECK(dtype >= SPEC_BF16 && dtype <= SPEC_E4M3, SGG_ERR_INVALID,
+            "cache dtype %d is unknown", dtype);
+  SGG_CHECK(latent > 0 && latent <= 512 && latent * (dtype == SPEC_E4M3 ? 1 : 2) % 16 == 0,
+            SGG_ERR_UNSUPPORTED, "latent_dim=%d must be a multiple of 16 bytes up to 512 values",
+            latent);
+  return SGG_OK;
+}
+
 int check_latent_cache(const SpecLatentCache* c, sgg::PagedRows* rows, int32_t* shift) {
   SGG_CHECK(c != nullptr, SGG_ERR_INVALID, "cache is NULL");
   SGG_CHECK(c->data != nullptr, SGG_ERR_INVALID, "cache data is NULL");
-  SGG_CHECK(c->dtype >= SPEC_BF16 && c->dtype <= SPEC_E4M3, SGG_ERR_INVALID,
-            "cache dtype %d is unknown", c->dtype);
+  SGG_TRY(check_latent_dim(c->latent_dim, c->dtype));
   SGG_CHECK(c->num_pages > 0 && c->num_pages <= INT32_MAX, SGG_ERR_INVALID,
             "num_pages=%" PRId64 " outside [1, 2^31)", c->num_pages);
   SGG_TRY(check_page_size(c->page_size, shift));
   const int32_t es = c->dtype == SPEC_E4M3 ? 1 : 2;
-  SGG_CHECK(c->latent_dim > 0 && c->latent_dim <= 512 && c->latent_dim * es % 16 == 0,
-            SGG_ERR_UNSUPPORTED, "latent_dim=%d must be a multiple of 16 bytes up to 512 values",
-            c->latent_dim);
   SGG_CHECK(c->rope_dim > 0 && c->rope_dim <= 64 && c->rope_dim * es % 16 == 0,
             SGG_ERR_UNSUPPORTED, "rope_dim=%d must be a multiple of 16 bytes up to 64 values",
             c->rope_dim);
@@ -305,7 +310,9 @@ LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t max_
 extern "C" int64_t spec_latent_attention_workspace_bytes(int32_t bs, int32_t num_heads,
                                                          int32_t latent_dim, int32_t cache_dtype,
                                                          int32_t max_q_len, int64_t max_kv_len) {
-  if (check_latent_heads(bs, num_heads, latent_dim, max_q_len, max_kv_len) != SGG_OK) return -1;
+  if (check_latent_heads(bs, num_heads, latent_dim, max_q_len, max_kv_len) != SGG_OK ||
+      check_latent_dim(latent_dim, cache_dtype) != SGG_OK)
+    return -1;
   const sgg::LatentShape s =
       sgg::latent_shape(bs, num_heads, latent_dim, max_q_len, max_kv_len);
   sgg::ok();
