@@ -138,14 +138,15 @@ def spec_latent_attention(q, cache, page_table, kv_lens, q_indptr, max_q_len, ma
     return out
 
 
-def spec_latent_prefill(q, k, v, k_pe, q_indptr, kv_indptr, max_q_len, max_kv_len, scale=None,
-                        out=None):
+def spec_latent_prefill(q, k, v, k_pe, q_indptr, kv_indptr, max_q_len, max_kv_len=None,
+                        scale=None, out=None):
     """Causal attention over expanded latents: the queries of request r, rows q_indptr[r] .. of
     ``q`` (tokens, heads, nope + rope), are the last of its tokens, whose keys and values are rows
     kv_indptr[r] .. of ``k`` (.., heads, nope), ``v`` (.., heads, v_dim) and ``k_pe`` (.., rope), the
-    rotated key part of all heads.  ``max_q_len`` / ``max_kv_len`` bound a request's queries and
-    keys; they shape the launch, not the result.  ``scale`` defaults to (nope + rope) ** -0.5.
-    Returns ``out`` (tokens, heads, v_dim)."""
+    rotated key part of all heads.  ``max_q_len`` bounds a request's queries; it shapes the launch,
+    not the result.  ``max_kv_len`` is not used: a row block takes all of its keys, and nothing is
+    divided over them.  ``scale`` defaults to (nope + rope) ** -0.5.  Returns ``out`` (tokens,
+    heads, v_dim)."""
     dev = q.get_device()
     qp, qt, qh = _heads("q", q)
     kp, kt, kh = _heads("k", k)
@@ -158,7 +159,7 @@ def spec_latent_prefill(q, k, v, k_pe, q_indptr, kv_indptr, max_q_len, max_kv_le
     if k.shape[1] != H or v.shape[:2] != (m, H) or k_pe.shape[0] != m or d != dn + dr:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} and k_pe "
                          f"{tuple(k_pe.shape)} do not match")
-    if max_kv_len < 0:
+    if max_kv_len is not None and max_kv_len < 0:
         raise ValueError(f"max_kv_len={max_kv_len} is negative")
     if out is None:
         out = torch.empty((n, H, dv), dtype=q.dtype, device=q.device)
