@@ -375,8 +375,9 @@ int spec_latent_prefill(const void* q, int64_t q_token, int64_t q_head, const vo
  *   added up in their order
  *   x = -inf if x is NaN or bit v % 32 of allowed[row][v / 32] is not set
  *   out = softmax(x / temperature[r]); a temperature that is not above 0: 1 at the
- *   first of the largest, 0 elsewhere.  Infinities count as the largest numbers
- *   (places of +inf share 1 equally); a row that holds nothing but -inf becomes 0.
+ *   first of the largest, 0 elsewhere.  +inf counts as the largest number (such
+ *   places share 1 equally); a row that holds nothing but -inf becomes 0, one that
+ *   holds nothing above the lowest number does not.
  *   The text of request r is history[rows[r]] (rows NULL: r; [num_rows], ld_history
  *   apart, history_width entries) up to history_lens[row], its prompt up to
  *   prompt_lens[row] (NULL: none).  tokens, parents: the nodes as in spec_verify

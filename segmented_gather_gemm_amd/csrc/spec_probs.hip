@@ -40,11 +40,16 @@ template <int kRotate>
 __device__ __forceinline__ float turned(float x) {
   return __int_as_float(rotated<kRotate>(__float_as_int(x)));
 }
-// What counts as nothing: NaN, -inf, and what the grammar does not allow.  Infinities are
-// the largest numbers from here on, so that differences are never NaN.
-constexpr float kNothing = -FLT_MAX;
-__device__ __forceinline__ float finite(float x) {  // (of NaN, the smallest of the three)
-  return __builtin_amdgcn_fmed3f(x, kNothing, FLT_MAX);
+// What counts as nothing: NaN, -inf, and what the grammar does not allow.  The lowest number
+// is one (a row may hold nothing else), so nothing stays -inf: its differences to a number
+// are -inf, and where there is only nothing, NaN, which the kernel drops.  +inf becomes the
+// largest number.
+constexpr float kNothing = -INFINITY;
+// (nothing: kNothing in a register that the compiler knows nothing of.  The median's NaN is
+// the smallest of the three, but one of a constant -inf is compiled as a minimum, whose NaN
+// is the other.)
+__device__ __forceinline__ float finite(float x, float nothing) {
+  return __builtin_amdgcn_fmed3f(x, nothing, FLT_MAX);
 }
 
 // What the text says of a value: occurrences since the prompt, and a flag.
@@ -259,6 +264,8 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
   };
   auto token_of = [&](int i) { return node_of(s.token, p.tokens, i); };
   const bool greedy = !(heat > 0.0f);
+  float nothing = kNothing;
+  asm("" : "+s"(nothing));
   // (what is nothing stays so at any temperature, and a tiny one does not make NaN of 0)
   const float k = fminf(fmaxf(kLog2e / heat, 0x1p-100f), 0x1p127f);
 
@@ -379,7 +386,7 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = finite(x[i]);
+      for (int i = 0; i < 8; ++i) x[i] = finite(x[i], nothing);
       if (here < kProbsChunk) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -486,7 +493,7 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
       first = min(first, rotated<1>(first));
       if (j < count && lane % 16 == 0) {
         const int64_t at = static_cast<int64_t>(q0 + i0 + j) * p.chunks + chunk;
-        p.stats[at] = make_float2(top, sum);
+        p.stats[at] = make_float2(top, top == kNothing ? 0.0f : sum);
         p.first[at] = first;
       }
     }
