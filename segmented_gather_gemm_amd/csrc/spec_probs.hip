@@ -58,7 +58,7 @@ constexpr uint32_t kInPrompt = 1u << 31, kCount = kInPrompt - 1;
 struct ProbsShared {
   uint32_t word[kProbsChunk];
   float shift[kProbsChunk];          // what is added to a value's logit
-  uint32_t path[kProbsChunk];        // occurrences on a long path; zero between its uses
+  uint32_t path[kProbsChunk];        // occurrences on a long path; before that, turns of biases
   int parent[kProbsTree], token[kProbsTree];
   int entries[kProbsNodes];          // of `entry`, or more than there is room for
   int entry[kProbsNodes][kProbsEntries];       // places in the chunk of the node's path
@@ -264,6 +264,7 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
   };
   auto token_of = [&](int i) { return node_of(s.token, p.tokens, i); };
   const bool greedy = !(heat > 0.0f);
+  int counted = -1;  // the node whose path s.path holds
   float nothing = kNothing;
   asm("" : "+s"(nothing));
   // (what is nothing stays so at any temperature, and a tiny one does not make NaN of 0)
@@ -356,24 +357,47 @@ __global__ __launch_bounds__(kProbsThreads, 4) void probs_kernel(ProbsParams p) 
           for (int i = 0; times != 0; ++i, times >>= 8)
             if (const uint32_t more = times & 255) redo(i, more);
         } else {
-          __syncthreads();  // the last long path's counts have been cleared
+          // A node that follows the last long path's end adds itself to that path's counts;
+          // else they are made anew.  (A chain of 4096 nodes of one chunk, given by its parents:
+          // 2.7 ms, 69 with one thread walking each path; two branches in turn: 5.4, 35.)
+          const int node = i0 + j;
+          const bool next = counted >= 0 && parent_of(node) == counted;
+          __syncthreads();  // the last long path's counts have been read
+          if (!next && p.parents) {
+            for (int e = tid; e < kProbsChunk; e += kProbsThreads) s.path[e] = 0;
+            __syncthreads();
+          }
           if (!p.parents) {
-            for (int i = tid; i <= i0 + j; i += kProbsThreads) {
+            for (int i = counted + 1 + tid; i <= node; i += kProbsThreads) {
               const int at = place(token_of(i));
               if (at >= 0) atomicAdd(&s.path[at], 1u);
             }
-          } else if (tid == 0) {
-            for (int i = i0 + j; i >= 0; i = parent_of(i)) {
-              const int at = place(token_of(i));
-              if (at >= 0) ++s.path[at];
+          } else if (next) {
+            const int at = place(token_of(node));
+            if (tid == 0 && at >= 0) ++s.path[at];
+          } else if (wave == 0) {
+            // 64 nodes at a time, and the way up among them through registers
+            for (int up = node; up >= 0;) {
+              const int base = up & -kWave, i = base + lane;
+              int before = -1, at = -1;
+              if (i <= node) {
+                before = parent_of(i);
+                at = place(token_of(i));
+              }
+              uint64_t on = 0;
+              do {
+                on |= 1ull << (up - base);
+                up = __builtin_amdgcn_readlane(before, up - base);
+              } while (up >= base);
+              if (at >= 0 && (on >> lane & 1)) atomicAdd(&s.path[at], 1u);
             }
           }
+          counted = node;
           __syncthreads();
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const int at = 4 * (tid + i / 4 * kProbsThreads) + i % 4;
             if (const uint32_t more = s.path[at]) redo(i, more);
-            s.path[at] = 0;
           }
         }
       }
