@@ -115,6 +115,11 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
   __shared__ float alpha[kBufs][D::kRows];
   __shared__ float2 stats[D::kRows];
   __shared__ __align__(16) int moved[kBufs][NG][4];
+  // latent_shape counts on two workgroups of one group of waves on a CU
+  static_assert(D::kTwo || sizeof(lds) + sizeof(weights) + sizeof(pages) + sizeof(find) +
+                                   sizeof(alpha) + sizeof(stats) + sizeof(moved) <=
+                               80 * 1024,
+                "too much LDS for a second workgroup");
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   const int l16 = lane % 16, g = lane / 16;
@@ -715,9 +720,12 @@ hipError_t launch_latent(const LatentParams& p, const LatentShape& s, hipStream_
   if (s.padded_dim == dl && s.block_rows == 16 * (m) * (groups)) \
     return launch_latent_as<kFp16, kE4M3, dl, m, groups, n, ahead>(p, s, stream)
   constexpr int two = kE4M3 ? 2 : 3;  // stages of a ring beside two tiles in use
-  SGG_LATENT(256, 1, 1, 4, 3);
-  SGG_LATENT(256, 2, 1, 4, 3);
-  SGG_LATENT(256, 4, 1, 4, 3);
+  // as many as leave room for a second workgroup (128 requests of 16 rows and some 4500
+  // latents of 256 columns, bf16: 90 us; 117 with four and one workgroup)
+  constexpr int one = kE4M3 ? 4 : 3;
+  SGG_LATENT(256, 1, 1, one, 3);
+  SGG_LATENT(256, 2, 1, one, 3);
+  SGG_LATENT(256, 4, 1, one, 3);
   SGG_LATENT(256, 4, 2, two, 3);
   SGG_LATENT(512, 1, 1, 2, 3);
   SGG_LATENT(512, 2, 1, 2, 3);
