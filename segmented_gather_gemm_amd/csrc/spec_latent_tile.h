@@ -26,6 +26,11 @@
 // and the exponentials share the rest, and 4.9 TB/s come through the second-level
 // caches, whose hits alone would save 40 us.  Deeper rings and more fragments under
 // way change nothing.
+//
+// Blocks of 64 and 128 rows of up to 512 columns hold 72 registers of queries and 128 of
+// sums, and some 45 others spill: constants of a unit, and what moves of the softmax's
+// reference and tiles that not every row sees need.  On the way of the other tiles nothing
+// is reloaded (see kTight).
 #pragma once
 
 #include "spec_attention_tile.h"
@@ -52,6 +57,11 @@ struct LatentDims {
   // Two groups fill the CU: scores and values of neighbouring tiles in one turn.
   static constexpr bool kTwo = NG == 2;
   static constexpr int kRing = NST * kStage + (kE4M3 ? (kTwo ? 2 : 1) * kTile : 0);
+  // Two addresses are made anew every tile.  Kept, they spill, and their reload waits for the
+  // loads of the next tile, which are counted with it (128 requests of 64 rows and some 4500
+  // latents, 8-bit: 163 us, 182 with these and a lane number reloaded).  In blocks of 128 rows
+  // none is reloaded in a tile that all rows see, and this would cost 3 %.
+  static constexpr bool kTight = kE4M3 && DL == 512 && MB == 4 && NG == 1;
   static constexpr int kKS = DL / 32;                 // steps of 32 columns, then 2 of the rope's
   static constexpr int kCols = DL / 16 / 4;           // 16-column tiles of a wave's values
   static constexpr int kSlotBytes = kRows * (DL * 4 + 8);
@@ -135,6 +145,19 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
   const int vr = 4 * g + (l16 >> 2), v0 = 2 * w4 * D::kCols;
   const int va = vr * D::kRow + (v0 / 16 << 8) +
                  (((v0 % 16 + (l16 >> 1 & 1)) ^ latent_swizzle(vr)) << 4) + 8 * (l16 & 1);
+  // ka and va once more, for an instance that has no registers to keep them in
+  auto ka_again = [] {
+    int l = threadIdx.x;
+    hide(l);
+    return l % 16 * D::kRow + ((l % kWave / 16 ^ latent_swizzle(l)) << 4);
+  };
+  auto va_again = [w4] {
+    int l = threadIdx.x;
+    hide(l);
+    const int vr = l % kWave / 4, v0 = 2 * w4 * D::kCols;
+    return vr * D::kRow + (v0 / 16 << 8) +
+           (((v0 % 16 + (l >> 1 & 1)) ^ latent_swizzle(vr)) << 4) + 8 * (l & 1);
+  };
   const int pieces = latent * (kE4M3 ? 1 : 2) / 16, rope_pieces = lp.rope * (kE4M3 ? 1 : 2) / 16;
   constexpr int kRopePieces = (kE4M3 ? D::kRawRope : D::kRopeRow) / 16;
 
@@ -223,8 +246,14 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
           (ll % kRopePieces) ^ (kE4M3 ? 0 : rope_swizzle(wave * D::kMine + sub));
       uint64_t at = at8;
       if constexpr (kE4M3) {
-        const uint32_t l = __shfl(lo, 8 * (sub & 7)), h = __shfl(hi, 8 * (sub & 7));
-        at = static_cast<uint64_t>(h) << 32 | l;
+        if constexpr (D::kTight) {  // (__shfl would keep the lane's number)
+          const uint32_t l = __builtin_amdgcn_ds_bpermute(32 * (sub & 7), lo);
+          const uint32_t h = __builtin_amdgcn_ds_bpermute(32 * (sub & 7), hi);
+          at = static_cast<uint64_t>(h) << 32 | l;
+        } else {
+          const uint32_t l = __shfl(lo, 8 * (sub & 7)), h = __shfl(hi, 8 * (sub & 7));
+          at = static_cast<uint64_t>(h) << 32 | l;
+        }
       }
       at += (kE4M3 ? latent : 2 * latent) + 16 * piece;
       char* to = base + D::kKeys * (D::kPieces * 16) + wave * D::kMine * (kRopePieces * 16);
@@ -316,7 +345,7 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
     // The weights of a tile, into buffer buf.
     auto take_scores = [&](int tile, const char* base, int buf) {
       const int key0 = tile * D::kKeys;
-      int kx = ka, rx = kr;
+      int kx = D::kTight ? ka_again() : ka, rx = kr;
       hide(kx);
       hide(rx);
       if (scores) {
@@ -394,7 +423,7 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
     };
     // O^T += V^T P^T
     auto take_values = [&](const char* base, int buf) {
-      int vx = va;
+      int vx = D::kTight ? va_again() : va;
       hide(vx);
       u32x4_t vf[kAheadV + 1];
       auto value = [&](int j) {

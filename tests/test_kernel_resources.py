@@ -74,3 +74,12 @@ def test_two_workgroups_of_up_to_64_rows_on_a_cu(e4m3, columns):
             assert -(-k[".group_segment_fixed_size"] // 1280) * 1280 <= LDS // 2, key
             assert -(-k[".vgpr_count"] // 8) * 8 <= REGISTERS // 2, key
     assert seen == 6
+
+
+def test_spilled_registers_of_the_latent_kernels():
+    """Only blocks of 64 and 128 rows of up to 512 columns spill, and no more than the constants of
+    a unit and of tiles that not every row sees: what is reloaded on the way of every tile waits for
+    the loads of the next."""
+    for (fp16, e4m3, columns, rows, groups, stages), k in latent_kernels().items():
+        allowed = 46 if (columns, rows) == (512, 4) else 0
+        assert k[".vgpr_spill_count"] <= allowed, (fp16, e4m3, columns, rows, groups, k)
