@@ -259,21 +259,22 @@ namespace sgg {
 
 // Row blocks of the smallest size that holds one request's rows, up to 128: rows that
 // nobody has cost matrix work, and a block fewer saves a read of all latents.  (128
-// requests of 16 rows and some 4500 latents: 149 us, 198 in blocks of 64.  The 128 rows
-// of each of two requests with 100003: 111 us, 117 in two blocks of 64.  32 requests of
-// 768 rows: 236 us, 244.)  Two workgroups of up to 64 rows share a CU's LDS and
-// registers, one of 128 takes it whole.  A batch that is too small to give every CU a
-// range takes smaller blocks: more workgroups, and less of each in one after another (one
-// request of 128 rows and 500 latents: 16.8 us, 24.8 in one block; 16 of 64 and 600:
-// 29.5, 36.9; one of 128 and 8000, the dearest: 39.7, 36.3).
+// requests of 16 rows and some 4500 latents: 148 us, 193 in blocks of 64.  Of 128 rows:
+// 265 us, 313 in blocks of 64.  32 requests of 768 rows: 220, 223.  Where the larger block
+// loses: the 128 rows of each of two requests with 100003 8-bit latents 107, 105; causal
+// chunks of 512 tokens of 16 heads 527, 494.)  Two workgroups of up to 64 rows share a
+// CU's LDS and registers, one of 128 takes it whole.  A batch that is too small to give
+// every CU a range takes smaller blocks: more workgroups, and less of each in one after
+// another (one request of 128 rows and 500 latents: 16.5 us, 24.6 in one block; 16 of 64
+// and 600: 28.9, 35.8; one of 128 and 8000, the dearest: 39.6, 36.6).
 //
 // The tiles of all units, a request's row blocks, are one line that is cut into as many
 // ranges as workgroups are on the GPU at once; a small block's ranges may be single tiles
-// (one request's 500 latents: 14.1 us, 14.9 at two tiles and more), larger blocks' at
+// (one request's 500 latents: 14.4 us, 15.7 at two tiles and more), larger blocks' at
 // least rows / 32 tiles, for a piece costs the write and the read of 2 KB a row.  Units so many
 // that they fill the GPU by themselves take a workgroup each and nothing is joined.
 // Where units are few and pieces many the join takes smaller items (two requests of 256
-// pieces: 111 us, 120; one of 16: 14.6, 16.0).
+// pieces: 108 us, 116; one of 16: 14.4, 15.6).
 LatentShape latent_shape(int32_t bs, int32_t heads, int32_t latent, int32_t max_q_len,
                          int64_t max_kv_len) {
   LatentShape s{};

@@ -20,12 +20,13 @@
 // values of one tile and the scores of the next in one turn: half the barriers, and
 // a SIMD's two waves need not be at the same of the two.
 //
-// What bounds it, with bf16: 16 rows (128 requests of some 4500 latents: 147 us) the
+// What bounds it, with bf16: 16 rows (128 requests of some 4500 latents: 148 us) the
 // read, at 4.5 TB/s; 768 rows a request (32 of some 2600: 219 us, 630 TFLOP/s) nothing
-// alone: matrix instructions take half of the time, the reads of fragments from LDS
-// and the exponentials share the rest, and 4.9 TB/s come through the second-level
-// caches, whose hits alone would save 40 us.  Deeper rings and more fragments under
-// way change nothing.
+// alone: by the counters the matrix unit is busy for 34 % of the time and the vector unit
+// with others for 20 %, the fragments read from LDS, at 128 bytes a cycle, fill 48 %, and
+// of the latents, which come once for each row block, 85 % miss the second-level caches
+// (from the first caches, one page in every place of the table: 167 us).  Deeper rings
+// and more fragments under way change nothing.
 //
 // Blocks of 64 and 128 rows of up to 512 columns hold 72 registers of queries and 128 of
 // sums, and some 45 others spill: constants of a unit, and what moves of the softmax's
@@ -85,7 +86,7 @@ __device__ __forceinline__ int rope_swizzle(int r) { return r & 6; }
 
 // The ranges of positions of a batch (see AttnWork).  Units too short to be worth two
 // ranges are taken one by one: ranges of min_tiles would hold several of them (123
-// requests of 192 rows and a tile: 78 us in ranges).
+// requests of 192 rows and a tile, in a launch for 128 tiles: 32 us, 73 in ranges).
 template <int NW, int R, int K>
 struct LatentPlan {
   AttnWork<NW, R, K> work;
@@ -400,6 +401,8 @@ __global__ __launch_bounds__(256 * NG, 2) void latent_kernel(LatentParams lp) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             st[t][i] = __builtin_amdgcn_exp2f(fmaf(st[t][i], scale, -ref));
+        // (rounded for the product as in the attention over pages, see kPSlack: 2.0e-3 of the
+        // norm from 64 bits in bf16, where one rounding at the end gives 1.7e-3)
         const u32x4_t pf = {pack16<kFp16>(st[0][0], st[0][1]), pack16<kFp16>(st[0][2], st[0][3]),
                             pack16<kFp16>(st[1][0], st[1][1]), pack16<kFp16>(st[1][2], st[1][3])};
         // the row's sum, of the weights as they are rounded: a product with ones

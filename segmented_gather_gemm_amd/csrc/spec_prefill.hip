@@ -9,9 +9,10 @@
 // as they stand, the second operand of O^T = V^T P^T.
 //
 // What bounds it: 4 requests of 1024 tokens behind up to 3000 others, 32 heads of
-// 128 + 64 and 128 columns, 750 TFLOP/s.  Matrix instructions take 41 % of the time,
-// the vector unit's others 31 %, LDS reads 20 %; a wave does these in turn, and the
-// two waves of a SIMD, all that its registers hold, overlap them in part.  Tiles of 64
+// 128 + 64 and 128 columns, 270 us, and 252 once the GPU has run for 60 ms: 730 - 785
+// TFLOP/s.  Matrix instructions take 42 % of the time, the vector unit's others 31 %, LDS
+// reads 20 %; a wave does these in turn, and the two waves of a SIMD, all that its
+// registers hold, overlap them in part.  Tiles of 64
 // keys (half the barriers) and 64 rows a wave (half the reads) want more registers
 // than there are and are slower.  The softmax has the higher priority: what waits for
 // it is the next matrix work (305 us without).
@@ -221,6 +222,8 @@ __global__ __launch_bounds__(kPrefillThreads, 2) void prefill_kernel(PrefillPara
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             st[m][t][i] = __builtin_amdgcn_exp2f(fmaf(st[m][t][i], scale, -ref));
+        // (rounded for the product as in the attention over pages, see kPSlack: 2.2e-3 of the
+        // norm from 64 bits in bf16, where one rounding at the end gives 1.7e-3)
         pf[m] = u32x4_t{pack16<kFp16>(st[m][0][0], st[m][0][1]),
                         pack16<kFp16>(st[m][0][2], st[m][0][3]),
                         pack16<kFp16>(st[m][1][0], st[m][1][1]),
@@ -305,7 +308,7 @@ hipError_t launch_prefill(PrefillParams p, bool fp16, int32_t max_q_len, hipStre
   const int64_t pairs = static_cast<int64_t>(p.bs) * p.heads;
   const int64_t rounds = (pairs + kXcds - 1) / kXcds;
   // 128 rows a workgroup once that fills the GPU (4 requests' 1024 tokens of 32 heads:
-  // 290 us, 395 with 64; 100 tokens of 16 heads: 10 us, 15 with 128)
+  // 270 us, 364 with 64; 100 tokens of 16 heads: 9.7 us, 14.3 with 128)
   const int mf = rounds * kXcds * ((max_q_len + 127) / 128) >= 512 ? 2 : 1;
   p.blocks = (max_q_len + 64 * mf - 1) / (64 * mf);
   if (p.blocks < 1) p.blocks = 1;

@@ -8,12 +8,16 @@
 // in a list by node.  Two launches: the maximum and the sum of every chunk, then
 // the probabilities, which take the chunks' together.
 //
-// 64 requests of 16 nodes, 128256 bf16 values each, 4000 tokens of text: 109 us for the
-// first launch, whose vector units are busy for 70 % of the time (some 15 instructions
-// a value), and 167 us for the second, which reads 263 MB and writes 525 MB at
-// 4.7 TB/s, what a large copy reaches.  What the text says of a thread's 8 values stays
-// in registers for all nodes (from LDS: 118 us), which four workgroups a CU just allow;
-// with three the second launch takes 198 us.
+// 64 requests of 16 nodes, 128256 bf16 values each, 4000 tokens of text: 104 us for the
+// first launch, whose vector units are busy for 76 % of the time (some 15 instructions
+// a value), and 162 us for the second, which reads 263 MB and writes 525 MB at
+// 4.8 TB/s, what a large copy reaches.  What the text says of a thread's 8 values stays
+// in registers for all nodes (from LDS the first launch took 9 us more), which four
+// workgroups a CU just allow (with three the second took 31 more); float32 logits spill a
+// few in the second launch, on the way of long paths alone.
+//
+// Every chunk walks the whole text, in both launches: 64 requests of one node and 128256
+// values take 297 us with up to 100000 tokens of text, 51 with 100.
 #include <cfloat>
 
 #include "spec_pages.h"
@@ -537,8 +541,7 @@ hipError_t launch_probs(ProbsParams p, int dtype, void* workspace, hipStream_t s
   p.stats = static_cast<float2*>(workspace);
   p.first = reinterpret_cast<int32_t*>(p.stats + static_cast<int64_t>(p.num_tokens) * p.chunks);
   // Nodes of a workgroup share its counts of the text; a small batch has a workgroup for
-  // each node rather (one user's 5 nodes of 32000 values:
-  // 18 us when this was chosen, 37 with 16 a workgroup).
+  // each node rather (one user's 5 nodes of 32000 values: 15.7 us, 27 with 16 a workgroup).
   p.nodes = kProbsNodes;
   const int64_t all = static_cast<int64_t>(p.chunks) * p.num_tokens;
   while (p.nodes > 1 && all / p.nodes < 1024) p.nodes /= 2;

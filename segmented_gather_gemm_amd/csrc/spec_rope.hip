@@ -11,8 +11,10 @@
 // them once for all heads of its tokens.
 //
 // What bounds it: a prompt's rows are read and written once, HBM (8192 tokens of
-// 32 + 2 * 8 heads of 128 columns: 43 us at 4 TB/s); a step of a few tokens is the
-// chain request, row, length, page before the first write (5 us).
+// 32 + 2 * 8 heads of 128 columns: 42 us at 4.2 TB/s); a step of a few tokens is the
+// chain request, row, length, page before the first write (5 us).  Halves apart that are
+// not multiples of 8 columns go pair by pair in accesses of 2 bytes (8192 tokens of heads
+// of 96: 104 us with 24 rotated columns, 35 with 32).
 #include "spec_pages.h"
 #include "spec_rope.h"
 
@@ -259,7 +261,7 @@ __global__ __launch_bounds__(kGatherThreads) void gather_kernel(GatherParams p) 
 hipError_t launch_rope(RopeParams p, bool fp16, bool to_e4m3, hipStream_t stream) {
   p.group = 1;
   // several tokens a workgroup once that leaves every CU some: they share the search for
-  // the request and the angles' division (8192 tokens of 40 heads: 43 us, 50 at one)
+  // the request and the angles' division (8192 tokens of 40 heads: 42 us, 49 at one)
   while (p.group < kRopeTokens && p.num_tokens / (2 * p.group) >= 1024) p.group *= 2;
   const bool vec = p.start % 8 == 0 && p.rot % (p.interleaved ? 8 : 16) == 0;
   const dim3 grid((p.num_tokens + p.group - 1) / p.group), block(kRopeThreads);
